@@ -16,9 +16,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libccb.so")
-SOURCES = ["ccb_kernels.hip", "ccb_api.hip"]
-HEADERS = [os.path.join(ROOT, "include", "ccb.h"), os.path.join(ROOT, "include", "ccb_device.h"),
-           os.path.join(CSRC, "ccb_internal.h")]
+SOURCES = ["ccb_kernels.hip", "ccb_api.hip", "ccb_kv8_cache.hip", "ccb_kv8_attend.hip",
+           "ccb_kv8_api.hip"]
+HEADERS = [os.path.join(ROOT, "include", h) for h in ("ccb.h", "ccb_device.h", "ccb_kv8.h")] + \
+          [os.path.join(CSRC, h) for h in ("ccb_internal.h", "ccb_kv8_internal.h", "ccb_kv8_math.h",
+                                           "ccb_kv8_device.h")]
 
 
 # flags shared by every compile of the kernels (the library and its review)

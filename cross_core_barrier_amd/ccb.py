@@ -75,6 +75,26 @@ CCB_CNT_RECORD_SET_VALUE, CCB_CNT_RECORD_ADD, CCB_CNT_RECORD_BIT_OR, CCB_CNT_REC
  CCB_CNT_WAIT_EQUAL_WITH_BITMASK) = 0, 1, 2, 3, 4
 
 
+CCB_KV8_INT8, CCB_KV8_E4M3 = 0, 1
+CCB_KV8_BF16, CCB_KV8_FP16, CCB_KV8_FP32 = 0, 1, 2
+
+
+class ccbKv8Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kScale", ctypes.c_void_p),
+                ("vScale", ctypes.c_void_p), ("pageTable", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("tableStride", ctypes.c_int64),
+                ("weightStride", ctypes.c_int64), ("format", ctypes.c_int32),
+                ("numPages", ctypes.c_int32), ("heads", ctypes.c_int32), ("pageSize", ctypes.c_int32),
+                ("headDim", ctypes.c_int32), ("batch", ctypes.c_int32), ("maxPages", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ccbKv8Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("strideBatch", ctypes.c_int64),
+                ("strideToken", ctypes.c_int64), ("strideHead", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class ccbCntRecordInfo(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("value", ctypes.c_uint32)]
 
@@ -96,6 +116,7 @@ def check(status: int, what: str = "ccb call") -> None:
 
 
 _V = ctypes.c_void_p
+_SZ, _F32 = ctypes.c_size_t, ctypes.c_float
 _I32, _U32, _I64, _U64 = ctypes.c_int32, ctypes.c_uint32, ctypes.c_int64, ctypes.c_uint64
 
 
@@ -148,6 +169,14 @@ _f = {
     "ccb_cnt_notify_query": _sig("ccb_cnt_notify_query", _I32, _V, _V, _V, _V),
     "ccb_cnt_notify_batch": _sig("ccb_cnt_notify_batch", _I32, _V, _V, _I64, _I32, _V, _V, _I32, _V,
                                  _V),
+    "ccb_kv8_append": _sig("ccb_kv8_append", _I32, _V, _V, _V, _I32, _V, _V, _V),
+    "ccb_kv8_attend": _sig("ccb_kv8_attend", _I32, _V, _V, _V, _V, _I32, _I32, _F32, _I32, _I32, _V,
+                           _SZ, _V, _V),
+    "ccb_kv8_attend_workspace_bytes": _sig("ccb_kv8_attend_workspace_bytes", _SZ, _V, _I32, _I32,
+                                           _I32),
+    "ccb_kv8_evict": _sig("ccb_kv8_evict", _I32, _V, _V, _I32, _I32, _I32, _V, _V, _SZ, _V, _V),
+    "ccb_kv8_evict_workspace_bytes": _sig("ccb_kv8_evict_workspace_bytes", _SZ, _V, _I32),
+    "ccb_kv8_read": _sig("ccb_kv8_read", _I32, _V, _V, _V, _I32, _V, _V, _V),
 }
 
 EXPORTED = sorted(_f)
@@ -345,3 +374,37 @@ def wait_info(mode: int, value: int, timeout: int = 0, is_clear: int = 0, rev=(0
     for i in range(3):
         w.rev[i] = rev[i]
     return w
+
+
+# --- 8-bit key/value cache ------------------------------------------------------------
+# cache arguments are ccbKv8Cache structures, rows ccbKv8Rows structures (or None)
+
+def _r(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def ccb_kv8_append(cache, k_new, v_new, n_new, counts=None, err=None, stream=None) -> int:
+    return _f["ccb_kv8_append"](_r(cache), _r(k_new), _r(v_new), n_new, _p(counts), _p(err), _s(stream))
+
+
+def ccb_kv8_attend(cache, q, out, lse, heads_q, n_query, scale, window, accumulate, ws, ws_bytes,
+                   err=None, stream=None) -> int:
+    return _f["ccb_kv8_attend"](_r(cache), _r(q), _r(out), _p(lse), heads_q, n_query, scale, window,
+                                accumulate, _p(ws), ws_bytes, _p(err), _s(stream))
+
+
+def ccb_kv8_attend_workspace_bytes(cache, heads_q: int, n_query: int, accumulate: int) -> int:
+    return int(_f["ccb_kv8_attend_workspace_bytes"](_r(cache), heads_q, n_query, accumulate))
+
+
+def ccb_kv8_evict(src, dst, budget, recent, sinks, kept, ws, ws_bytes, err=None, stream=None) -> int:
+    return _f["ccb_kv8_evict"](_r(src), _r(dst), budget, recent, sinks, _p(kept), _p(ws), ws_bytes,
+                               _p(err), _s(stream))
+
+
+def ccb_kv8_evict_workspace_bytes(src, budget: int) -> int:
+    return int(_f["ccb_kv8_evict_workspace_bytes"](_r(src), budget))
+
+
+def ccb_kv8_read(cache, k_out, v_out, count, first=None, err=None, stream=None) -> int:
+    return _f["ccb_kv8_read"](_r(cache), _r(k_out), _r(v_out), count, _p(first), _p(err), _s(stream))

@@ -82,6 +82,18 @@ ccbStatus current_device(int* devOut, DeviceInfo* infoOut)
     return CCB_OK;
 }
 
+}  // namespace
+
+ccbStatus ccb::device_ready(int* numCUs)
+{
+    DeviceInfo info;
+    const ccbStatus st = current_device(nullptr, &info);
+    if (st == CCB_OK) *numCUs = info.numCUs;
+    return st;
+}
+
+namespace {
+
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 

@@ -1,0 +1,38 @@
+// ccb_kv8_internal.h -- private interface between the C entry points of the 8-bit
+// key/value cache (ccb_kv8_api.hip) and its kernels.  Not installed.
+#ifndef CCB_KV8_INTERNAL_H
+#define CCB_KV8_INTERNAL_H
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ccb_kv8.h"
+
+namespace ccb {
+
+struct Kv8AttendArgs {
+    ccbKv8Cache c;
+    ccbKv8Rows q, out;
+    float* lse;
+    int32_t headsQ, nQuery, window, accumulate;
+    float scale;
+    void* ws;
+    int32_t* err;
+};
+
+size_t kv8_attend_bytes(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, int32_t accumulate);
+hipError_t kv8_attend(const Kv8AttendArgs& a, int numCUs, hipStream_t s);
+
+size_t kv8_evict_bytes(const ccbKv8Cache& from, int32_t budget);
+hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t budget, int32_t recent,
+                     int32_t sinks, int32_t* kept, void* ws, int32_t* err, int numCUs, hipStream_t s);
+
+hipError_t kv8_append(const ccbKv8Cache& c, const ccbKv8Rows& k, const ccbKv8Rows& v, int32_t nNew,
+                      const int32_t* counts, int32_t* err, hipStream_t s);
+
+hipError_t kv8_read(const ccbKv8Cache& c, const ccbKv8Rows* k, const ccbKv8Rows* v, int32_t count,
+                    const int32_t* first, int32_t* err, hipStream_t s);
+
+}  // namespace ccb
+
+#endif  // CCB_KV8_INTERNAL_H

@@ -1,0 +1,207 @@
+"""The 8-bit key/value cache over torch tensors: one class around the
+ccb_kv8_* calls of include/ccb_kv8.h.  PyTorch provides memory and streams
+only; every step runs in libccb.so's HIP kernels.
+
+    cache = Kv8Cache.allocate(pages=4096, heads=8, page_size=64, head_dim=128,
+                              batch=16, max_pages=256, fmt="e4m3", weights=True)
+    cache.page_table[...] = ...                # pages from the caller's allocator
+    cache.lens += 1                            # one token more for every sequence
+    cache.append(k_new, v_new)                 # [batch, 1, heads, head_dim]
+    out, lse = cache.attend(q, accumulate=True)  # q [batch, 1, q_heads, head_dim]
+    kept = cache.evict(smaller, budget=1024, recent=128, sinks=4)
+
+Calls run on torch's current stream, or on `stream` (a torch.cuda.Stream or a
+raw hipStream_t) after the work already queued on the current stream, which
+is then ordered after them.  They copy nothing to the host.  Bad page numbers,
+lengths and counts are met on the device: they set `cache.err`, which
+`cache.check()` reads (and waits for).
+"""
+
+from __future__ import annotations
+
+import math
+from typing import Optional
+
+import torch
+
+from . import ccb
+from .workloads import _enter, _leave
+
+_CODES = {torch.int8: ccb.CCB_KV8_INT8, torch.float8_e4m3fn: ccb.CCB_KV8_E4M3}
+_FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+_ROWS = {torch.bfloat16: ccb.CCB_KV8_BF16, torch.float16: ccb.CCB_KV8_FP16, torch.float32: ccb.CCB_KV8_FP32}
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+class Kv8Cache:
+    """A cache in the caller's tensors (they are kept, not copied):
+    k, v [pages, heads, page_size, head_dim] (int8 or float8_e4m3fn); k_scale,
+    v_scale [pages, heads] float32; page_table [batch, max_pages] int32; lens
+    [batch] int32; weight [batch, heads, at least max_pages * page_size]
+    float32 or None.  All contiguous, but for the page table's rows."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table, lens, weight=None):
+        _need(k.dim() == 4 and k.dtype in _CODES, "k: [pages, heads, page_size, head_dim], int8 or float8_e4m3fn")
+        pages, heads, page_size, head_dim = k.shape
+        _need(v.shape == k.shape and v.dtype == k.dtype, "v: shape and dtype of k")
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _need(tuple(s.shape) == (pages, heads) and s.dtype == torch.float32, f"{name}: [pages, heads] float32")
+        _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and page_table.shape[1] >= 1 and
+              page_table.stride(1) == 1, "page_table: [batch, max_pages] int32")
+        batch, max_pages = page_table.shape
+        _need(tuple(lens.shape) == (batch,) and lens.dtype == torch.int32, "lens: [batch] int32")
+        if weight is not None:
+            _need(weight.dim() == 3 and tuple(weight.shape[:2]) == (batch, heads) and weight.dtype == torch.float32
+                  and weight.shape[2] >= max_pages * page_size,
+                  "weight: [batch, heads, max_pages * page_size or more] float32")
+        for t in (k, v, k_scale, v_scale, lens) + (() if weight is None else (weight,)):
+            _need(t.is_contiguous(), "cache tensors are contiguous")
+        for t in (v, k_scale, v_scale, page_table, lens) + (() if weight is None else (weight,)):
+            _need(t.device == k.device, "cache tensors share a device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table, self.lens, self.weight = page_table, lens, weight
+        self.heads, self.head_dim, self.batch, self.device = heads, head_dim, batch, k.device
+        self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._c = ccb.ccbKv8Cache(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+            lens.data_ptr(), 0 if weight is None else weight.data_ptr(),
+            page_table.stride(0) if batch > 1 else max_pages, 0 if weight is None else weight.shape[2],
+            _CODES[k.dtype], pages, heads, page_size, head_dim, batch, max_pages, 0)
+
+    @classmethod
+    def allocate(cls, pages: int, heads: int, page_size: int, head_dim: int, batch: int, max_pages: int,
+                 fmt: str = "e4m3", weights: bool = False, device="cuda") -> "Kv8Cache":
+        """Zeroed tensors: no sequence holds a token, every page number is 0."""
+        _need(fmt in _FORMATS, "fmt: int8 or e4m3")
+        shape = (pages, heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.int8, device=device).view(_FORMATS[fmt]) for _ in range(2))
+        ks, vs = (torch.zeros((pages, heads), dtype=torch.float32, device=device) for _ in range(2))
+        table = torch.zeros((batch, max_pages), dtype=torch.int32, device=device)
+        lens = torch.zeros(batch, dtype=torch.int32, device=device)
+        weight = torch.zeros((batch, heads, max_pages * page_size), dtype=torch.float32, device=device) \
+            if weights else None
+        return cls(k, v, ks, vs, table, lens, weight)
+
+    def _rows(self, t: torch.Tensor, heads: int, what: str):
+        _need(t.dim() == 4 and t.shape[0] == self.batch and t.shape[2] == heads and t.shape[3] == self.head_dim
+              and t.dtype in _ROWS and t.device == self.device and (t.stride(3) == 1 or t.numel() == 0),
+              f"{what}: [batch {self.batch}, tokens, heads {heads}, head_dim {self.head_dim}] on {self.device}, "
+              "bfloat16 or float16, the last dimension contiguous")
+        # the stride of a dimension with one place is never used
+        n, c, h, _ = t.shape
+        sb, st, sh, _ = t.stride()
+        return ccb.ccbKv8Rows(t.data_ptr(), sb if n > 1 else 0, st if c > 1 else 0, sh if h > 1 else 0,
+                              _ROWS[t.dtype], 0)
+
+    def _ints(self, t: Optional[torch.Tensor], shape: tuple, what: str):
+        _need(t is None or (tuple(t.shape) == shape and t.dtype == torch.int32 and t.is_contiguous()
+                            and t.device == self.device), f"{what}: {list(shape)} int32, contiguous")
+        return t
+
+    def _space(self, ws: Optional[torch.Tensor], need: int, s):
+        """The caller's workspace, or a new one for this call."""
+        if ws is None:
+            ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            if s is not None:
+                s.wait_stream(torch.cuda.current_stream(self.device))
+                ws.record_stream(s)
+        _need(ws.is_contiguous() and ws.device == self.device, "workspace: contiguous, on the cache's device")
+        return ws, ws.numel() * ws.element_size()
+
+    def _on(self, s):
+        return torch.cuda.current_stream(self.device) if s is None else s
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+        """Write each sequence's counts[b] (None: all) new tokens as its last
+        ones; lens counts them already.  k_new, v_new [batch, n, heads, head_dim]."""
+        k, v = self._rows(k_new, self.heads, "k_new"), self._rows(v_new, self.heads, "v_new")
+        _need(k_new.shape == v_new.shape and k_new.dtype == v_new.dtype, "v_new: shape and dtype of k_new")
+        self._ints(counts, (self.batch,), "counts")
+        s = _enter(stream, self.device)
+        ccb.check(ccb.ccb_kv8_append(self._c, k, v, k_new.shape[1], counts, self.err, self._on(s)), "ccb_kv8_append")
+        _leave(s, self.device)
+
+    def attend_workspace(self, q_heads: int, queries: int = 1, accumulate: bool = False) -> torch.Tensor:
+        """A workspace for attend() calls of these sizes that follow each other."""
+        n = ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
+        _need(n > 0, "attend: sizes that ccb_kv8_attend refuses")
+        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+    def attend(self, q: torch.Tensor, scale: Optional[float] = None, window: int = 0, accumulate: bool = False,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None):
+        """Attention of q [batch, queries, q_heads, head_dim], the sequences'
+        last tokens; scale None is 1 / sqrt(head_dim).  Returns (out, lse)."""
+        _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
+        queries, q_heads = q.shape[1], q.shape[2]
+        s = _enter(stream, self.device)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if s is not None:
+                out.record_stream(s)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+            if s is not None:
+                lse.record_stream(s)
+        _need(out.shape == q.shape and out.dtype == q.dtype, "out: shape and dtype of q")
+        _need(lse.shape == q.shape[:3] and lse.dtype == torch.float32 and lse.is_contiguous()
+              and lse.device == self.device, "lse: [batch, queries, q_heads] float32, contiguous")
+        qr, outr = self._rows(q, q_heads, "q"), self._rows(out, q_heads, "out")
+        need = 0 if workspace is not None else \
+            ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
+        ws, size = self._space(workspace, need, s)
+        ccb.check(ccb.ccb_kv8_attend(self._c, qr, outr, lse, q_heads, queries,
+                                     1.0 / math.sqrt(self.head_dim) if scale is None else scale, window,
+                                     int(accumulate), ws, size, self.err, self._on(s)), "ccb_kv8_attend")
+        _leave(s, self.device)
+        return out, lse
+
+    def evict_workspace(self, budget: int) -> torch.Tensor:
+        """A workspace for evict() calls with this budget that follow each other."""
+        n = ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
+        _need(n > 0, "evict: sizes that ccb_kv8_evict refuses")
+        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+    def evict(self, to: "Kv8Cache", budget: int, recent: int = 0, sinks: int = 0,
+              kept: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream=None) -> Optional[torch.Tensor]:
+        """Copy the budget tokens of each sequence and head with the largest
+        weight (and its first `sinks` and last `recent`) into the cache `to`.
+        kept [batch, heads, budget] int32 gets their numbers; it is returned."""
+        _need(to.device == self.device, "to: on the cache's device")
+        self._ints(kept, (self.batch, self.heads, budget), "kept")
+        s = _enter(stream, self.device)
+        need = 0 if workspace is not None else ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
+        ws, size = self._space(workspace, need, s)
+        ccb.check(ccb.ccb_kv8_evict(self._c, to._c, budget, recent, sinks, kept, ws, size, self.err, self._on(s)),
+                  "ccb_kv8_evict")
+        _leave(s, self.device)
+        return kept
+
+    def read(self, count: int, first: Optional[torch.Tensor] = None, dtype=torch.float32, stream=None):
+        """The values of `count` tokens of each sequence from first[b] (None: 0)
+        as (k, v) [batch, count, heads, head_dim]; zeros where there is none."""
+        _need(dtype in _ROWS, "dtype: float32, bfloat16 or float16")
+        self._ints(first, (self.batch,), "first")
+        shape = (self.batch, count, self.heads, self.head_dim)
+        s = _enter(stream, self.device)
+        k, v = (torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+        if s is not None:
+            k.record_stream(s)
+            v.record_stream(s)
+        ccb.check(ccb.ccb_kv8_read(self._c, self._rows(k, self.heads, "k"), self._rows(v, self.heads, "v"), count,
+                                   first, self.err, self._on(s)), "ccb_kv8_read")
+        _leave(s, self.device)
+        return k, v
+
+    def check(self) -> None:
+        """Raise if a call on this cache met a bad page number, length or
+        count since the last check.  Waits for the device."""
+        status = int(self.err.item())
+        self.err.zero_()
+        ccb.check(status, "8-bit cache")

@@ -1,0 +1,623 @@
+"""The 8-bit key/value cache on the GPU against the oracle in 64 bits
+(oracle/kv8.py).  Codes, scales, kept tokens and lengths are compared exactly;
+attention within bounds counted from its roundings (see _attend_case).  Unused
+pages, and slots past a sequence's end, hold NaN codes and NaN scales."""
+
+import math
+
+import numpy as np
+import pytest
+
+from oracle import kv8 as oracle
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+CODES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+
+def _say(msg):
+    print(f"[gpu case] {msg}", flush=True)
+
+
+@pytest.fixture(scope="module")
+def kv8():
+    from cross_core_barrier_amd import ccb, kv8 as module
+    st, _, _, _ = ccb.ccb_device_info()
+    assert st == 0, ccb.ccb_status_string(st)
+    return module
+
+
+def _host(rng, fmt, lens, heads, P, D, width=None, extra=3, quiet=1.0):
+    """A cache on the host: pages in random order, the bytes no token owns all
+    0x7F / 0x80 (NaN in e4m3, the out-of-range -128 in int8)."""
+    batch = len(lens)
+    width = width or max(1, -(-max(lens) // P)) + 1
+    pages = batch * width + extra
+    junk = 0x7F if fmt == "e4m3" else 0x80
+    c = dict(fmt=fmt, lens=np.array(lens, np.int32), table=rng.permutation(pages)[:batch * width].astype(np.int32)
+             .reshape(batch, width), weight=None)
+    for w in ("k", "v"):
+        c[w] = np.full((pages, heads, P, D), junk, np.uint8)
+        c[w + "s"] = np.full((pages, heads), np.nan, np.float32)
+    for b, n in enumerate(lens):
+        for number in range(-(-n // P)):
+            page = c["table"][b, number]
+            slots = min(P, n - number * P)
+            for w in ("k", "v"):
+                if fmt == "int8":
+                    x = np.clip(np.round(rng.normal(0, 40, (heads, slots, D))), -127, 127).astype(np.int8)
+                    c[w][page, :, :slots] = x.view(np.uint8)
+                else:
+                    x = rng.integers(0, 127, (heads, slots, D)) | (rng.integers(0, 2, (heads, slots, D)) << 7)
+                    c[w][page, :, :slots] = x
+                top = 40 if fmt == "int8" else 150
+                c[w + "s"][page] = (rng.uniform(0.2, 2, heads) / top * quiet).astype(np.float32)
+    return c
+
+
+def _device(kv8, c):
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    code = CODES[c["fmt"]]
+    return kv8.Kv8Cache(up(c["k"]).view(code), up(c["v"]).view(code), up(c["ks"]), up(c["vs"]), up(c["table"]),
+                        up(c["lens"]), None if c["weight"] is None else up(c["weight"]))
+
+
+def _codes(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def _spread_heads(x, spare):
+    """The same values with strides: a slice of a wider tensor."""
+    wide = torch.zeros((*x.shape[:2], x.shape[2] + spare, x.shape[3]), dtype=x.dtype, device=x.device)
+    wide[:, :, 1:1 + x.shape[2]] = x
+    return wide[:, :, 1:1 + x.shape[2]]
+
+
+def _bounds(D, tokens, seen_mag, big, lse):
+    """What fp32 attention over exact 8-bit products may be off by.
+    A score is a sum of D exact products in fp32, scaled by two more factors:
+    off by at most (D + 4) half steps of sum |q k| scale (`big`).  Its weight
+    is off, relatively, by that plus as much for the maximum it is compared
+    with, plus the exponential's own error (the argument's rounding, a few
+    half steps of the largest |s - m| <= 2 big, and 4 of its value); sums over
+    the tokens add `tokens` half steps at worst."""
+    u = 2.0 ** -24
+    ds = (D + 4) * u * big
+    rel = 2 * ds + (4 * big + 8 + 2 * tokens) * u
+    return rel, ds + rel + 4 * u * np.abs(np.where(np.isfinite(lse), lse, 0)), rel[..., None] * seen_mag
+
+
+def _attend_case(kv8, seed, fmt, dtype, lens, heads, group, D, P, queries=1, window=0, accumulate=True, scale=None,
+                 q_size=1.0, c=None, strided=False, skip=(), **kw):
+    rng = np.random.default_rng(seed)
+    c = c or _host(rng, fmt, lens, heads, P, D)
+    tokens = c["table"].shape[1] * P
+    base = rng.uniform(0, 1, (len(lens), heads, tokens)).astype(np.float32) * 1e-2
+    c["weight"] = base.copy()
+    cache = _device(kv8, c)
+    q = torch.from_numpy(rng.normal(0, q_size, (len(lens), queries, heads * group, D))).to(TYPES[dtype])
+    scale = 1 / math.sqrt(D) if scale is None else scale
+    want, lse, weight, mag, big = oracle.attend(c, q.double().numpy(), float(np.float32(scale)), window)
+    dq = q.cuda()
+    out = None
+    if strided:
+        dq = _spread_heads(dq, 3)
+        out = _spread_heads(torch.zeros_like(q, device="cuda"), 2)
+    got, got_lse = cache.attend(dq, scale=scale, window=window, accumulate=accumulate, out=out, **kw)
+    torch.cuda.synchronize()
+    rel, tol_lse, tol = _bounds(D, max(max(lens), 1), mag, big, lse)
+    eps = torch.finfo(TYPES[dtype]).eps / 2
+    tiny = 2.0 ** -25 if dtype == "fp16" else 0.0  # half a step of fp16's subnormals
+    y = got.double().cpu().numpy()
+    live = [b for b in range(len(lens)) if b not in skip]
+    assert np.all(np.abs(y - want)[live] <= (tol + eps * (np.abs(want) + tol) + tiny)[live])
+    z = got_lse.double().cpu().numpy()
+    empty = np.isinf(lse)
+    assert np.array_equal(np.isneginf(z)[live], empty[live])
+    assert np.all(y[empty] == 0)
+    diff = np.abs(np.where(empty, 0, z) - np.where(empty, 0, lse))
+    assert np.all(diff[live] <= tol_lse[live] + 1e-45)
+    w = cache.weight.double().cpu().numpy()
+    worst = rel.max() if rel.size else 0.0
+    if accumulate:
+        rows = queries * group
+        tol_w = weight * (worst + rows * 2.0 ** -24) + 2.0 ** -24 * (base + weight) + rows * 2.0 ** -120
+        assert np.all(np.abs(w - (base.astype(np.float64) + weight))[live] <= tol_w[live])
+    else:
+        assert np.array_equal(w, base.astype(np.float64))
+    return cache, dq, got, got_lse
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,P", [(64, 16), (64, 128), (96, 32), (96, 64), (128, 64), (128, 16), (192, 128), (192, 32),
+                                 (256, 64), (256, 128)])
+def test_attend_sizes(kv8, fmt, dtype, D, P):
+    """Lengths around the borders of pages and tiles, empty ones among them."""
+    lens = [0, 1, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 200, 257]
+    _say(f"attend {fmt} {dtype} D={D} P={P} lens={lens}")
+    _attend_case(kv8, D + P, fmt, dtype, lens, 2, 4, D, P)
+
+
+@pytest.mark.parametrize("heads,group,queries", [(1, 1, 1), (3, 1, 2), (2, 5, 1), (1, 16, 1), (2, 7, 3), (1, 17, 1),
+                                                 (1, 8, 4), (1, 32, 2), (1, 71, 1), (2, 4, 40), (1, 3, 100)])
+@pytest.mark.parametrize("window", [0, 1, 33])
+def test_attend_heads_queries_windows(kv8, heads, group, queries, window):
+    """Rows that see nothing (more queries than tokens), windows that begin
+    inside a tile, and more rows than one tile of queries holds."""
+    _say(f"attend heads={heads} group={group} queries={queries} window={window}")
+    fmt, dtype = ("int8", "bf16") if (heads + group) % 2 else ("e4m3", "fp16")
+    _attend_case(kv8, group, fmt, dtype, [0, 1, 2, 39, 150], heads, group, 64, 32, queries, window, strided=True)
+
+
+@pytest.mark.parametrize("fmt,group,D", [("int8", 4, 128), ("e4m3", 8, 64), ("int8", 1, 96), ("e4m3", 20, 128)])
+def test_attend_long_among_short(kv8, fmt, group, D):
+    """One long sequence that many workgroups share, short ones beside it."""
+    _say(f"attend long {fmt} group={group} D={D}")
+    _attend_case(kv8, 5, fmt, "fp16", [7, 9001, 0, 130, 2050], 2, group, D, 64)
+
+
+@pytest.mark.parametrize("queries,window", [(1, 700), (6, 1000), (3, 0)])
+def test_attend_long_windows(kv8, queries, window):
+    _say(f"attend long, queries={queries} window={window}")
+    _attend_case(kv8, 6, "int8", "bf16", [5003, 64, 1500], 2, 6, 96, 128, queries, window)
+
+
+def test_attend_many_sequences(kv8):
+    _say("attend 150 sequences, 3 heads")
+    lens = [(i * 37) % 211 for i in range(150)]
+    _attend_case(kv8, 7, "e4m3", "bf16", lens, 3, 2, 64, 16)
+
+
+@pytest.mark.parametrize("q_size,scale", [(30.0, None), (1.0, 0.0), (1e-3, -2.0), (1.0, 1e-30), (300.0, 1e-3)])
+def test_attend_score_ranges(kv8, q_size, scale):
+    """One token that takes everything, all tokens alike, a negative scale."""
+    _say(f"attend q_size={q_size} scale={scale}")
+    _attend_case(kv8, 8, "int8", "fp16", [100, 1, 65], 2, 3, 64, 32, scale=scale, q_size=q_size)
+
+
+@pytest.mark.parametrize("q_size", [1e-30, 1e30])
+def test_attend_bf16_range(kv8, q_size):
+    """Queries far outside fp16's range; the scale brings the scores back."""
+    _say(f"attend bf16 queries of size {q_size}")
+    _attend_case(kv8, 9, "e4m3", "bf16", [90, 300], 2, 4, 128, 64, scale=0.1 / q_size, q_size=q_size)
+
+
+def test_attend_quiet_and_loud_blocks(kv8):
+    """Scales of a sequence's blocks 2^-40 .. 2^20 apart, zero among them: a
+    block that is quiet beside its neighbours still counts where the loud ones
+    draw no weight."""
+    rng = np.random.default_rng(10)
+    c = _host(rng, "int8", [256, 130], 2, 16, 64)
+    for b in range(2):
+        for j in range(c["table"].shape[1]):
+            c["vs"][c["table"][b, j]] *= np.float32(2.0 ** rng.integers(-40, 20))
+    c["vs"][c["table"][0, 3]] = 0
+    c["ks"][c["table"][0, 4]] = 0
+    _say("attend with unlike block scales")
+    _attend_case(kv8, 10, "int8", "bf16", [256, 130], 2, 4, 64, 16, c=c)
+
+
+def test_attend_without_weight_and_lse_unasked(kv8):
+    from cross_core_barrier_amd import ccb
+    rng = np.random.default_rng(11)
+    c = _host(rng, "int8", [50, 3], 2, 16, 64)
+    cache = _device(kv8, c)
+    q = torch.from_numpy(rng.normal(0, 1, (2, 1, 4, 64))).to(torch.bfloat16).cuda()
+    _say("attend without weight, and without lse")
+    out, lse = cache.attend(q)
+    ws = cache.attend_workspace(4)
+    again = torch.empty_like(out)
+    st = ccb.ccb_kv8_attend(cache._c, cache._rows(q, 4, "q"), cache._rows(again, 4, "out"), None, 4, 1, 0.125, 0, 0,
+                            ws, ws.numel())
+    assert st == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)
+    with pytest.raises(ccb.CcbError):
+        cache.attend(q, accumulate=True)
+
+
+def test_attend_nan_and_infinite_queries_stay_in_their_rows(kv8):
+    rng = np.random.default_rng(12)
+    c = _host(rng, "int8", [70, 20], 2, 16, 64)
+    cache = _device(kv8, c)
+    q = torch.from_numpy(rng.normal(0, 1, (2, 2, 8, 64))).to(torch.bfloat16)
+    want, *_ = oracle.attend(c, q.double().numpy(), 0.125, 0)
+    q[0, 1, 2, 5] = math.nan
+    q[1, 0, 7, 0] = math.inf
+    _say("attend with NaN and infinity in two queries")
+    out, _ = cache.attend(q.cuda())
+    y = out.float().cpu().numpy()
+    assert np.isnan(y[0, 1, 2]).all() and np.isnan(y[1, 0, 7]).all()
+    good = np.ones(y.shape[:3], bool)
+    good[0, 1, 2] = good[1, 0, 7] = False
+    assert np.all(np.abs(y - want)[good] < 0.02 * np.abs(want[good]) + 0.02)
+
+
+def test_attend_same_bits_every_time(kv8):
+    _say("attend twice, with and without another call between")
+    rng = np.random.default_rng(13)
+    c = _host(rng, "e4m3", [4000, 17, 900], 4, 64, 128)
+    c["weight"] = np.zeros((3, 4, c["table"].shape[1] * 64), np.float32)
+    cache = _device(kv8, c)
+    q = torch.from_numpy(rng.normal(0, 1, (3, 1, 16, 128))).half().cuda()
+    ws = cache.attend_workspace(16, 1, True)
+    first = None
+    for _ in range(4):
+        cache.weight.zero_()
+        out, lse = cache.attend(q, accumulate=True, workspace=ws)
+        now = [t.clone() for t in (out, lse, cache.weight)]
+        torch.cuda.synchronize()
+        if first is not None:
+            assert all(torch.equal(a, b) for a, b in zip(first, now))
+        first = now
+
+
+def test_attend_workspace_serves_other_lengths(kv8):
+    """One workspace over calls with other lengths: nothing stays behind."""
+    rng = np.random.default_rng(14)
+    c = _host(rng, "int8", [900, 900, 900], 2, 32, 64)
+    c["weight"] = np.zeros((3, 2, c["table"].shape[1] * 32), np.float32)
+    cache = _device(kv8, c)
+    ws = cache.attend_workspace(6, 2, True)
+    for lens in ([900, 900, 900], [0, 0, 0], [1, 900, 33], [64, 2, 0], [0, 0, 850]):
+        _say(f"attend, one workspace, lens={lens}")
+        c["lens"][:] = lens
+        c["weight"][:] = 0
+        cache.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        cache.weight.zero_()
+        q = torch.from_numpy(rng.normal(0, 1, (3, 2, 6, 64))).half()
+        want, lse, weight, *_ = oracle.attend(c, q.double().numpy(), 0.125, 0)
+        out, got = cache.attend(q.cuda(), accumulate=True, workspace=ws)
+        assert np.allclose(out.double().cpu().numpy(), want, rtol=2e-3, atol=2e-3)
+        assert np.allclose(got.double().cpu().numpy(), lse, rtol=1e-4, atol=1e-4)
+        assert np.allclose(cache.weight.cpu().numpy(), weight, rtol=1e-3, atol=1e-6)
+
+
+def test_bad_pages_and_lengths_are_met(kv8):
+    """Page numbers and lengths out of range: reported, unseen, harmless."""
+    from cross_core_barrier_amd import ccb
+    rng = np.random.default_rng(15)
+    lens = [100, 100, 100, 100]
+    c = _host(rng, "int8", lens, 2, 16, 64)
+    want_c = {k: (v.copy() if isinstance(v, np.ndarray) else v) for k, v in c.items()}
+    c["weight"] = np.zeros((4, 2, c["table"].shape[1] * 16), np.float32)
+    cache = _device(kv8, c)
+    cache.page_table[0, 2] = -1
+    cache.page_table[1, 0] = c["k"].shape[0]
+    cache.page_table[1, 6] = 2**31 - 1
+    cache.lens[2] = c["table"].shape[1] * 16 + 1
+    q = torch.from_numpy(rng.normal(0, 1, (4, 1, 4, 64))).half()
+    _say("attend with bad pages and a bad length")
+    out, lse = cache.attend(q.cuda(), accumulate=True)
+    with pytest.raises(ccb.CcbError):
+        cache.check()
+    cache.check()  # cleared
+    # the oracle without the tokens of the bad pages
+    for b, gone in ((0, range(32, 48)), (1, list(range(16)) + list(range(96, 100)))):
+        stay = np.array([t for t in range(100) if t not in gone])
+        for h in range(2):
+            k, v = oracle.dense(want_c, "k", b, h, stay), oracle.dense(want_c, "v", b, h, stay)
+            for j in (2 * h, 2 * h + 1):
+                s = k @ q[b, 0, j].double().numpy() * 0.125
+                p = np.exp(s - s.max())
+                assert np.allclose(out[b, 0, j].double().cpu().numpy(), p @ v / p.sum(), rtol=2e-3, atol=2e-3)
+        assert float(cache.weight[b, :, list(gone)].abs().max()) == 0
+    assert float(out[2].abs().max()) == 0 and torch.isneginf(lse[2]).all()
+    want, *_ = oracle.attend(want_c, q.double().numpy(), 0.125, 0)
+    assert np.allclose(out[3].double().cpu().numpy(), want[3], rtol=2e-3, atol=2e-3)
+    # append, evict and read meet them too
+    before = (cache.k.clone(), cache.v.clone())
+    x = torch.ones((4, 5, 2, 64), dtype=torch.bfloat16, device="cuda")
+    counts = torch.tensor([0, 2, 3, 6], dtype=torch.int32, device="cuda")  # 2: page 2^31 - 1; 6 > 5
+    _say("append with bad pages, lengths and counts")
+    cache.append(x, x, counts)
+    assert torch.equal(cache.k, before[0]) and torch.equal(cache.v, before[1])
+    with pytest.raises(ccb.CcbError):
+        cache.check()
+    _say("read with bad pages and lengths")
+    k, _ = cache.read(100)
+    assert float(k[0, 32:48].abs().max()) == 0 and float(k[2].abs().max()) == 0
+    assert np.array_equal(k[3].double().cpu().numpy(), np.float32(oracle.read(want_c, 100, [0] * 4)[0][3]).astype(float))
+    with pytest.raises(ccb.CcbError):
+        cache.check()
+    to = kv8.Kv8Cache.allocate(20, 2, 16, 64, 4, 4, "int8", weights=True)
+    to.page_table.copy_(torch.arange(16, dtype=torch.int32).view(4, 4))
+    to.page_table[3, 1] = -5
+    _say("evict with bad pages and lengths")
+    cache.evict(to, 40, recent=10)
+    with pytest.raises(ccb.CcbError):
+        cache.check()
+    assert to.lens.tolist() == [40, 40, 0, 40]
+
+
+# --- append ---------------------------------------------------------------------------
+
+def _append_case(kv8, seed, fmt, dtype, lens, counts, n, heads, P, D, strided=False, special=False, quiet=1.0,
+                 null_counts=False):
+    rng = np.random.default_rng(seed)
+    c = _host(rng, fmt, lens, heads, P, D, quiet=quiet)
+    c["weight"] = rng.uniform(0, 1, (len(lens), heads, c["table"].shape[1] * P)).astype(np.float32)
+    cache = _device(kv8, c)
+    xs = []
+    for _ in range(2):
+        x = rng.normal(0, 1, (len(lens), n, heads, D)) * rng.choice([0.01, 1, 8], (len(lens), n, heads, 1))
+        if special:
+            pick = rng.random(x.shape)
+            x[pick < 0.02] = np.nan
+            x[(pick > 0.02) & (pick < 0.03)] = np.inf
+            x[(pick > 0.03) & (pick < 0.04)] = -np.inf
+            x[:, :, 0] = 0
+            x[0, :, 1] = np.nan
+        xs.append(torch.from_numpy(x).to(TYPES[dtype]))
+    oracle.append(c, xs[0].double().numpy(), xs[1].double().numpy(), counts)
+    dx = [x.cuda() for x in xs]
+    if strided:
+        dx = [_spread_heads(x, 3) for x in dx]
+    dc = None if null_counts else torch.tensor(counts, dtype=torch.int32, device="cuda")
+    for again in range(2):  # a second call changes nothing
+        cache.append(dx[0], dx[1], dc)
+        for which, codes, scales in (("k", cache.k, cache.k_scale), ("v", cache.v, cache.v_scale)):
+            got = _codes(codes)
+            s = scales.cpu().numpy()
+            assert np.array_equal(s, c[which + "s"], equal_nan=True), (which, again)
+            junk = 0x7F if fmt == "e4m3" else 0x80
+            # -0 and 0 are one value
+            same = (got == c[which]) | (((got | c[which]) == 0x80) & (fmt == "e4m3") & (junk != 0x80))
+            assert same.all(), (which, again, np.argwhere(~same)[:5])
+        assert np.array_equal(cache.weight.cpu().numpy(), c["weight"])
+    cache.check()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,P", [(64, 16), (96, 32), (128, 64), (192, 128), (256, 128), (128, 128), (256, 16)])
+def test_append_one_token(kv8, fmt, dtype, D, P):
+    _say(f"append one token {fmt} {dtype} D={D} P={P}")
+    lens = [1, 2, P - 1, P, P + 1, 2 * P, 3 * P + 5]
+    _append_case(kv8, D + P, fmt, dtype, lens, [1] * 7, 1, 3, P, D, null_counts=True, quiet=0.3)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D,P", [(64, 16), (96, 64), (128, 128), (256, 32)])
+@pytest.mark.parametrize("special", [False, True])
+def test_append_many_tokens(kv8, fmt, D, P, special):
+    _say(f"append many {fmt} D={D} P={P} special={special}")
+    _append_case(kv8, P, fmt, "bf16", [300, 77, 5, 200, 0], [300, 70, 0, 129, 0], 300, 2, P, D, strided=True,
+                 special=special, quiet=0.1)
+
+
+def test_append_whole_pages(kv8):
+    """Counts and starts that fall on page borders."""
+    _say("append whole pages")
+    _append_case(kv8, 3, "int8", "fp16", [64, 128, 96, 33], [64, 64, 32, 32], 64, 2, 32, 64)
+
+
+def test_append_tiny_and_huge_values(kv8):
+    """Subnormal values and the largest bf16 values."""
+    from cross_core_barrier_amd import ccb  # noqa: F401
+    for fmt in ("int8", "e4m3"):
+        c = _host(np.random.default_rng(4), fmt, [3, 2], 1, 16, 64)
+        cache = _device(kv8, c)
+        x = torch.zeros((2, 2, 1, 64), dtype=torch.bfloat16)
+        x[0, 0] = torch.linspace(-3.3e38, 3.3e38, 64)
+        x[0, 1] = 1e30
+        x[1, 0] = 2.0 ** -130
+        x[1, 1] = torch.linspace(-1, 1, 64) * 2.0 ** -66
+        _say(f"append tiny and huge values {fmt}")
+        oracle.append(c, x.double().numpy(), x.double().numpy(), [2, 2])
+        cache.append(x.cuda(), x.cuda())
+        assert np.array_equal(cache.k_scale.cpu().numpy(), c["ks"], equal_nan=True)
+        got = oracle.values(_codes(cache.k), fmt)
+        assert np.array_equal(got, oracle.values(c["k"], fmt), equal_nan=True)
+
+
+# --- evict and read -------------------------------------------------------------------
+
+def _evict_case(kv8, seed, fmt, lens, budget, recent, sinks, heads, P, D, ties=False, shared=True):
+    rng = np.random.default_rng(seed)
+    batch, out_width = len(lens), -(-budget // P)
+    c = _host(rng, fmt, lens, heads, P, D, extra=batch * out_width + 2)
+    room = c["table"].shape[1] * P
+    w = rng.exponential(1, (batch, heads, room)).astype(np.float32)
+    if ties:
+        w = np.round(w * 2) / 2
+        w[rng.random(w.shape) < 0.05] = np.nan
+        w[rng.random(w.shape) < 0.02] = np.inf
+        w[rng.random(w.shape) < 0.1] *= -1
+    c["weight"] = w.astype(np.float32)
+    free = np.setdiff1d(np.arange(c["k"].shape[0]), c["table"])
+    to = dict(c, table=rng.permutation(free)[:batch * out_width].astype(np.int32).reshape(batch, out_width),
+              lens=np.full(batch, -7, np.int32), weight=np.full((batch, heads, out_width * P), 5, np.float32))
+    cache = _device(kv8, c)
+    dst = kv8.Kv8Cache(cache.k, cache.v, cache.k_scale, cache.v_scale, torch.from_numpy(to["table"]).cuda(),
+                       torch.from_numpy(to["lens"]).cuda(), torch.from_numpy(to["weight"]).cuda())
+    index = oracle.evict(c, to, budget, recent, sinks)
+    ws = cache.evict_workspace(budget)
+    kept = torch.zeros((batch, heads, budget), dtype=torch.int32, device="cuda")
+    for again in range(3):  # the workspace is ready for the next call
+        kept.zero_()
+        dst.weight.fill_(5)
+        cache.evict(dst, budget, recent, sinks, kept=kept, workspace=ws)
+        assert np.array_equal(kept.cpu().numpy(), index), again
+        assert np.array_equal(dst.lens.cpu().numpy(), to["lens"])
+        assert np.array_equal(dst.weight.cpu().numpy(), to["weight"], equal_nan=True)
+        k, v = dst.read(budget)
+        for got, which in ((k, "k"), (v, "v")):
+            x = got.double().cpu().numpy()
+            for b in range(batch):
+                n = to["lens"][b]
+                assert np.all(x[b, n:] == 0)
+                for h in range(heads):
+                    want = oracle.dense(to, which, b, h, np.arange(n)).astype(np.float32).astype(np.float64)
+                    assert np.array_equal(x[b, :n, h], want), (again, which, b, h)
+    cache.check()
+    dst.check()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D,P", [(64, 16), (96, 32), (128, 64), (192, 128), (256, 128)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict(kv8, fmt, D, P, ties):
+    _say(f"evict {fmt} D={D} P={P} ties={ties}")
+    _evict_case(kv8, D, fmt, [0, 1, 60, 61, 100, 333], 60, 13, 4, 2, P, D, ties)
+
+
+@pytest.mark.parametrize("budget,recent,sinks", [(1, 0, 0), (1, 1, 0), (1, 0, 1), (700, 0, 0), (700, 696, 4),
+                                                 (700, 0, 700), (129, 64, 1), (1025, 100, 4)])
+def test_evict_budgets(kv8, budget, recent, sinks):
+    _say(f"evict budget={budget} recent={recent} sinks={sinks}")
+    _evict_case(kv8, budget, "int8", [2500, 1024, 1025, 3], budget, recent, sinks, 2, 32, 64, ties=True)
+
+
+@pytest.mark.parametrize("same", [0.0, 1.0, math.nan, -math.inf])
+def test_evict_all_alike(kv8, same):
+    """Equal weights: the lowest tokens stay."""
+    rng = np.random.default_rng(1)
+    c = _host(rng, "int8", [3000, 40], 1, 64, 64)
+    c["weight"] = np.full((2, 1, c["table"].shape[1] * 64), same, np.float32)
+    cache = _device(kv8, c)
+    to = kv8.Kv8Cache.allocate(16, 1, 64, 64, 2, 8, "int8", weights=False)
+    to.page_table.copy_(torch.arange(16, dtype=torch.int32).view(2, 8))
+    kept = torch.zeros((2, 1, 500), dtype=torch.int32, device="cuda")
+    _say(f"evict with every weight {same}")
+    cache.evict(to, 500, recent=7, sinks=2, kept=kept)
+    want = list(range(493)) + list(range(2993, 3000))
+    assert kept[0, 0].tolist() == want
+    assert kept[1, 0].tolist() == list(range(40)) + [-1] * 460
+
+
+def test_evict_long(kv8):
+    """A long row, many heads: selection over several workgroups' worth."""
+    _say("evict 40001 tokens")
+    _evict_case(kv8, 2, "int8", [40001, 9000], 2000, 64, 4, 3, 128, 64, ties=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_read(kv8, fmt, dtype):
+    rng = np.random.default_rng(3)
+    c = _host(rng, fmt, [0, 5, 64, 130], 3, 32, 96)
+    cache = _device(kv8, c)
+    first = [0, -3, 60, 100]
+    _say(f"read {fmt} {dtype}")
+    t = {**TYPES, "fp32": torch.float32}[dtype]
+    got = cache.read(70, torch.tensor(first, dtype=torch.int32, device="cuda"), dtype=t)
+    for x, want in zip(got, oracle.read(c, 70, first)):
+        # code * scale as float, then rounded once to the type
+        exact = torch.from_numpy(want.astype(np.float32)).to(t)
+        assert torch.equal(x.cpu(), exact)
+    cache.check()
+
+
+# --- streams, graphs, far pages --------------------------------------------------------
+
+def _step(cache, k, v, q, ws):
+    cache.append(k, v)
+    return cache.attend(q, accumulate=True, workspace=ws)
+
+
+def test_side_stream(kv8):
+    rng = np.random.default_rng(20)
+    c = _host(rng, "e4m3", [400, 33, 129], 2, 32, 128)
+    c["weight"] = np.zeros((3, 2, c["table"].shape[1] * 32), np.float32)
+    k, v = (torch.from_numpy(rng.normal(0, 1, (3, 1, 2, 128))).half().cuda() for _ in range(2))
+    q = torch.from_numpy(rng.normal(0, 1, (3, 1, 8, 128))).half().cuda()
+    a, b = _device(kv8, c), _device(kv8, c)
+    s = torch.cuda.Stream()
+    _say("append + attend + read on a side stream")
+    want = _step(a, k, v, q, None)
+    b.append(k, v, stream=s)
+    got = b.attend(q, accumulate=True, stream=s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(a.weight, b.weight)
+    with torch.cuda.stream(s):
+        again = b.read(20)
+    s.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(again, a.read(20)))
+
+
+def test_graph_replays(kv8):
+    """A whole step and an eviction captured once, replayed with other inputs,
+    lengths and pages, with eager work between."""
+    rng = np.random.default_rng(21)
+    c = _host(rng, "int8", [500, 120, 64], 2, 32, 64, width=20)
+    c["weight"] = np.zeros((3, 2, 20 * 32), np.float32)
+    cache, plain = _device(kv8, c), _device(kv8, c)
+    k, v = (torch.zeros((3, 1, 2, 64), dtype=torch.float16, device="cuda") for _ in range(2))
+    q = torch.zeros((3, 1, 8, 64), dtype=torch.float16, device="cuda")
+    to, to_plain = (kv8.Kv8Cache.allocate(9, 2, 32, 64, 3, 3, "int8", weights=True) for _ in range(2))
+    for t in (to, to_plain):
+        t.page_table.copy_(torch.arange(9, dtype=torch.int32).view(3, 3))
+    kept, kept_plain = (torch.zeros((3, 2, 90), dtype=torch.int32, device="cuda") for _ in range(2))
+    ws, ews = cache.attend_workspace(8, 1, True), cache.evict_workspace(90)
+    out, lse = torch.empty_like(q), torch.empty((3, 1, 8), device="cuda")
+    _step(cache, k, v, q, ws)  # once outside the capture
+    cache.evict(to, 90, 20, 2, kept=kept, workspace=ews)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.lens.add_(1)
+        cache.append(k, v)
+        cache.attend(q, accumulate=True, out=out, lse=lse, workspace=ws)
+        cache.evict(to, 90, 20, 2, kept=kept, workspace=ews)
+    for t in ("k", "v", "k_scale", "v_scale", "weight", "lens"):
+        getattr(cache, t).copy_(getattr(plain, t))
+    for rep in range(5):
+        _say(f"graph replay {rep}")
+        for t in (k, v, q):
+            t.copy_(torch.from_numpy(rng.normal(0, 1, t.shape)).half())
+        if rep == 3:  # other lengths, eagerly (of tokens that were written)
+            for x in (cache, plain):
+                x.lens.copy_(torch.tensor([3, 119, 40], dtype=torch.int32))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        plain.lens.add_(1)
+        plain.append(k, v)
+        want = plain.attend(q, accumulate=True)
+        plain.evict(to_plain, 90, 20, 2, kept=kept_plain)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), rep
+        assert torch.equal(cache.weight, plain.weight) and torch.equal(kept, kept_plain), rep
+        assert torch.equal(to.lens, to_plain.lens) and torch.equal(to.weight, to_plain.weight), rep
+        assert all(torch.equal(x, y) for x, y in zip(to.read(90), to_plain.read(90))), rep
+
+
+def test_pages_past_32_bits(kv8):
+    """Pages whose bytes lie beyond 2^32: every operator on the far end of a
+    5.4 GB pool."""
+    heads, P, D = 8, 128, 128
+    pages = 41_000  # 41,000 * 8 * 128 * 128 bytes
+    k, v = (torch.empty((pages, heads, P, D), dtype=torch.int8, device="cuda") for _ in range(2))
+    scales = [torch.full((pages, heads), math.nan, device="cuda") for _ in range(2)]
+    lens = [300, 129]
+    rng = np.random.default_rng(22)
+    table = torch.tensor([[pages - 1, pages - 7, pages - 3], [pages - 2, 5, 40_000]], dtype=torch.int32, device="cuda")
+    far = kv8.Kv8Cache(k, v, *scales, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                       torch.zeros((2, heads, 3 * P), device="cuda"))
+    near = kv8.Kv8Cache.allocate(6, heads, P, D, 2, 3, "int8", weights=True)
+    near.page_table.copy_(torch.arange(6, dtype=torch.int32).view(2, 3))
+    near.lens.copy_(far.lens)
+    x = [torch.from_numpy(rng.normal(0, 1, (2, 300, heads, D))).half().cuda() for _ in range(2)]
+    q = torch.from_numpy(rng.normal(0, 1, (2, 1, 16, D))).half().cuda()
+    counts = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    _say("append, attend, evict and read beyond 2^32 bytes")
+    results = []
+    for c, out_pages in ((far, [[pages - 10], [pages - 9]]), (near, None)):
+        c.append(*x, counts)
+        got = [*c.attend(q, accumulate=True), c.weight]
+        if out_pages is None:
+            dst = kv8.Kv8Cache.allocate(2, heads, P, D, 2, 1, "int8", weights=True)
+            dst.page_table.copy_(torch.tensor([[0], [1]], dtype=torch.int32))
+        else:
+            dst = kv8.Kv8Cache(k, v, *scales, torch.tensor(out_pages, dtype=torch.int32, device="cuda"),
+                               torch.zeros(2, dtype=torch.int32, device="cuda"),
+                               torch.zeros((2, heads, P), device="cuda"))
+        kept = torch.zeros((2, heads, 100), dtype=torch.int32, device="cuda")
+        c.evict(dst, 100, 10, 2, kept=kept)
+        results.append([*got, kept, dst.weight, *dst.read(100), *c.read(300)])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

@@ -1,0 +1,291 @@
+"""The 8-bit key/value cache on the CPU: its rounding and range checks,
+compiled for the host, against exact fractions; the oracle against itself on
+tiny inputs; and every refusal of the entry points that precedes device work."""
+
+import ctypes
+import math
+import os
+import subprocess
+from fractions import Fraction
+
+import numpy as np
+import pytest
+
+from oracle import kv8 as oracle
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+FMT = {"int8": "0", "e4m3": "1"}
+
+
+@pytest.fixture(scope="module")
+def driver(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("kv8") / "math_driver")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-ffp-contract=off", "-I",
+                    os.path.join(ROOT, "cross_core_barrier_amd", "csrc"),
+                    os.path.join(HERE, "kv8", "math_driver.cpp"), "-o", exe], check=True)
+
+    def run(mode, fmt, data, dtype):
+        res = subprocess.run([exe, mode] + ([FMT[fmt]] if fmt else []), input=np.ascontiguousarray(data).tobytes(),
+                             capture_output=True, check=True)
+        return np.frombuffer(res.stdout, dtype)
+    return run
+
+
+def _exact(x) -> Fraction:
+    return Fraction(float(x))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_new_values_round_once(driver, fmt):
+    """Codes of bf16-like values over random scales, among them values that
+    lie on or next to the border between two codes."""
+    rng = np.random.default_rng(1)
+    s = (rng.uniform(1, 2, 6000) * 2.0 ** rng.integers(-60, 60, 6000)).astype(np.float32)
+    s[:2000] = (2.0 ** rng.integers(-40, 40, 2000)).astype(np.float32)  # exact borders happen
+    grid = np.arange(128.0) if fmt == "int8" else oracle._GRID
+    i = rng.integers(0, len(grid) - 1, 6000)
+    border = (grid[i] + grid[i + 1]) / 2
+    x = (border * s.astype(np.float64)).astype(np.float32)
+    x[3000:] = (rng.uniform(-1.2, 1.2, 3000) * oracle.Q[fmt] * s[3000:]).astype(np.float32)
+    x[::7] = np.nextafter(x[::7], np.float32(0))
+    x[1::7] = np.nextafter(x[1::7], np.float32(np.inf))
+    x[::2] *= -1
+    inv = (np.float32(1) / s).astype(np.float32)
+    got = driver("v", fmt, np.stack([x, inv, s], 1), np.uint8)
+    want = np.array([oracle.nearest_code(_exact(a) / _exact(b), fmt) for a, b in zip(x, s)], np.uint8)
+    assert np.array_equal(oracle.values(got, fmt), oracle.values(want, fmt))
+    # a reciprocal that is off by a few units changes nothing
+    for ulps in (-3, 3):
+        off = inv.copy()
+        for _ in range(abs(ulps)):
+            off = np.nextafter(off, np.float32(np.inf if ulps > 0 else 0))
+        assert np.array_equal(driver("v", fmt, np.stack([x, off, s], 1), np.uint8), got)
+    assert np.array_equal(oracle.values(oracle.encode(x.astype(np.float64), s, fmt), fmt), oracle.values(want, fmt))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_old_codes_round_once(driver, fmt):
+    """code * s0 / s1 for every code, at random and at simple ratios (ties)."""
+    rng = np.random.default_rng(2)
+    codes = np.array([c for c in range(256) if c not in ((0x80,) if fmt == "int8" else (0x7F, 0xFF))], np.uint8)
+    v = oracle.values(codes, fmt).astype(np.float32)
+    for trial in range(40):
+        s0 = np.float32(rng.uniform(1, 2) * 2.0 ** int(rng.integers(-40, 40)))
+        ratio = [1.0, 2.0, 3.0, 6.0, 5.0, 4.0, 1.5][trial] if trial < 7 else rng.uniform(1, 30)
+        s1 = np.float32(s0 * np.float32(ratio))
+        hi = (v * s0).astype(np.float32)
+        lo = (v.astype(np.float64) * np.float64(s0) - hi).astype(np.float32)
+        n = len(v)
+        rec = np.stack([hi, lo, np.full(n, np.float32(1) / s1, np.float32), np.full(n, s1, np.float32)], 1)
+        got = driver("e", fmt, rec, np.uint8)
+        want = np.array([oracle.nearest_code(_exact(a) * _exact(s0) / _exact(s1), fmt) for a in v], np.uint8)
+        assert np.array_equal(oracle.values(got, fmt), oracle.values(want, fmt)), (trial, s0, s1)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_special_values(driver, fmt):
+    one = np.float32(1)
+    x = np.array([np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-40, 3e38, -3e38], np.float32)
+    got = oracle.values(driver("v", fmt, np.stack([x, np.full(8, one), np.full(8, one)], 1), np.uint8), fmt)
+    q = oracle.Q[fmt]
+    assert np.array_equal(got, [0, q, -q, 0, 0, 0, q, -q])
+    # a block of zeros has scale 0 and codes 0
+    assert driver("v", fmt, np.array([[np.inf, np.inf, 0], [0, np.inf, 0]], np.float32), np.uint8).tolist() == [0, 0]
+    a = np.array([0.0, 1e-30, 127.0, 448.0, 1.0, 3e38], np.float32)
+    want = np.array([oracle.block_scale(v, fmt) for v in a], np.float32)
+    assert np.array_equal(driver("b", fmt, a, np.float32), want)
+    assert want[0] == 0 and want[1] == np.float32(2.0 ** -64)
+
+
+def test_weight_order(driver):
+    w = np.array([-np.inf, -2.0, -1e-40, 0.0, 1e-45, 1e-40, 0.5, 1.0, 3e38, np.inf], np.float32)
+    key = driver("w", None, w, np.uint32).astype(np.int64)
+    assert np.all(np.diff(key) > 0)
+    nan = driver("w", None, np.array([np.nan, -np.nan], np.float32), np.uint32)
+    assert nan.tolist() == [0, 0] and key[0] > 0
+    assert len(set(driver("w", None, np.array([0.0, -0.0], np.float32), np.uint32).tolist())) == 1
+
+
+def test_range_checks(driver):
+    lens = np.array([[0, 64], [64, 64], [65, 64], [-1, 64], [-2**31, 64], [2**31 - 1, 64]], np.int32)
+    assert driver("l", None, lens, np.int32).tolist() == [0, 64, -1, -1, -1, -1]
+    pages = np.array([[0, 7], [6, 7], [7, 7], [-1, 7], [-2**31, 7], [2**31 - 1, 7]], np.int32)
+    assert driver("p", None, pages, np.int32).tolist() == [0, 6, -1, -1, -1, -1]
+
+
+def test_oracle_on_worked_values():
+    """One page, one head, numbers small enough to follow by hand."""
+    c = dict(k=np.zeros((1, 1, 16, 2), np.uint8), v=np.zeros((1, 1, 16, 2), np.uint8), ks=np.ones((1, 1), np.float32),
+             vs=np.ones((1, 1), np.float32), table=np.zeros((1, 1), np.int32), lens=np.array([1], np.int32),
+             weight=np.full((1, 1, 16), 9, np.float32), fmt="int8")
+    oracle.append(c, np.array([[[[127.0, 1.0]]]]), np.array([[[[2.0, 4.0]]]]), [1])
+    assert c["k"][0, 0, 0].tolist() == [127, 1] and c["ks"][0, 0] == 1  # s = 127 / 127
+    assert c["v"][0, 0, 0].tolist() == [64, 127]  # 2 * 127 / 4 = 63.5: half to even
+    assert c["weight"][0, 0, :2].tolist() == [0, 9]
+    c["lens"][0] = 2
+    oracle.append(c, np.array([[[[254.0, 0.0]]]]), np.array([[[[4.0, 0.0]]]]), [1])
+    assert c["k"][0, 0, :2].tolist() == [[64, 0], [127, 0]]  # 63.5 -> 64, 0.5 -> 0
+    out, lse, w, _, _ = oracle.attend(c, np.zeros((1, 1, 1, 2)), 1.0, 0)
+    assert np.allclose(lse, math.log(2)) and np.allclose(w[0, 0, :2], 0.5)
+    assert oracle.kept(np.array([1, 3, 3, math.nan, 0, 5.0]), 6, 3, 1, 0) == [1, 2, 5]
+    assert oracle.kept(np.array([1, 3, 3, math.nan, 0, 5.0]), 6, 5, 1, 0) == [0, 1, 2, 4, 5]
+
+
+# --- refusals --------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def ccb():
+    from cross_core_barrier_amd import ccb as lib
+    return lib
+
+
+def _cache(ccb, **changes):
+    f = dict(k=1 << 20, v=2 << 20, kScale=3 << 20, vScale=4 << 20, pageTable=5 << 20, lens=6 << 20, weight=7 << 20,
+             tableStride=4, weightStride=64, format=0, numPages=8, heads=2, pageSize=16, headDim=64, batch=3, maxPages=4,
+             reserved=0)
+    f.update(changes)
+    return ccb.ccbKv8Cache(**f)
+
+
+def _rows(ccb, **changes):
+    f = dict(data=8 << 20, strideBatch=512, strideToken=128, strideHead=64, type=0, reserved=0)
+    f.update(changes)
+    return ccb.ccbKv8Rows(**f)
+
+
+BAD_CACHES = [dict(format=2), dict(format=-1), dict(pageSize=8), dict(pageSize=48), dict(pageSize=256),
+              dict(headDim=32), dict(headDim=100), dict(headDim=512), dict(numPages=0), dict(heads=0), dict(batch=-1),
+              dict(maxPages=0), dict(maxPages=1 << 27, tableStride=1 << 27), dict(tableStride=3), dict(weightStride=63),
+              dict(k=(1 << 20) + 8), dict(v=(1 << 20) + 8), dict(kScale=2), dict(vScale=2), dict(pageTable=2),
+              dict(lens=2), dict(weight=2), dict(reserved=1)]
+NULL_CACHES = [dict(k=0), dict(v=0), dict(kScale=0), dict(vScale=0), dict(pageTable=0), dict(lens=0)]
+BAD_ROWS = [dict(type=2), dict(type=3), dict(type=-1), dict(data=(8 << 20) + 2), dict(strideBatch=4),
+            dict(strideToken=130), dict(strideHead=1), dict(reserved=1)]
+
+
+def _calls(ccb, cache, rows):
+    big = 1 << 30
+    return {
+        "append": lambda: ccb.ccb_kv8_append(cache, rows, rows, 2),
+        "attend": lambda: ccb.ccb_kv8_attend(cache, rows, rows, None, 4, 1, 0.1, 0, 0, 9 << 20, big),
+        "evict": lambda: ccb.ccb_kv8_evict(cache, _cache(ccb, pageTable=10 << 20, lens=11 << 20, weight=12 << 20), 32,
+                                           4, 4, None, 9 << 20, big),
+        "read": lambda: ccb.ccb_kv8_read(cache, rows, rows, 5),
+    }
+
+
+def test_struct_sizes(ccb):
+    assert ctypes.sizeof(ccb.ccbKv8Cache) == 7 * 8 + 2 * 8 + 8 * 4
+    assert ctypes.sizeof(ccb.ccbKv8Rows) == 4 * 8 + 2 * 4
+
+
+@pytest.mark.parametrize("change", BAD_CACHES, ids=str)
+def test_refuses_a_bad_cache(ccb, change):
+    for name, call in _calls(ccb, _cache(ccb, **change), _rows(ccb)).items():
+        assert call() == ccb.CCB_ERR_INVALID_VALUE, name
+    assert ccb.ccb_kv8_attend_workspace_bytes(_cache(ccb, **change), 4, 1, 0) == 0
+    assert ccb.ccb_kv8_evict_workspace_bytes(_cache(ccb, **change), 32) == 0
+
+
+@pytest.mark.parametrize("change", NULL_CACHES, ids=str)
+def test_refuses_missing_tensors(ccb, change):
+    for name, call in _calls(ccb, _cache(ccb, **change), _rows(ccb)).items():
+        assert call() == ccb.CCB_ERR_NULL_POINTER, name
+    for name, call in _calls(ccb, None, _rows(ccb)).items():
+        assert call() == ccb.CCB_ERR_NULL_POINTER, name
+
+
+@pytest.mark.parametrize("change", BAD_ROWS, ids=str)
+def test_refuses_bad_rows(ccb, change):
+    calls = _calls(ccb, _cache(ccb), _rows(ccb, **change))
+    for name in ("append", "attend"):
+        assert calls[name]() == ccb.CCB_ERR_INVALID_VALUE, name
+    if change != dict(type=2):  # float rows can be read into
+        assert calls["read"]() == ccb.CCB_ERR_INVALID_VALUE
+
+
+def test_refuses_bad_arguments(ccb):
+    c, r = _cache(ccb), _rows(ccb)
+    inv, null, ok = ccb.CCB_ERR_INVALID_VALUE, ccb.CCB_ERR_NULL_POINTER, ccb.CCB_OK
+    ws, big = 9 << 20, 1 << 30
+    # append
+    assert ccb.ccb_kv8_append(c, r, r, -1) == inv
+    assert ccb.ccb_kv8_append(c, r, r, 65) == inv
+    assert ccb.ccb_kv8_append(c, None, r, 1) == null
+    assert ccb.ccb_kv8_append(c, r, None, 1) == null
+    assert ccb.ccb_kv8_append(c, r, _rows(ccb, data=0), 1) == null
+    assert ccb.ccb_kv8_append(c, r, _rows(ccb, type=1), 1) == inv
+    assert ccb.ccb_kv8_append(c, r, r, 1, counts=2) == inv
+    assert ccb.ccb_kv8_append(c, r, r, 1, err=2) == inv
+    assert ccb.ccb_kv8_append(c, None, None, 0) == ok  # nothing to do
+    assert ccb.ccb_kv8_append(_cache(ccb, batch=0, k=0), None, None, 1) == ok
+    # attend
+    def attend(cache=c, q=r, out=r, lse=None, heads=4, n=1, scale=0.1, window=0, acc=0, w=ws, size=big, err=None):
+        return ccb.ccb_kv8_attend(cache, q, out, lse, heads, n, scale, window, acc, w, size, err)
+    assert attend(heads=3) == inv and attend(heads=0) == inv and attend(n=-1) == inv and attend(window=-1) == inv
+    assert attend(scale=math.nan) == inv and attend(scale=math.inf) == inv
+    assert attend(q=None) == null and attend(out=None) == null and attend(out=_rows(ccb, type=1)) == inv
+    assert attend(lse=2) == inv and attend(err=2) == inv
+    assert attend(w=None) == null and attend(w=ws + 64) == inv
+    need = ccb.ccb_kv8_attend_workspace_bytes(c, 4, 1, 0)
+    assert need > 0 and attend(size=need - 1) == inv
+    assert attend(cache=_cache(ccb, weight=0), acc=1) == null
+    assert attend(n=0, q=None, out=None, w=None) == ok
+    assert attend(cache=_cache(ccb, batch=0, k=0), q=None) == ok
+    assert ccb.ccb_kv8_attend_workspace_bytes(c, 3, 1, 0) == 0
+    # evict
+    to = dict(pageTable=10 << 20, lens=11 << 20, weight=12 << 20)
+
+    def evict(src=c, dst=_cache(ccb, **to), budget=32, recent=4, sinks=4, kept=None, w=ws, size=big, err=None):
+        return ccb.ccb_kv8_evict(src, dst, budget, recent, sinks, kept, w, size, err)
+    assert evict(budget=0) == inv and evict(recent=-1) == inv and evict(sinks=-1) == inv
+    assert evict(recent=30, sinks=3) == inv and evict(budget=65) == inv
+    assert evict(dst=None) == null and evict(src=_cache(ccb, weight=0)) == null and evict(w=None) == null
+    for change in (dict(format=1), dict(heads=1), dict(headDim=128), dict(pageSize=32, weightStride=128),
+                   dict(batch=2), dict(maxPages=1)):
+        assert evict(dst=_cache(ccb, **{**to, **change})) == inv, change
+    for same in ("pageTable", "lens", "weight"):  # these belong to one cache only
+        assert evict(dst=_cache(ccb, **{**to, same: getattr(c, same)})) == inv, same
+    assert evict(kept=2) == inv and evict(err=2) == inv and evict(w=ws + 64) == inv
+    need = ccb.ccb_kv8_evict_workspace_bytes(c, 32)
+    assert need > 0 and evict(size=need - 1) == inv
+    assert ccb.ccb_kv8_evict_workspace_bytes(c, 0) == 0
+    assert evict(src=_cache(ccb, batch=0), dst=_cache(ccb, batch=0, **to)) == ok
+    # read
+    assert ccb.ccb_kv8_read(c, r, r, -1) == inv
+    assert ccb.ccb_kv8_read(c, None, None, 1) == null
+    assert ccb.ccb_kv8_read(c, r, _rows(ccb, type=1), 1) == inv
+    assert ccb.ccb_kv8_read(c, r, r, 1, first=2) == inv
+    assert ccb.ccb_kv8_read(c, None, None, 0) == ok
+
+
+def test_class_checks_its_tensors():
+    torch = pytest.importorskip("torch")
+    from cross_core_barrier_amd import kv8
+    f = dict(k=torch.zeros((4, 2, 16, 64), dtype=torch.int8), v=torch.zeros((4, 2, 16, 64), dtype=torch.int8),
+             k_scale=torch.zeros((4, 2)), v_scale=torch.zeros((4, 2)), page_table=torch.zeros((3, 2), dtype=torch.int32),
+             lens=torch.zeros(3, dtype=torch.int32), weight=torch.zeros((3, 2, 32)))
+    c = kv8.Kv8Cache(**f)
+    for name, bad in (("k", f["k"].float()), ("v", f["v"][:3]), ("k_scale", f["k_scale"].double()),
+                      ("v_scale", f["v_scale"][:, :1]), ("page_table", f["page_table"].long()),
+                      ("page_table", torch.zeros((2, 3), dtype=torch.int32).t()), ("lens", f["lens"][:2]),
+                      ("weight", f["weight"][:, :, :31]), ("k", f["k"].transpose(1, 2))):
+        with pytest.raises(ValueError):
+            kv8.Kv8Cache(**{**f, name: bad})
+    x = torch.zeros((3, 1, 2, 64), dtype=torch.bfloat16)
+    for bad in (x.double(), x[:, :, :1], x[:2], x[..., :32], x[0], torch.zeros((3, 1, 64, 2)).transpose(2, 3)):
+        with pytest.raises(ValueError):
+            c.append(bad, bad)
+    with pytest.raises(ValueError):
+        c.append(x, x.half())
+    with pytest.raises(ValueError):
+        c.append(x, x, counts=torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        c.evict(c, 8, kept=torch.zeros((3, 2, 7), dtype=torch.int32))
+    with pytest.raises(ValueError):
+        c.read(1, dtype=torch.int8)
+    with pytest.raises(ValueError):
+        c.attend_workspace(3)
+    with pytest.raises(ValueError):
+        kv8.Kv8Cache.allocate(4, 2, 16, 64, 1, 2, fmt="int4", device="cpu")
