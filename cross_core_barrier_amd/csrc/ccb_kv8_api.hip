@@ -62,8 +62,8 @@ ccbStatus done(hipError_t e)
 
 bool attend_sizes_ok(const ccbKv8Cache* c, int32_t headsQ, int32_t nQuery)
 {
-    return headsQ >= 1 && headsQ % c->heads == 0 && headsQ <= (1 << 20) && nQuery >= 0 &&
-           nQuery <= (1 << 20);
+    return headsQ >= 1 && headsQ % c->heads == 0 && nQuery >= 0 &&
+           (int64_t)(headsQ / c->heads) * nQuery <= (1 << 20);
 }
 
 }  // namespace

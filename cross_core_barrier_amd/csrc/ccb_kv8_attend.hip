@@ -1,5 +1,27 @@
 // ccb_kv8_attend.hip -- attention of a decoding step over the 8-bit
-// key/value cache.
+// key/value cache: flash decoding on the matrix cores, split over tokens.
+//
+// The rows of one cache head (its queries and query heads) share every key
+// and value, so one workgroup takes a (sequence, cache head, run of tokens)
+// and up to 16 * NT rows.  Its four waves take 32-token tiles in turn and
+// never wait for one another in the loop: a wave streams its own tiles into
+// its own part of LDS (16 bytes per lane, straight from memory, two tiles
+// ahead) and keeps its own running maximum, sum and weighted values.
+//
+// S^T = K Q^T and O^T = V^T P^T on 16x16x32 tiles.  In that order a row of
+// scores lies on one lane index (lane % 16), so the softmax needs no
+// transposition: a lane's 4 + 4 scores of a tile are the 8 places of the next
+// product's operand that it has to supply.  Which token or dimension stands at
+// which place of a contraction is free as long as both operands agree; keys
+// are read 16 dimensions at a time, values through the transposing LDS read.
+//
+// Codes become 16-bit values exactly (int8 and e4m3 both fit bf16 and fp16),
+// so q k is exact up to its 32-bit sums.  The weights p (times the block's
+// scale) go into the second product as two bf16 pieces, together within 2^-18
+// of p; one piece would cost 2^-9.
+//
+// Bound by memory: a tile of 32 tokens costs a wave about 350 instructions
+// for 64 * D bytes.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -13,135 +35,722 @@ using namespace kv8;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+constexpr int kTile = 32;                     // tokens of a wave's step
+constexpr int kSegment = 32 * kWaves * kTile;  // tokens whose pages fit a wave's lanes
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kSlack = 8.0f;  // how far (in powers of two) scores may pass the running maximum
+constexpr int kStoredRows = 16;  // up to here scores are kept for the weights, beyond they are computed again
+constexpr int kJoinTokens = 1024;
 
-// A lane's share of a token's row: D / 64 values, lanes past the row hold 0.
-template <int D>
-struct Share {
-    static constexpr int n = (D + 63) / 64;
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef int i2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+
+struct Plan {
+    ccb::Kv8AttendArgs a;
+    int32_t rows;       // of a cache head
+    int32_t tilesN;     // NT
+    int32_t rowBlocks;  // workgroups that share a run of tokens
+    int32_t chunk;      // tokens of a workgroup, a multiple of kWaves * kTile
+    int32_t splits;     // runs a sequence may have
+    int32_t joinBlocks;
+    float* partO;   // [pair][split][row][D]
+    float2* partML; // [pair][split][row]: maximum (base 2) and sum
+    float* scores;  // [pair][row][splits * chunk] (base 2), or null
+    float* lse2;    // [pair][row], +infinity for a row that sees nothing; or null
 };
 
-// One workgroup per query row; its waves take every fourth token, keep a
-// running maximum, sum and weighted values, and join at the end.
-template <int F, int T, int D>
-__global__ __launch_bounds__(kThreads) void kv8_k_attend_plain(ccb::Kv8AttendArgs a, float* lseOut)
+// Four codes (lowest byte first) as two words of two 16-bit values.
+template <int F, int T>
+__device__ __forceinline__ void codes16(uint32_t w, uint32_t& a, uint32_t& b)
 {
-    constexpr int N = Share<D>::n;
-    __shared__ float sm[kWaves], sl[kWaves], sacc[kWaves][D];
-    const ccbKv8Cache& c = a.c;
-    uint32_t rest = blockIdx.x;
-    const int32_t hq = rest % (uint32_t)a.headsQ;
-    rest /= (uint32_t)a.headsQ;
-    const int32_t i = rest % (uint32_t)a.nQuery;
-    const int32_t b = rest / (uint32_t)a.nQuery;
-    const int32_t h = hq / (a.headsQ / c.heads);
-    const int32_t P = c.pageSize;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int32_t len = checked_len(c.lens[b], c.maxPages * P);
-    if (len < 0) {
-        if (threadIdx.x == 0) report(a.err);
-        len = 0;
-    }
-    const int32_t end = len - a.nQuery + i + 1;
-    const int32_t begin = a.window > 0 && end > a.window ? end - a.window : 0;
-    const uint16_t* q = (const uint16_t*)a.q.data + b * a.q.strideBatch + i * a.q.strideToken +
-                        hq * a.q.strideHead;
-    float qv[N], acc[N];
+    if constexpr (F == kE4m3 && T == CCB_KV8_BF16) {
+        a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+        b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+    } else if constexpr (F == kE4m3) {
+        a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+        b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
+    } else if constexpr (T == CCB_KV8_BF16) {
+        // a whole number below 2^8 is exact in the upper half of its float
+        float f[4];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        qv[e] = lane + 64 * e < D ? widen<T>(q[lane + 64 * e]) : 0.0f;
-        acc[e] = 0.0f;
-    }
-    float m = -INFINITY, l = 0.0f;
-    for (int32_t t = begin + wave; t < end; t += kWaves) {
-        const int32_t page = checked_page(c.pageTable[b * c.tableStride + t / P], c.numPages);
-        if (page < 0) {
-            if (lane == 0) report(a.err);
-            continue;
-        }
-        const int64_t block = (int64_t)page * c.heads + h;
-        const int64_t off = (block * P + t % P) * D;
-        float s = 0.0f;
-        float v[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            float x[4] = {0, 0, 0, 0}, y[4] = {0, 0, 0, 0};
-            if (lane + 64 * e < D) {
-                decode4<F>(((const uint8_t*)c.k)[off + lane + 64 * e], x);
-                decode4<F>(((const uint8_t*)c.v)[off + lane + 64 * e], y);
-            }
-            s += qv[e] * x[0];
-            v[e] = y[0];
-        }
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
-        s *= c.kScale[block] * a.scale;
-        const float mn = fmaxf(m, s);
-        const float f = expf(m - mn), p = expf(s - mn);
-        l = l * f + p;
-        const float pv = p * c.vScale[block];
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = acc[e] * f + pv * v[e];
-        m = mn;
-    }
-    if (lane == 0) sm[wave] = m, sl[wave] = l;
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-        if (lane + 64 * e < D) sacc[wave][lane + 64 * e] = acc[e];
-    __syncthreads();
-    float mm = -INFINITY, ll = 0.0f;
-    for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, sm[w]);
-    for (int w = 0; w < kWaves; ++w) ll += sl[w] != 0.0f ? sl[w] * expf(sm[w] - mm) : 0.0f;
-    uint16_t* out = (uint16_t*)a.out.data + b * a.out.strideBatch + i * a.out.strideToken +
-                    hq * a.out.strideHead;
-    for (int d = threadIdx.x; d < D; d += kThreads) {
-        float o = 0.0f;
-        for (int w = 0; w < kWaves; ++w) o += sl[w] != 0.0f ? sacc[w][d] * expf(sm[w] - mm) : 0.0f;
-        out[d] = (uint16_t)narrow<T>(ll != 0.0f ? o / ll : 0.0f);
-    }
-    if (threadIdx.x == 0) {
-        const float lse = ll != 0.0f ? mm + logf(ll) : -INFINITY;
-        lseOut[blockIdx.x] = lse;
-        if (a.lse != nullptr) a.lse[blockIdx.x] = lse;
+        for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(w >> (8 * i));
+        a = __builtin_amdgcn_perm(bits(f[1]), bits(f[0]), 0x07060302u);
+        b = __builtin_amdgcn_perm(bits(f[3]), bits(f[2]), 0x07060302u);
+    } else {
+        // 0x6400 | u is 1024 + u in fp16; u = code + 128
+        const uint32_t u = w ^ 0x80808080u;
+        const h2 m = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+        const h2 x = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, u, 0x07010700u)) + m;
+        const h2 y = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, u, 0x07030702u)) + m;
+        a = __builtin_bit_cast(uint32_t, x);
+        b = __builtin_bit_cast(uint32_t, y);
     }
 }
 
-// One thread per token and cache head adds the weights of every row.
-template <int F, int T, int D>
-__global__ __launch_bounds__(kThreads) void kv8_k_weights_plain(ccb::Kv8AttendArgs a, const float* lse,
-                                                                int32_t perRow)
+template <int F, int T>
+__device__ __forceinline__ u4 codes16x8(uint32_t lo, uint32_t hi)
 {
+    uint32_t a, b, c, d;
+    codes16<F, T>(lo, a, b);
+    codes16<F, T>(hi, c, d);
+    return u4{a, b, c, d};
+}
+
+template <int T>
+__device__ __forceinline__ f4 mfma(const u4& a, const u4& b, const f4& c)
+{
+    if constexpr (T == CCB_KV8_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a),
+                                                       __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a),
+                                                      __builtin_bit_cast(h8, b), c, 0, 0, 0);
+}
+
+// a and b as bf16 pieces: hi + lo is within 2^-18 of the value.
+__device__ __forceinline__ void pieces(float a, float b, uint32_t& hi, uint32_t& lo)
+{
+    const bf2 h = {(__bf16)a, (__bf16)b};
+    hi = __builtin_bit_cast(uint32_t, h);
+    const bf2 l = {(__bf16)(a - of_bits(hi << 16)), (__bf16)(b - of_bits(hi & 0xffff0000u))};
+    lo = __builtin_bit_cast(uint32_t, l);
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Sequence, head and what the rows of a workgroup may see.
+struct Range {
+    int32_t len;    // 0 where the length is bad
+    int32_t first;  // first token any query sees
+    int32_t base;   // first, at a tile's border: where the runs start
+};
+
+__device__ __forceinline__ Range range_of(const ccb::Kv8AttendArgs& a, int32_t b)
+{
+    Range r;
+    r.len = checked_len(a.c.lens[b], a.c.maxPages * a.c.pageSize);
+    if (r.len < 0) {
+        if (threadIdx.x == 0) report(a.err);
+        r.len = 0;
+    }
+    const int64_t f = a.window > 0 ? (int64_t)r.len - a.nQuery + 1 - a.window : 0;
+    r.first = f > 0 ? (int32_t)f : 0;
+    r.base = r.first & ~(kTile - 1);
+    return r;
+}
+
+// What query i sees, as [begin, end); empty for a row that is not there.
+__device__ __forceinline__ void seen_by(const ccb::Kv8AttendArgs& a, const Range& r, int32_t row,
+                                        int32_t rows, int32_t group, int32_t& begin, int32_t& end)
+{
+    begin = 0, end = 0;
+    if (row < rows) {
+        end = r.len - a.nQuery + row / group + 1;
+        begin = a.window > 0 && end > a.window ? end - a.window : 0;
+    }
+}
+
+// How the chunks of 16 codes of a token are swapped in LDS, so that 16 tokens
+// read at one chunk fall on all the banks.  Depends on the token modulo 16.
+template <int D>
+__device__ __forceinline__ int swap_of(int r)
+{
+    constexpr int C = D / 16;
+    return C == 8 ? (r >> 1) & 7 : C == 16 ? r & 15 : C == 6 ? (r >> 3) & 1 : (r >> 2) & 3;
+}
+
+// Bytes straight from memory into LDS: lane i's 16 bytes land at dst + 16 i.
+__device__ __forceinline__ void load_lds(const uint8_t* src, uint8_t* dst)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                     (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// The address of one row of queries.
+__device__ __forceinline__ int64_t row_at(const ccbKv8Rows& r, int32_t b, int32_t h, int32_t row,
+                                          int32_t group)
+{
+    return b * r.strideBatch + (row / group) * r.strideToken +
+           (int64_t)(h * group + row % group) * r.strideHead;
+}
+
+// The 8 query values of a row that stand opposite the key's 8 codes in step j.
+template <int D>
+__device__ __forceinline__ int dim_at(int j, int g)
+{
+    return (D % 64 != 0 && j == D / 32 - 1) ? 32 * j + 8 * g : 64 * (j >> 1) + 16 * g + 8 * (j & 1);
+}
+
+template <int F, int T, int D, int NT>
+__global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(Plan p)
+{
+    constexpr int C = D / 16;             // chunks of 16 codes in a token
+    constexpr int NI = kTile * C / 64;    // loads of a wave for a tile of keys
+    constexpr int NB = D / 16;            // blocks of 16 dimensions
+    constexpr int NJ = D / 32;            // steps of the first product
+    // (separate arrays: the compiler then knows which reads a load in flight may touch)
+    __shared__ __attribute__((aligned(16))) uint8_t k0[kWaves][kTile * D], k1[kWaves][kTile * D];
+    __shared__ __attribute__((aligned(16))) uint8_t v0[kWaves][kTile * D], v1[kWaves][kTile * D];
+    __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT], slse[16 * NT];
+
+    const ccb::Kv8AttendArgs& a = p.a;
     const ccbKv8Cache& c = a.c;
     uint32_t rest = blockIdx.x;
-    const int32_t t = (int32_t)(rest % (uint32_t)perRow) * kThreads + (int)threadIdx.x;
-    rest /= (uint32_t)perRow;
-    const int32_t h = rest % (uint32_t)c.heads;
-    const int32_t b = rest / (uint32_t)c.heads;
+    const int32_t split = rest % (uint32_t)p.splits;
+    rest /= (uint32_t)p.splits;
+    const int32_t row0 = (int32_t)(rest % (uint32_t)p.rowBlocks) * (16 * NT);
+    const int32_t pair = rest / (uint32_t)p.rowBlocks;
+    const int32_t h = pair % c.heads, b = pair / c.heads;
     const int32_t P = c.pageSize, group = a.headsQ / c.heads;
-    const int32_t len = checked_len(c.lens[b], c.maxPages * P);
-    if (t >= len) return;
-    const int32_t page = checked_page(c.pageTable[b * c.tableStride + t / P], c.numPages);
-    if (page < 0) return;
-    const int64_t block = (int64_t)page * c.heads + h;
-    const uint8_t* k = (const uint8_t*)c.k + (block * P + t % P) * D;
-    float sum = 0.0f;
-    for (int32_t i = 0; i < a.nQuery; ++i) {
-        const int32_t end = len - a.nQuery + i + 1;
-        if (t >= end || (a.window > 0 && t < end - a.window)) continue;
-        for (int32_t g = 0; g < group; ++g) {
-            const int32_t hq = h * group + g;
-            const uint16_t* q = (const uint16_t*)a.q.data + b * a.q.strideBatch +
-                                i * a.q.strideToken + hq * a.q.strideHead;
-            float s = 0.0f;
-            for (int d = 0; d < D; d += 4) {
-                float x[4];
-                decode4<F>(*(const uint32_t*)(k + d), x);
-                for (int e = 0; e < 4; ++e) s += widen<T>(q[d + e]) * x[e];
-            }
-            s *= c.kScale[block] * a.scale;
-            sum += expf(s - lse[((int64_t)b * a.nQuery + i) * a.headsQ + hq]);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+
+    const Range r = range_of(a, b);
+    const int64_t lo64 = (int64_t)r.base + (int64_t)split * p.chunk;
+    if (p.splits > 1 && lo64 >= r.len) return;  // the join knows
+    const int32_t lo = (int32_t)lo64;
+    const int32_t hi = r.len - lo < p.chunk ? r.len : lo + p.chunk;
+
+    // queries, 8 values of a row per lane and step
+    u4 q[NT][NJ];
+    int32_t begin[NT], end[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int32_t row = row0 + nt * 16 + n;
+        seen_by(a, r, row, p.rows, group, begin[nt], end[nt]);
+        const uint16_t* src = (const uint16_t*)a.q.data + row_at(a.q, b, h, row < p.rows ? row : row0, group);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            q[nt][j] = *(const u4*)(src + dim_at<D>(j, g));
+            if (row >= p.rows) q[nt][j] = u4{0, 0, 0, 0};
         }
     }
-    c.weight[((int64_t)b * c.heads + h) * c.weightStride + t] += sum;
+    // tokens in [allBegin, allEnd) are seen by every row of the workgroup
+    int32_t allBegin, allEnd, unused;
+    {
+        const int32_t last = row0 + 16 * NT < p.rows ? row0 + 16 * NT - 1 : p.rows - 1;
+        seen_by(a, r, last, p.rows, group, allBegin, unused);
+        seen_by(a, r, row0, p.rows, group, unused, allEnd);
+    }
+
+    f4 o[NT][NB];
+    float m[NT], ref[NT], l[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        m[nt] = -INFINITY, ref[nt] = 0.0f, l[nt] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < NB; ++d) o[nt][d] = f4{0, 0, 0, 0};
+    }
+
+    // where this lane's chunks of a tile come from (in bytes, within 16 tokens)
+    int32_t from[NI];
+#pragma unroll
+    for (int it = 0; it < NI; ++it) {
+        const int at = it * 64 + lane, tok = at / C;
+        from[it] = ((tok & 15) * C + ((at % C) ^ swap_of<D>(tok & 15))) * 16;
+    }
+    // where this lane reads keys (its token n) and values (two lanes for a token)
+    const int kAt = n * C * 16, kSwap = swap_of<D>(n);
+    const int vSlot = n >> 1;
+    const int vTok = 4 * g + (vSlot & 3) + (vSlot < 4 ? 0 : 16);
+    const int vAt = vTok * C * 16 + 8 * (lane & 1), vSwap = swap_of<D>(vTok & 15);
+
+    for (int32_t seg = lo; seg < hi; seg += kSegment) {
+        const int32_t segEnd = hi - seg < kSegment ? hi : seg + kSegment;
+        // lane i holds page and scales of the wave's i-th half tile
+        int32_t page = -1;
+        float kf = 0.0f, vf = 0.0f;
+        {
+            const int32_t t = seg + ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
+            if (t < segEnd && t + 16 > r.first) {
+                page = checked_page(c.pageTable[b * c.tableStride + t / P], c.numPages);
+                if (page < 0) {
+                    report(a.err);
+                } else {
+                    const int64_t block = (int64_t)page * c.heads + h;
+                    kf = c.kScale[block] * (a.scale * kLog2e);
+                    vf = c.vScale[block];
+                }
+            }
+        }
+        const int32_t nTiles = ((segEnd - seg + kTile - 1) / kTile - wave + kWaves - 1) / kWaves;
+
+        auto issue = [&](const void* codes, int32_t i, uint8_t* buf) {
+            const int32_t t = seg + (i * kWaves + wave) * kTile;
+            const uint8_t* src[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                int32_t pg = __builtin_amdgcn_readlane(page, 2 * i + half);
+                pg = pg < 0 ? 0 : pg;  // an unseen page's place: page 0 is loaded and not used
+                src[half] = (const uint8_t*)codes +
+                            (((int64_t)pg * c.heads + h) * P + ((t + 16 * half) & (P - 1))) * D;
+            }
+#pragma unroll
+            for (int it = 0; it < NI; ++it) {
+                const uint8_t* s = (it * 64 + 63) / C < 16 ? src[0] : it * 64 / C >= 16 ? src[1]
+                                   : (it * 64 + lane) / C < 16 ? src[0] : src[1];
+                load_lds(s + from[it], buf + it * 1024);
+            }
+        };
+
+        auto step = [&](int32_t i, uint8_t* kb, uint8_t* vb) {
+            const int32_t t0 = seg + (i * kWaves + wave) * kTile;
+            const bool more = i + 1 < nTiles;
+            // scores
+            if (more) wait_loads<3 * NI>(); else wait_loads<NI>();
+            f4 s[NT][2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[nt][half] = f4{0, 0, 0, 0};
+                const uint8_t* row = kb + kAt + half * 16 * C * 16;
+#pragma unroll
+                for (int j = 0; j + 1 < NJ; j += 2) {
+                    const u4 w = *(const u4*)(row + (((2 * j + g) ^ kSwap) * 16));
+                    const u4 x = codes16x8<F, T>(w.x, w.y), y = codes16x8<F, T>(w.z, w.w);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        s[nt][half] = mfma<T>(x, q[nt][j], s[nt][half]);
+                        s[nt][half] = mfma<T>(y, q[nt][j + 1], s[nt][half]);
+                    }
+                }
+                if constexpr (NJ % 2 == 1) {
+                    const uint2 w =
+                        *(const uint2*)(row + (((2 * (NJ - 1) + (g >> 1)) ^ kSwap) * 16 + 8 * (g & 1)));
+                    const u4 x = codes16x8<F, T>(w.x, w.y);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) s[nt][half] = mfma<T>(x, q[nt][NJ - 1], s[nt][half]);
+                }
+            }
+            if (i + 2 < nTiles) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the keys are read
+                issue(c.k, i + 2, kb);
+            }
+            const int32_t pg0 = __builtin_amdgcn_readlane(page, 2 * i);
+            const int32_t pg1 = __builtin_amdgcn_readlane(page, 2 * i + 1);
+            const float kf0 = of_bits(__builtin_amdgcn_readlane(bits(kf), 2 * i));
+            const float kf1 = of_bits(__builtin_amdgcn_readlane(bits(kf), 2 * i + 1));
+            const float vf0 = of_bits(__builtin_amdgcn_readlane(bits(vf), 2 * i));
+            const float vf1 = of_bits(__builtin_amdgcn_readlane(bits(vf), 2 * i + 1));
+            const bool whole = t0 >= allBegin && t0 + kTile <= allEnd && (pg0 | pg1) >= 0;
+            bool grows = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                s[nt][0] *= kf0, s[nt][1] *= kf1;
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int32_t t = t0 + 4 * g + e;
+                        if (!(t >= begin[nt] && t < end[nt] && pg0 >= 0)) s[nt][0][e] = -INFINITY;
+                        if (!(t + 16 >= begin[nt] && t + 16 < end[nt] && pg1 >= 0))
+                            s[nt][1][e] = -INFINITY;
+                    }
+                }
+                if (p.scores != nullptr && n + nt * 16 < p.rows) {
+                    float* dst = p.scores +
+                                 ((int64_t)pair * p.rows + nt * 16 + n) * ((int64_t)p.splits * p.chunk) +
+                                 (t0 - r.base) + 4 * g;
+                    *(f4*)dst = s[nt][0];
+                    *(f4*)(dst + 16) = s[nt][1];
+                }
+                float mx = fmaxf(fmaxf(s[nt][0].x, s[nt][0].y), fmaxf(s[nt][0].z, s[nt][0].w));
+                mx = fmaxf(mx, fmaxf(fmaxf(s[nt][1].x, s[nt][1].y), fmaxf(s[nt][1].z, s[nt][1].w)));
+                grows |= mx > m[nt] + kSlack;
+            }
+            if (__any(grows)) {  // a new maximum, for the row's four lanes alike
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float mx = fmaxf(fmaxf(s[nt][0].x, s[nt][0].y), fmaxf(s[nt][0].z, s[nt][0].w));
+                    mx = fmaxf(mx, fmaxf(fmaxf(s[nt][1].x, s[nt][1].y), fmaxf(s[nt][1].z, s[nt][1].w)));
+                    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+                    mx = fmaxf(m[nt], fmaxf(mx, __shfl_xor(mx, 32, 64)));
+                    ref[nt] = mx == -INFINITY ? 0.0f : mx;
+                    const float f = exp2_(m[nt] - ref[nt]);
+                    m[nt] = mx;
+                    l[nt] *= f;
+#pragma unroll
+                    for (int d = 0; d < NB; ++d) o[nt][d] *= f;
+                }
+            }
+            u4 ph[NT], pl[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    f4 x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = exp2_(s[nt][half][e] - ref[nt]);
+                    l[nt] += (x.x + x.y) + (x.z + x.w);
+                    x *= half ? vf1 : vf0;
+                    uint32_t h0, l0, h1, l1;
+                    pieces(x.x, x.y, h0, l0);
+                    pieces(x.z, x.w, h1, l1);
+                    ph[nt][2 * half] = h0, ph[nt][2 * half + 1] = h1;
+                    pl[nt][2 * half] = l0, pl[nt][2 * half + 1] = l1;
+                }
+            }
+            // values
+            if (i + 2 < nTiles) wait_loads<3 * NI>(); else if (more) wait_loads<2 * NI>(); else wait_loads<0>();
+            uint32_t keep0 = ~0u, keep1 = ~0u;  // e4m3: NaN codes where nothing is held
+            if (F == kE4m3 && !whole) {
+                keep0 = keep1 = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    keep0 |= (pg0 >= 0 && t0 + 4 * g + e < r.len) ? 0xffu << (8 * e) : 0u;
+                    keep1 |= (pg1 >= 0 && t0 + 16 + 4 * g + e < r.len) ? 0xffu << (8 * e) : 0u;
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < NB; ++d) {
+                i2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                    (__attribute__((address_space(3))) i2*)(vb + vAt + ((d ^ vSwap) * 16)));
+                if (F == kE4m3 && !whole) w.x &= keep0, w.y &= keep1;
+                const u4 x = codes16x8<F, CCB_KV8_BF16>(w.x, w.y);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    o[nt][d] = mfma<CCB_KV8_BF16>(x, ph[nt], o[nt][d]);
+                    o[nt][d] = mfma<CCB_KV8_BF16>(x, pl[nt], o[nt][d]);
+                }
+            }
+            if (i + 2 < nTiles) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the values are read
+                issue(c.v, i + 2, vb);
+            }
+        };
+
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last segment's reads
+        if (nTiles > 0) {
+            issue(c.k, 0, k0[wave]);
+            issue(c.v, 0, v0[wave]);
+        }
+        if (nTiles > 1) {
+            issue(c.k, 1, k1[wave]);
+            issue(c.v, 1, v1[wave]);
+        }
+        for (int32_t i = 0; i < nTiles; i += 2) {
+            step(i, k0[wave], v0[wave]);
+            if (i + 1 < nTiles) step(i + 1, k1[wave], v1[wave]);
+        }
+    }
+
+    // join the waves
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        l[nt] += __shfl_xor(l[nt], 16, 64);
+        l[nt] += __shfl_xor(l[nt], 32, 64);
+        if (g == 0) sm[wave][nt * 16 + n] = m[nt], sl[wave][nt * 16 + n] = l[nt];
+    }
+    __syncthreads();
+    const bool direct = p.splits == 1;
+    const int64_t part = ((int64_t)pair * p.splits + split) * p.rows;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][nt * 16 + n]);
+        const float f = l[nt] == 0.0f ? 0.0f : exp2_(m[nt] - top);  // (a NaN stays)
+        // chunks of 4 dimensions are swapped so that rows fall on different banks
+        float* dst = (float*)(wave < 2 ? k0[0] : v0[0]) + ((wave & 1) * 16 + n) * D;
+#pragma unroll
+        for (int d = 0; d < NB; ++d) *(f4*)(dst + (((4 * d + g) ^ (n & 7)) * 4)) = o[nt][d] * f;
+        __syncthreads();
+        for (int32_t at = threadIdx.x; at < 4 * D; at += kThreads) {
+            const int32_t i = at / (D / 4), d4 = at % (D / 4), row = row0 + nt * 16 + i;
+            if (row >= p.rows) continue;
+            f4 sum = {0, 0, 0, 0};
+            float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                sum += *(const f4*)((const float*)(w < 2 ? k0[0] : v0[0]) + ((w & 1) * 16 + i) * D +
+                                    ((d4 ^ (i & 7)) * 4));
+                mm = fmaxf(mm, sm[w][nt * 16 + i]);
+            }
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                ll += sl[w][nt * 16 + i] == 0.0f ? 0.0f : sl[w][nt * 16 + i] * exp2_(sm[w][nt * 16 + i] - mm);
+            if (direct) {
+                uint2 u = make_uint2(0, 0);
+                if (ll != 0.0f) {
+                    u.x = narrow<T>(sum.x / ll) | (narrow<T>(sum.y / ll) << 16);
+                    u.y = narrow<T>(sum.z / ll) | (narrow<T>(sum.w / ll) << 16);
+                }
+                *(uint2*)((uint16_t*)a.out.data + row_at(a.out, b, h, row, group) + d4 * 4) = u;
+                if (d4 == 0) {
+                    const float lse = ll != 0.0f ? mm + log2f(ll) : INFINITY;
+                    slse[nt * 16 + i] = lse;
+                    if (p.lse2 != nullptr) p.lse2[(int64_t)pair * p.rows + row] = lse;
+                    if (a.lse != nullptr)
+                        a.lse[((int64_t)b * a.nQuery + row / group) * a.headsQ + h * group + row % group] =
+                            ll != 0.0f ? lse * kLn2 : -INFINITY;
+                }
+            } else {
+                *(f4*)(p.partO + (part + row) * D + d4 * 4) = sum;
+                if (d4 == 0) p.partML[part + row] = make_float2(mm, ll);
+            }
+        }
+        __syncthreads();
+    }
+    if (direct && p.scores != nullptr) {
+        // this workgroup has all scores of its head: add the weights at once
+        const float* sc = p.scores + (int64_t)pair * p.rows * p.chunk;
+        float* w = c.weight + (int64_t)pair * c.weightStride;
+        for (int32_t t = r.first + (int32_t)threadIdx.x; t < r.len; t += kThreads) {
+            float sum = 0.0f;
+            for (int32_t i = 0; i < p.rows; ++i)
+                sum += exp2_(sc[(int64_t)i * p.chunk + (t - r.base)] - slse[i]);
+            w[t] += sum;
+        }
+    }
+}
+
+// A maximum and sum joined with another (a sum of 0 has no maximum; a NaN stays).
+__device__ __forceinline__ void merge(float& top, float& all, float top2, float all2)
+{
+    const float t = fmaxf(top, top2);
+    const float x = all == 0.0f ? 0.0f : all * exp2_(top - t);
+    const float y = all2 == 0.0f ? 0.0f : all2 * exp2_(top2 - t);
+    top = t;
+    all = x + y;
+}
+
+// Join the runs of a sequence's tokens: out and lse, and the weights from the
+// stored scores.  Workgroup `part` of a (sequence, cache head) takes every
+// joinBlocks-th row and block of tokens.
+template <int T>
+__global__ __launch_bounds__(kThreads) void kv8_k_join(Plan p, int32_t D)
+{
+    __shared__ f4 sum[kThreads];
+    __shared__ float slse[kStoredRows];
+    const ccb::Kv8AttendArgs& a = p.a;
+    const ccbKv8Cache& c = a.c;
+    const int32_t part = blockIdx.x % (uint32_t)p.joinBlocks, pair = blockIdx.x / (uint32_t)p.joinBlocks;
+    const int32_t h = pair % c.heads, b = pair / c.heads, group = a.headsQ / c.heads;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const Range r = range_of(a, b);
+    const int32_t n = (r.len - r.base + p.chunk - 1) / p.chunk;  // runs that hold tokens
+    const float2* ml = p.partML + (int64_t)pair * p.splits * p.rows;
+
+    // maximum and sum of a row over the runs, by one wave
+    auto totals = [&](int32_t row, float& top, float& all) {
+        top = -INFINITY, all = 0.0f;
+        for (int32_t s = lane; s < n; s += 64) {
+            const float2 x = ml[(int64_t)s * p.rows + row];
+            merge(top, all, x.x, x.y);
+        }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) {
+            const float om = __shfl_xor(top, d, 64), ol = __shfl_xor(all, d, 64);
+            merge(top, all, om, ol);
+        }
+    };
+
+    const int32_t V = D / 4, groups = kThreads / V;  // vectors of a row, runs summed side by side
+    const int32_t d4 = threadIdx.x % V, sg = threadIdx.x / V;
+    for (int32_t row = part; row < p.rows; row += p.joinBlocks) {
+        float top, all;
+        totals(row, top, all);
+        f4 o = {0, 0, 0, 0};
+        if (sg < groups)
+            for (int32_t s = sg; s < n; s += groups) {
+                const int64_t at = ((int64_t)pair * p.splits + s) * p.rows + row;
+                const float2 x = p.partML[at];
+                const float f = x.y == 0.0f ? 0.0f : exp2_(x.x - top);
+                o += *(const f4*)(p.partO + at * D + d4 * 4) * f;
+            }
+        sum[threadIdx.x] = o;
+        __syncthreads();
+        if ((int32_t)threadIdx.x < V) {
+            for (int32_t i = 1; i < groups; ++i) o += sum[i * V + d4];
+            uint2 u = make_uint2(0, 0);
+            if (all != 0.0f) {
+                u.x = narrow<T>(o.x / all) | (narrow<T>(o.y / all) << 16);
+                u.y = narrow<T>(o.z / all) | (narrow<T>(o.w / all) << 16);
+            }
+            *(uint2*)((uint16_t*)a.out.data + row_at(a.out, b, h, row, group) + d4 * 4) = u;
+            if (threadIdx.x == 0) {
+                const float lse = all != 0.0f ? top + log2f(all) : INFINITY;
+                if (p.lse2 != nullptr) p.lse2[(int64_t)pair * p.rows + row] = lse;
+                if (a.lse != nullptr)
+                    a.lse[((int64_t)b * a.nQuery + row / group) * a.headsQ + h * group + row % group] =
+                        all != 0.0f ? lse * kLn2 : -INFINITY;
+            }
+        }
+        __syncthreads();
+    }
+    if (p.scores == nullptr || r.base + part * kJoinTokens >= r.len) return;
+    for (int32_t row = wave; row < p.rows; row += kWaves) {
+        float top, all;
+        totals(row, top, all);
+        if (lane == 0) slse[row] = all != 0.0f ? top + log2f(all) : INFINITY;
+    }
+    __syncthreads();
+    const int64_t stride = (int64_t)p.splits * p.chunk;
+    const float* sc = p.scores + (int64_t)pair * p.rows * stride;
+    float* w = c.weight + (int64_t)pair * c.weightStride;
+    for (int64_t from = (int64_t)r.base + part * kJoinTokens; from < r.len;
+         from += (int64_t)p.joinBlocks * kJoinTokens) {
+        const int32_t t = (int32_t)from + 4 * (int32_t)threadIdx.x;
+        if (t >= r.len) break;
+        f4 x = {0, 0, 0, 0};
+        for (int32_t i = 0; i < p.rows; ++i) {
+            const f4 s = *(const f4*)(sc + i * stride + (t - r.base));
+            const float lse = slse[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] += exp2_(s[e] - lse);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (t + e >= r.first && t + e < r.len) w[t + e] += x[e];
+    }
+}
+
+// Weights of many rows: the scores again, S = Q K^T so that a token's rows lie
+// on one lane index.  One wave takes 32 tokens and goes over all rows.
+template <int F, int T, int D>
+__global__ __launch_bounds__(kThreads) void kv8_k_weights(Plan p, int32_t blocks)
+{
+    constexpr int NJ = D / 32;
+    const ccb::Kv8AttendArgs& a = p.a;
+    const ccbKv8Cache& c = a.c;
+    const int32_t pair = blockIdx.x / (uint32_t)blocks;
+    const int32_t h = pair % c.heads, b = pair / c.heads;
+    const int32_t P = c.pageSize, group = a.headsQ / c.heads;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = lane & 15, g = lane >> 4;
+    const Range r = range_of(a, b);
+    for (int64_t from = (int64_t)r.base + ((int64_t)(blockIdx.x % (uint32_t)blocks) * kWaves + wave) * kTile;
+         from < r.len; from += (int64_t)blocks * kWaves * kTile) {
+        u4 k[2][NJ];
+        float kf[2];
+        bool held[2];
+        int32_t tok[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int32_t t = tok[half] = (int32_t)from + 16 * half + n;
+            const int32_t page = t < r.len && t >= r.first
+                                     ? checked_page(c.pageTable[b * c.tableStride + t / P], c.numPages)
+                                     : -1;
+            held[half] = page >= 0;
+            const int64_t block = (int64_t)(page < 0 ? 0 : page) * c.heads + h;
+            kf[half] = held[half] ? c.kScale[block] * (a.scale * kLog2e) : 0.0f;
+            const uint8_t* src = (const uint8_t*)c.k + (block * P + (t & (P - 1))) * D;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const uint2 w = *(const uint2*)(src + 32 * j + 8 * g);
+                k[half][j] = codes16x8<F, T>(w.x, w.y);
+            }
+        }
+        float sum[2] = {0.0f, 0.0f};
+        for (int32_t row0 = 0; row0 < p.rows; row0 += 16) {
+            const int32_t row = row0 + n;
+            const uint16_t* src =
+                (const uint16_t*)a.q.data + row_at(a.q, b, h, row < p.rows ? row : row0, group);
+            f4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const u4 q = *(const u4*)(src + 32 * j + 8 * g);
+                s[0] = mfma<T>(q, k[0][j], s[0]);
+                s[1] = mfma<T>(q, k[1][j], s[1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                int32_t begin, end;
+                seen_by(a, r, row0 + 4 * g + e, p.rows, group, begin, end);
+                const float lse = end > begin ? p.lse2[(int64_t)pair * p.rows + row0 + 4 * g + e] : INFINITY;
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    if (held[half] && tok[half] >= begin && tok[half] < end)
+                        sum[half] += exp2_(s[half][e] * kf[half] - lse);
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            sum[half] += __shfl_xor(sum[half], 16, 64);
+            sum[half] += __shfl_xor(sum[half], 32, 64);
+            if (g == 0 && held[half])
+                c.weight[(int64_t)pair * c.weightStride + tok[half]] += sum[half];
+        }
+    }
+}
+
+// How a call is split, and where its workspace's parts lie; returns its bytes,
+// which do not depend on the window.
+size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, int32_t window,
+                 int32_t accumulate, void* ws)
+{
+    const int64_t pairs = (int64_t)c.batch * c.heads;
+    const int64_t rows = (int64_t)nQuery * (headsQ / c.heads);
+    p.rows = (int32_t)rows;
+    p.tilesN = rows <= 16 ? 1 : (rows <= 32 || c.headDim > 128) ? 2 : 4;
+    p.rowBlocks = (int32_t)((rows + 16 * p.tilesN - 1) / (16 * p.tilesN));
+    // tokens that a sequence's queries may see, from a tile's border
+    const int64_t room = (int64_t)c.maxPages * c.pageSize;
+    int64_t span = room;
+    if (window > 0 && (int64_t)window + nQuery - 1 + kTile < span)
+        span = (int64_t)window + nQuery - 1 + kTile;
+    constexpr int64_t unit = kWaves * kTile;
+    constexpr int64_t target = 2048;  // workgroups
+    auto up = [](int64_t x, int64_t by) { return (x + by - 1) / by; };
+    int64_t most = target / (pairs * p.rowBlocks);
+    if (most < 1) most = 1;
+    p.chunk = (int32_t)(up(up(span, most), unit) * unit);
+    if (span <= 256) p.chunk = (int32_t)(up(span, unit) * unit);
+    p.splits = (int32_t)up(span, p.chunk);
+    const int64_t mostSplits = most < up(room, unit) ? most : up(room, unit);
+    const int64_t mostTokens = room + up(room, most) + unit;  // >= splits * chunk
+    size_t bytes = 0;
+    auto take = [&](int64_t n, size_t each) {
+        char* here = (char*)ws + bytes;
+        bytes += ((size_t)n * each + 127) / 128 * 128;
+        return here;
+    };
+    const int64_t parts = mostSplits > 1 ? pairs * mostSplits * rows : 0;
+    p.partO = (float*)take(parts * c.headDim, sizeof(float));
+    p.partML = (float2*)take(parts, sizeof(float2));
+    p.scores = nullptr, p.lse2 = nullptr;
+    if (accumulate && rows <= kStoredRows)
+        p.scores = (float*)take(pairs * rows * (mostTokens / 4 + 1), 4 * sizeof(float));
+    else if (accumulate)
+        p.lse2 = (float*)take(pairs * rows, sizeof(float));
+    const int64_t byTokens = p.scores != nullptr ? up((int64_t)p.splits * p.chunk, kJoinTokens) : 1;
+    const int64_t byRows = rows < 64 ? rows : 64;
+    p.joinBlocks = (int32_t)(byTokens > byRows ? byTokens : byRows);
+    return bytes;
+}
+
+template <int F, int T, int D>
+hipError_t launch(const Plan& p, int64_t blocks, hipStream_t s)
+{
+    const dim3 grid((unsigned)blocks), block(kThreads);
+    if (p.tilesN == 1)
+        kv8_k_attend<F, T, D, 1><<<grid, block, 0, s>>>(p);
+    else if (p.tilesN == 2)
+        kv8_k_attend<F, T, D, 2><<<grid, block, 0, s>>>(p);
+    else if constexpr (D <= 128)
+        kv8_k_attend<F, T, D, 4><<<grid, block, 0, s>>>(p);
+    const int64_t pairs = (int64_t)p.a.c.batch * p.a.c.heads;
+    if (p.splits > 1)
+        kv8_k_join<T><<<dim3((unsigned)(pairs * p.joinBlocks)), block, 0, s>>>(p, D);
+    if (p.lse2 != nullptr) {
+        const int64_t span = (int64_t)p.splits * p.chunk;
+        int64_t each = (span + kWaves * kTile - 1) / (kWaves * kTile);
+        const int64_t most = pairs < 4096 ? 8192 / pairs : 2;
+        each = each < most ? each : most;
+        kv8_k_weights<F, T, D><<<dim3((unsigned)(pairs * each)), block, 0, s>>>(p, (int32_t)each);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -150,46 +759,34 @@ namespace ccb {
 
 size_t kv8_attend_bytes(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, int32_t accumulate)
 {
-    (void)accumulate;
-    return (size_t)c.batch * headsQ * nQuery * sizeof(float);
+    Plan p;
+    return make_plan(p, c, headsQ, nQuery, 0, accumulate, nullptr);
 }
 
 hipError_t kv8_attend(const Kv8AttendArgs& a, int numCUs, hipStream_t s)
 {
     (void)numCUs;
     const ccbKv8Cache& c = a.c;
-    float* lse = (float*)a.ws;
-    const int64_t rows = (int64_t)c.batch * a.nQuery * a.headsQ;
-    const int32_t perRow = (c.maxPages * c.pageSize + kThreads - 1) / kThreads;
-    const int64_t blocks = (int64_t)c.batch * c.heads * perRow;
-    if (rows > INT32_MAX || blocks > INT32_MAX) return hipErrorInvalidValue;
-#define KV8_PLAIN(F, T, D) \
-    kv8_k_attend_plain<F, T, D><<<dim3((unsigned)rows), dim3(kThreads), 0, s>>>(a, lse); \
-    if (a.accumulate) \
-        kv8_k_weights_plain<F, T, D><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(a, lse, perRow); \
-    break;
-#define KV8_PLAIN_DIM(F, T) \
+    Plan p;
+    p.a = a;
+    make_plan(p, c, a.headsQ, a.nQuery, a.window, a.accumulate, a.ws);
+    const int64_t pairs = (int64_t)c.batch * c.heads;
+    const int64_t blocks = pairs * p.rowBlocks * p.splits;
+    if (blocks > INT32_MAX || pairs * p.joinBlocks > INT32_MAX) return hipErrorInvalidValue;
+#define KV8_ATTEND_DIM(F, T) \
     switch (c.headDim) { \
-    case 64: KV8_PLAIN(F, T, 64) \
-    case 96: KV8_PLAIN(F, T, 96) \
-    case 128: KV8_PLAIN(F, T, 128) \
-    case 192: KV8_PLAIN(F, T, 192) \
-    default: KV8_PLAIN(F, T, 256) \
+    case 64: return launch<F, T, 64>(p, blocks, s); \
+    case 96: return launch<F, T, 96>(p, blocks, s); \
+    case 128: return launch<F, T, 128>(p, blocks, s); \
+    case 192: return launch<F, T, 192>(p, blocks, s); \
+    default: return launch<F, T, 256>(p, blocks, s); \
     }
     if (c.format == CCB_KV8_INT8) {
-        if (a.q.type == CCB_KV8_BF16) {
-            KV8_PLAIN_DIM(kInt8, CCB_KV8_BF16)
-        } else {
-            KV8_PLAIN_DIM(kInt8, CCB_KV8_FP16)
-        }
-    } else {
-        if (a.q.type == CCB_KV8_BF16) {
-            KV8_PLAIN_DIM(kE4m3, CCB_KV8_BF16)
-        } else {
-            KV8_PLAIN_DIM(kE4m3, CCB_KV8_FP16)
-        }
+        if (a.q.type == CCB_KV8_BF16) KV8_ATTEND_DIM(kInt8, CCB_KV8_BF16)
+        KV8_ATTEND_DIM(kInt8, CCB_KV8_FP16)
     }
-    return hipGetLastError();
+    if (a.q.type == CCB_KV8_BF16) KV8_ATTEND_DIM(kE4m3, CCB_KV8_BF16)
+    KV8_ATTEND_DIM(kE4m3, CCB_KV8_FP16)
 }
 
 }  // namespace ccb

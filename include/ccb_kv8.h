@@ -120,8 +120,8 @@ CCB_API ccbStatus ccb_kv8_append(const ccbKv8Cache* cache, const ccbKv8Rows* kNe
  *           zeroed by the caller before its first use; every call leaves it
  *           ready for the next.  Calls that overlap in time need their own.
  * Errors: NULL_POINTER (also accumulate without weight), INVALID_VALUE (as
- * above; headsQ not a multiple of heads, nQuery or window < 0, a scale that is not
- * finite, a workspace too small), UNSUPPORTED_DEVICE, HIP. */
+ * above; headsQ not a multiple of heads, nQuery or window < 0, more than 2^20 rows
+ * (headsQ / heads * nQuery), a scale that is not finite, a workspace too small), UNSUPPORTED_DEVICE, HIP. */
 CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
                                  const ccbKv8Rows* out, float* lse, int32_t headsQ, int32_t nQuery,
                                  float scale, int32_t window, int32_t accumulate, void* ws,
