@@ -5,8 +5,11 @@
 // and value, so one workgroup takes a (sequence, cache head, run of tokens)
 // and up to 16 * NT rows.  Its four waves take 32-token tiles in turn and
 // never wait for one another in the loop: a wave streams its own tiles into
-// its own part of LDS (16 bytes per lane, straight from memory, two tiles
-// ahead) and keeps its own running maximum, sum and weighted values.
+// its own part of LDS (16 bytes per lane, straight from memory; the next
+// tile's keys are on their way as soon as this one's are read, and its values
+// likewise) and keeps its own running maximum, sum and weighted values.  Rings
+// of two tiles leave room for two workgroups on a CU instead of four and
+// measured slower: 32 against 24 us for 16 sequences of up to 4096 tokens.
 //
 // S^T = K Q^T and O^T = V^T P^T on 16x16x32 tiles.  In that order a row of
 // scores lies on one lane index (lane % 16), so the softmax needs no
@@ -53,12 +56,14 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 struct Plan {
     ccb::Kv8AttendArgs a;
+    int32_t pairs;      // (sequence, cache head)
     int32_t rows;       // of a cache head
     int32_t tilesN;     // NT
     int32_t rowBlocks;  // workgroups that share a run of tokens
     int32_t chunk;      // tokens of a workgroup, a multiple of kWaves * kTile
     int32_t splits;     // runs a sequence may have
-    int32_t joinBlocks;
+    int32_t joinRows;   // workgroups of the join for a pair's rows
+    int32_t joinTokens; // and for its tokens
     float* partO;   // [pair][split][row][D]
     float2* partML; // [pair][split][row]: maximum (base 2) and sum
     float* scores;  // [pair][row][splits * chunk] (base 2), or null
@@ -200,18 +205,19 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
     constexpr int NI = kTile * C / 64;    // loads of a wave for a tile of keys
     constexpr int NB = D / 16;            // blocks of 16 dimensions
     constexpr int NJ = D / 32;            // steps of the first product
-    // (separate arrays: the compiler then knows which reads a load in flight may touch)
-    __shared__ __attribute__((aligned(16))) uint8_t k0[kWaves][kTile * D], k1[kWaves][kTile * D];
-    __shared__ __attribute__((aligned(16))) uint8_t v0[kWaves][kTile * D], v1[kWaves][kTile * D];
+    __shared__ __attribute__((aligned(16))) uint8_t kBuf[kWaves][kTile * D];
+    __shared__ __attribute__((aligned(16))) uint8_t vBuf[kWaves][kTile * D];
     __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT], slse[16 * NT];
 
     const ccb::Kv8AttendArgs& a = p.a;
     const ccbKv8Cache& c = a.c;
+    // Neighbouring workgroups, which go to different XCDs, take neighbouring
+    // heads of one run: runs past short sequences' ends cost every XCD alike.
     uint32_t rest = blockIdx.x;
-    const int32_t split = rest % (uint32_t)p.splits;
-    rest /= (uint32_t)p.splits;
+    const int32_t pair = rest % (uint32_t)p.pairs;
+    rest /= (uint32_t)p.pairs;
     const int32_t row0 = (int32_t)(rest % (uint32_t)p.rowBlocks) * (16 * NT);
-    const int32_t pair = rest / (uint32_t)p.rowBlocks;
+    const int32_t split = rest / (uint32_t)p.rowBlocks;
     const int32_t h = pair % c.heads, b = pair / c.heads;
     const int32_t P = c.pageSize, group = a.headsQ / c.heads;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -309,7 +315,7 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
             const int32_t t0 = seg + (i * kWaves + wave) * kTile;
             const bool more = i + 1 < nTiles;
             // scores
-            if (more) wait_loads<3 * NI>(); else wait_loads<NI>();
+            wait_loads<NI>();
             f4 s[NT][2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -334,9 +340,9 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
                     for (int nt = 0; nt < NT; ++nt) s[nt][half] = mfma<T>(x, q[nt][NJ - 1], s[nt][half]);
                 }
             }
-            if (i + 2 < nTiles) {
+            if (more) {
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the keys are read
-                issue(c.k, i + 2, kb);
+                issue(c.k, i + 1, kb);
             }
             const int32_t pg0 = __builtin_amdgcn_readlane(page, 2 * i);
             const int32_t pg1 = __builtin_amdgcn_readlane(page, 2 * i + 1);
@@ -402,7 +408,7 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
                 }
             }
             // values
-            if (i + 2 < nTiles) wait_loads<3 * NI>(); else if (more) wait_loads<2 * NI>(); else wait_loads<0>();
+            if (more) wait_loads<NI>(); else wait_loads<0>();
             uint32_t keep0 = ~0u, keep1 = ~0u;  // e4m3: NaN codes where nothing is held
             if (F == kE4m3 && !whole) {
                 keep0 = keep1 = 0;
@@ -424,25 +430,18 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
                     o[nt][d] = mfma<CCB_KV8_BF16>(x, pl[nt], o[nt][d]);
                 }
             }
-            if (i + 2 < nTiles) {
+            if (more) {
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the values are read
-                issue(c.v, i + 2, vb);
+                issue(c.v, i + 1, vb);
             }
         };
 
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last segment's reads
         if (nTiles > 0) {
-            issue(c.k, 0, k0[wave]);
-            issue(c.v, 0, v0[wave]);
+            issue(c.k, 0, kBuf[wave]);
+            issue(c.v, 0, vBuf[wave]);
         }
-        if (nTiles > 1) {
-            issue(c.k, 1, k1[wave]);
-            issue(c.v, 1, v1[wave]);
-        }
-        for (int32_t i = 0; i < nTiles; i += 2) {
-            step(i, k0[wave], v0[wave]);
-            if (i + 1 < nTiles) step(i + 1, k1[wave], v1[wave]);
-        }
+        for (int32_t i = 0; i < nTiles; ++i) step(i, kBuf[wave], vBuf[wave]);
     }
 
     // join the waves
@@ -462,7 +461,7 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
         for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][nt * 16 + n]);
         const float f = l[nt] == 0.0f ? 0.0f : exp2_(m[nt] - top);  // (a NaN stays)
         // chunks of 4 dimensions are swapped so that rows fall on different banks
-        float* dst = (float*)(wave < 2 ? k0[0] : v0[0]) + ((wave & 1) * 16 + n) * D;
+        float* dst = (float*)(wave < 2 ? kBuf[0] : vBuf[0]) + ((wave & 1) * 16 + n) * D;
 #pragma unroll
         for (int d = 0; d < NB; ++d) *(f4*)(dst + (((4 * d + g) ^ (n & 7)) * 4)) = o[nt][d] * f;
         __syncthreads();
@@ -473,7 +472,7 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
             float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                sum += *(const f4*)((const float*)(w < 2 ? k0[0] : v0[0]) + ((w & 1) * 16 + i) * D +
+                sum += *(const f4*)((const float*)(w < 2 ? kBuf[0] : vBuf[0]) + ((w & 1) * 16 + i) * D +
                                     ((d4 ^ (i & 7)) * 4));
                 mm = fmaxf(mm, sm[w][nt * 16 + i]);
             }
@@ -525,95 +524,119 @@ __device__ __forceinline__ void merge(float& top, float& all, float top2, float 
     all = x + y;
 }
 
-// Join the runs of a sequence's tokens: out and lse, and the weights from the
-// stored scores.  Workgroup `part` of a (sequence, cache head) takes every
-// joinBlocks-th row and block of tokens.
+// Join the runs of a sequence's tokens.  A (sequence, cache head) has joinRows
+// workgroups that take its rows in turn (out and lse) and joinTokens that take
+// its tokens (weights, from the stored scores).
 template <int T>
 __global__ __launch_bounds__(kThreads) void kv8_k_join(Plan p, int32_t D)
 {
     __shared__ f4 sum[kThreads];
-    __shared__ float slse[kStoredRows];
+    __shared__ float factor[kThreads];
+    __shared__ float wm[kWaves], wl[kWaves];
     const ccb::Kv8AttendArgs& a = p.a;
     const ccbKv8Cache& c = a.c;
-    const int32_t part = blockIdx.x % (uint32_t)p.joinBlocks, pair = blockIdx.x / (uint32_t)p.joinBlocks;
+    const int32_t pair = blockIdx.x % (uint32_t)p.pairs;
+    const int32_t part = blockIdx.x / (uint32_t)p.pairs;
     const int32_t h = pair % c.heads, b = pair / c.heads, group = a.headsQ / c.heads;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int tid = threadIdx.x;
     const Range r = range_of(a, b);
     const int32_t n = (r.len - r.base + p.chunk - 1) / p.chunk;  // runs that hold tokens
     const float2* ml = p.partML + (int64_t)pair * p.splits * p.rows;
 
-    // maximum and sum of a row over the runs, by one wave
-    auto totals = [&](int32_t row, float& top, float& all) {
-        top = -INFINITY, all = 0.0f;
-        for (int32_t s = lane; s < n; s += 64) {
-            const float2 x = ml[(int64_t)s * p.rows + row];
-            merge(top, all, x.x, x.y);
+    if (part < p.joinRows) {
+        const int32_t V = D / 4, groups = kThreads / V;  // vectors of a row, runs summed side by side
+        const int32_t d4 = tid % V, sg = tid / V;
+        for (int32_t row = part; row < p.rows; row += p.joinRows) {
+            float top = -INFINITY, all = 0.0f;
+            for (int32_t s = tid; s < n; s += kThreads) {
+                const float2 x = ml[(int64_t)s * p.rows + row];
+                merge(top, all, x.x, x.y);
+            }
+#pragma unroll
+            for (int d = 32; d >= 1; d >>= 1)
+                merge(top, all, __shfl_xor(top, d, 64), __shfl_xor(all, d, 64));
+            if ((tid & 63) == 0) wm[tid >> 6] = top, wl[tid >> 6] = all;
+            __syncthreads();
+            top = wm[0], all = wl[0];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) merge(top, all, wm[w], wl[w]);
+            f4 o = {0, 0, 0, 0};
+            for (int32_t s0 = 0; s0 < n; s0 += kThreads) {
+                const int32_t mine = s0 + tid;
+                const float2 x = mine < n ? ml[(int64_t)mine * p.rows + row] : make_float2(0.0f, 0.0f);
+                factor[tid] = x.y == 0.0f ? 0.0f : exp2_(x.x - top);
+                __syncthreads();
+                const int32_t here = n - s0 < kThreads ? n - s0 : kThreads;
+                const float* src = p.partO + (((int64_t)pair * p.splits + s0) * p.rows + row) * D + d4 * 4;
+                const int64_t step = (int64_t)p.rows * D;
+                if (sg < groups) {
+                    int32_t s = sg;
+                    for (; s + 7 * groups < here; s += 8 * groups) {  // 8 loads in flight
+                        f4 v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = *(const f4*)(src + (s + i * groups) * step);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o += v[i] * factor[s + i * groups];
+                    }
+                    for (; s < here; s += groups) o += *(const f4*)(src + s * step) * factor[s];
+                }
+                __syncthreads();
+            }
+            sum[tid] = o;
+            __syncthreads();
+            if (tid < V) {
+                for (int32_t i = 1; i < groups; ++i) o += sum[i * V + d4];
+                uint2 u = make_uint2(0, 0);
+                if (all != 0.0f) {
+                    u.x = narrow<T>(o.x / all) | (narrow<T>(o.y / all) << 16);
+                    u.y = narrow<T>(o.z / all) | (narrow<T>(o.w / all) << 16);
+                }
+                *(uint2*)((uint16_t*)a.out.data + row_at(a.out, b, h, row, group) + d4 * 4) = u;
+                if (tid == 0) {
+                    const float lse = all != 0.0f ? top + log2f(all) : INFINITY;
+                    if (p.lse2 != nullptr) p.lse2[(int64_t)pair * p.rows + row] = lse;
+                    if (a.lse != nullptr)
+                        a.lse[((int64_t)b * a.nQuery + row / group) * a.headsQ + h * group + row % group] =
+                            all != 0.0f ? lse * kLn2 : -INFINITY;
+                }
+            }
+            __syncthreads();
+        }
+        return;
+    }
+    const int32_t from = (part - p.joinRows) * kJoinTokens;  // from base
+    if (r.base + (int64_t)from >= r.len) return;
+    // every row's lse, by 16 threads each
+    {
+        const int32_t row = tid >> 4;
+        float top = -INFINITY, all = 0.0f;
+        if (row < p.rows) {
+#pragma unroll 8
+            for (int32_t s = tid & 15; s < n; s += 16) {
+                const float2 x = ml[(int64_t)s * p.rows + row];
+                merge(top, all, x.x, x.y);
+            }
         }
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) {
-            const float om = __shfl_xor(top, d, 64), ol = __shfl_xor(all, d, 64);
-            merge(top, all, om, ol);
-        }
-    };
-
-    const int32_t V = D / 4, groups = kThreads / V;  // vectors of a row, runs summed side by side
-    const int32_t d4 = threadIdx.x % V, sg = threadIdx.x / V;
-    for (int32_t row = part; row < p.rows; row += p.joinBlocks) {
-        float top, all;
-        totals(row, top, all);
-        f4 o = {0, 0, 0, 0};
-        if (sg < groups)
-            for (int32_t s = sg; s < n; s += groups) {
-                const int64_t at = ((int64_t)pair * p.splits + s) * p.rows + row;
-                const float2 x = p.partML[at];
-                const float f = x.y == 0.0f ? 0.0f : exp2_(x.x - top);
-                o += *(const f4*)(p.partO + at * D + d4 * 4) * f;
-            }
-        sum[threadIdx.x] = o;
-        __syncthreads();
-        if ((int32_t)threadIdx.x < V) {
-            for (int32_t i = 1; i < groups; ++i) o += sum[i * V + d4];
-            uint2 u = make_uint2(0, 0);
-            if (all != 0.0f) {
-                u.x = narrow<T>(o.x / all) | (narrow<T>(o.y / all) << 16);
-                u.y = narrow<T>(o.z / all) | (narrow<T>(o.w / all) << 16);
-            }
-            *(uint2*)((uint16_t*)a.out.data + row_at(a.out, b, h, row, group) + d4 * 4) = u;
-            if (threadIdx.x == 0) {
-                const float lse = all != 0.0f ? top + log2f(all) : INFINITY;
-                if (p.lse2 != nullptr) p.lse2[(int64_t)pair * p.rows + row] = lse;
-                if (a.lse != nullptr)
-                    a.lse[((int64_t)b * a.nQuery + row / group) * a.headsQ + h * group + row % group] =
-                        all != 0.0f ? lse * kLn2 : -INFINITY;
-            }
-        }
-        __syncthreads();
-    }
-    if (p.scores == nullptr || r.base + part * kJoinTokens >= r.len) return;
-    for (int32_t row = wave; row < p.rows; row += kWaves) {
-        float top, all;
-        totals(row, top, all);
-        if (lane == 0) slse[row] = all != 0.0f ? top + log2f(all) : INFINITY;
+        for (int d = 8; d >= 1; d >>= 1) merge(top, all, __shfl_xor(top, d, 64), __shfl_xor(all, d, 64));
+        if ((tid & 15) == 0) factor[row] = all != 0.0f ? top + log2f(all) : INFINITY;
     }
     __syncthreads();
     const int64_t stride = (int64_t)p.splits * p.chunk;
-    const float* sc = p.scores + (int64_t)pair * p.rows * stride;
+    const int32_t t = r.base + from + 4 * tid;
+    if (t >= r.len) return;
+    const float* sc = p.scores + (int64_t)pair * p.rows * stride + from + 4 * tid;
     float* w = c.weight + (int64_t)pair * c.weightStride;
-    for (int64_t from = (int64_t)r.base + part * kJoinTokens; from < r.len;
-         from += (int64_t)p.joinBlocks * kJoinTokens) {
-        const int32_t t = (int32_t)from + 4 * (int32_t)threadIdx.x;
-        if (t >= r.len) break;
-        f4 x = {0, 0, 0, 0};
-        for (int32_t i = 0; i < p.rows; ++i) {
-            const f4 s = *(const f4*)(sc + i * stride + (t - r.base));
-            const float lse = slse[i];
+    f4 x = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int32_t i = 0; i < p.rows; ++i) {
+        const f4 s = *(const f4*)(sc + i * stride);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] += exp2_(s[e] - lse);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (t + e >= r.first && t + e < r.len) w[t + e] += x[e];
+        for (int e = 0; e < 4; ++e) x[e] += exp2_(s[e] - factor[i]);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (t + e >= r.first && t + e < r.len) w[t + e] += x[e];
 }
 
 // Weights of many rows: the scores again, S = Q K^T so that a token's rows lie
@@ -624,13 +647,13 @@ __global__ __launch_bounds__(kThreads) void kv8_k_weights(Plan p, int32_t blocks
     constexpr int NJ = D / 32;
     const ccb::Kv8AttendArgs& a = p.a;
     const ccbKv8Cache& c = a.c;
-    const int32_t pair = blockIdx.x / (uint32_t)blocks;
+    const int32_t pair = blockIdx.x % (uint32_t)p.pairs, part = blockIdx.x / (uint32_t)p.pairs;
     const int32_t h = pair % c.heads, b = pair / c.heads;
     const int32_t P = c.pageSize, group = a.headsQ / c.heads;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int n = lane & 15, g = lane >> 4;
     const Range r = range_of(a, b);
-    for (int64_t from = (int64_t)r.base + ((int64_t)(blockIdx.x % (uint32_t)blocks) * kWaves + wave) * kTile;
+    for (int64_t from = (int64_t)r.base + ((int64_t)part * kWaves + wave) * kTile;
          from < r.len; from += (int64_t)blocks * kWaves * kTile) {
         u4 k[2][NJ];
         float kf[2];
@@ -692,6 +715,7 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
 {
     const int64_t pairs = (int64_t)c.batch * c.heads;
     const int64_t rows = (int64_t)nQuery * (headsQ / c.heads);
+    p.pairs = (int32_t)pairs;
     p.rows = (int32_t)rows;
     p.tilesN = rows <= 16 ? 1 : (rows <= 32 || c.headDim > 128) ? 2 : 4;
     p.rowBlocks = (int32_t)((rows + 16 * p.tilesN - 1) / (16 * p.tilesN));
@@ -701,7 +725,7 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
     if (window > 0 && (int64_t)window + nQuery - 1 + kTile < span)
         span = (int64_t)window + nQuery - 1 + kTile;
     constexpr int64_t unit = kWaves * kTile;
-    constexpr int64_t target = 2048;  // workgroups
+    constexpr int64_t target = 1024;  // workgroups: four on a CU at head size 128
     auto up = [](int64_t x, int64_t by) { return (x + by - 1) / by; };
     int64_t most = target / (pairs * p.rowBlocks);
     if (most < 1) most = 1;
@@ -724,9 +748,8 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
         p.scores = (float*)take(pairs * rows * (mostTokens / 4 + 1), 4 * sizeof(float));
     else if (accumulate)
         p.lse2 = (float*)take(pairs * rows, sizeof(float));
-    const int64_t byTokens = p.scores != nullptr ? up((int64_t)p.splits * p.chunk, kJoinTokens) : 1;
-    const int64_t byRows = rows < 64 ? rows : 64;
-    p.joinBlocks = (int32_t)(byTokens > byRows ? byTokens : byRows);
+    p.joinRows = (int32_t)(rows < 64 ? rows : 64);
+    p.joinTokens = p.scores != nullptr ? (int32_t)up((int64_t)p.splits * p.chunk, kJoinTokens) : 0;
     return bytes;
 }
 
@@ -742,7 +765,7 @@ hipError_t launch(const Plan& p, int64_t blocks, hipStream_t s)
         kv8_k_attend<F, T, D, 4><<<grid, block, 0, s>>>(p);
     const int64_t pairs = (int64_t)p.a.c.batch * p.a.c.heads;
     if (p.splits > 1)
-        kv8_k_join<T><<<dim3((unsigned)(pairs * p.joinBlocks)), block, 0, s>>>(p, D);
+        kv8_k_join<T><<<dim3((unsigned)(pairs * (p.joinRows + p.joinTokens))), block, 0, s>>>(p, D);
     if (p.lse2 != nullptr) {
         const int64_t span = (int64_t)p.splits * p.chunk;
         int64_t each = (span + kWaves * kTile - 1) / (kWaves * kTile);
@@ -772,7 +795,7 @@ hipError_t kv8_attend(const Kv8AttendArgs& a, int numCUs, hipStream_t s)
     make_plan(p, c, a.headsQ, a.nQuery, a.window, a.accumulate, a.ws);
     const int64_t pairs = (int64_t)c.batch * c.heads;
     const int64_t blocks = pairs * p.rowBlocks * p.splits;
-    if (blocks > INT32_MAX || pairs * p.joinBlocks > INT32_MAX) return hipErrorInvalidValue;
+    if (blocks > INT32_MAX || pairs * (p.joinRows + (int64_t)p.joinTokens) > INT32_MAX) return hipErrorInvalidValue;
 #define KV8_ATTEND_DIM(F, T) \
     switch (c.headDim) { \
     case 64: return launch<F, T, 64>(p, blocks, s); \
