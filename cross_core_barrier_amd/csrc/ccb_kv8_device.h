@@ -72,6 +72,84 @@ __device__ __forceinline__ uint32_t narrow(float x)
     }
 }
 
+// Four quotients x / s as codes of one word, and whether any of them is too
+// near a border between two codes to be sure (then encode() has to decide).
+// t = x * inv is within 2^-22 of the quotient; int8: 2^-14 around a border,
+// e4m3: 16 units of t's last place, and every quotient below 2^-6, where the
+// step no longer follows the exponent.
+template <int F>
+__device__ __forceinline__ uint32_t encode4_near(const float* t, bool& unsure)
+{
+    if constexpr (F == kInt8) {
+        uint32_t n[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float c = __builtin_amdgcn_fmed3f(t[i], -127.0f, 127.0f);
+            const float r = __builtin_rintf(c);
+            unsure |= fabsf(c - r) > 0.5f - 0x1p-14f;
+            n[i] = (uint32_t)(int32_t)r;
+        }
+        const uint32_t a = __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400u);
+        const uint32_t b = __builtin_amdgcn_perm(n[3], n[2], 0x04000c0cu);
+        return a | b;
+    } else {
+        float c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = __builtin_amdgcn_fmed3f(t[i], -448.0f, 448.0f);
+            const uint32_t u = bits(c[i]);
+            unsure |= (u & 0xfffffu) - (0x80000u - 16u) <= 32u;
+            unsure |= fabsf(c[i]) < 0x1p-6f && c[i] != 0.0f;
+        }
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+    }
+}
+
+// Eight new values as codes of the block scale s; inv is 1 / s.
+template <int F>
+__device__ __forceinline__ uint2 encode8(const float* x, float inv, float s)
+{
+    if (!(s > 0.0f)) return make_uint2(0, 0);
+    float t[8];
+    bool unsure = s > 0x1p120f;  // there 1 / s loses bits
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = x[i] != x[i] ? 0.0f : x[i] * inv;
+    uint2 u = make_uint2(encode4_near<F>(t, unsure), encode4_near<F>(t + 4, unsure));
+    if (unsure) {
+        u = make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u.x |= (uint32_t)encode_value<F>(x[i], inv, s) << (8 * i);
+            u.y |= (uint32_t)encode_value<F>(x[4 + i], inv, s) << (8 * i);
+        }
+    }
+    return u;
+}
+
+// Eight codes (two words) of the scale sOld as codes of the scale s.
+template <int F>
+__device__ __forceinline__ uint2 encode8_again(const uint2& w, float sOld, float inv, float s)
+{
+    if (!(s > 0.0f)) return make_uint2(0, 0);
+    float v[8], t[8];
+    decode4<F>(w.x, v);
+    decode4<F>(w.y, v + 4);
+    bool unsure = s > 0x1p120f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[i] * sOld * inv;
+    uint2 u = make_uint2(encode4_near<F>(t, unsure), encode4_near<F>(t + 4, unsure));
+    if (unsure) {
+        u = make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u.x |= (uint32_t)encode_again<F>(v[i], sOld, inv, s) << (8 * i);
+            u.y |= (uint32_t)encode_again<F>(v[4 + i], sOld, inv, s) << (8 * i);
+        }
+    }
+    return u;
+}
+
 // The largest of a value over the workgroup (256 threads); x is not NaN.
 __device__ __forceinline__ float block_max(float x, float* scratch)
 {
