@@ -84,9 +84,15 @@ __global__ __launch_bounds__(kThreads) void kv8_k_append(ccbKv8Cache c, ccbKv8Ro
         raw[k] = make_uint4(0, 0, 0, 0);
         if (i < nVec) raw[k] = *(const uint4*)(src + (i / V) * rows.strideToken + (i % V) * 8);
     }
+    uint32_t most = 0;
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        if (k * kThreads < nVec) {
+    for (int k = 0; k < N; ++k) most = larger16(most, raw[k]);
+    most = (most >> 16) > (most & 0xffffu) ? most >> 16 : most & 0xffffu;
+    a = widen<T>(most);
+    if (!(a < INFINITY)) {  // an infinity or NaN: the largest of the others
+        a = 0.0f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
             float x[8];
             widen8<T>(raw[k], x);
 #pragma unroll
@@ -199,24 +205,41 @@ __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows
 // ---------------------------------------------------------------------------
 // evict: which tokens stay
 //
-// One workgroup per sequence and head.  The kept tokens are those whose key
-// is above the k-th largest key, and the first few that equal it; the k-th
-// largest is found 11, 11 and 10 bits at a time from the top with a histogram
-// in LDS (integer counts: the order of the atomics does not matter), and the
-// search ends early where every key of the threshold's bin stays.
+// The kept tokens are those whose key is above the k-th largest key, and the
+// first few that equal it; the k-th largest is found 11, 11 and 10 bits at a
+// time from the top with histograms in LDS (integer counts: the order of the
+// atomics does not matter), and the search ends early where every key of the
+// threshold's bin stays.  Each wave owns a run of tokens, so places among the
+// kept ones need one scan over the waves' counts and then only votes within a
+// wave.
 //
-// Each wave owns a run of tokens, so places among the kept ones need one scan
-// over the waves' counts and then only votes within the wave.  Rows of up to
-// 16384 tokens stay in registers between the passes; longer ones are read
-// again from L2 (four times in all).
+// Rows of up to 16384 tokens are chosen from by one workgroup, which keeps
+// them in registers.  A pass costs a CU about 0.2 us per 1024 tokens, so longer
+// rows are cut into segments, one workgroup each, and the passes become
+// kernels: each stage sums its row's histograms of the stage before, finds the
+// bin, and counts the next bits of its segment.  Nothing waits inside a kernel.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
 constexpr int kSelStep = 256;     // tokens of a wave's step, four to a lane
 constexpr int kSelResident = 4;   // steps that stay in registers
+constexpr int kSelShort = kSelWaves * kSelStep * kSelResident;
 constexpr int kBins = 2048;
 
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+
+struct SelectArgs {
+    ccbKv8Cache from, to;
+    int32_t budget, recent, sinks;
+    int32_t segments;  // of a row
+    int32_t* index;    // [row][budget]
+    int32_t* kept;
+    int32_t* hist;     // [2][row][segment][kBins]
+    int32_t* state;    // [2][row][kState]
+    int2* counts;      // [row][segment]: tokens that stay for sure, and that equal the threshold
+    int32_t* err;
+};
+constexpr int kState = 4;  // prefix, shift, need, whether the search is over
 
 // Exclusive prefix sum of x over the workgroup.
 __device__ __forceinline__ int32_t block_scan(int32_t x, int32_t* scratch)
@@ -250,166 +273,299 @@ __device__ __forceinline__ void count_bin(int32_t* hist, uint32_t bin, bool coun
     if ((int)(threadIdx.x & 63) == leader) atomicAdd(&hist[b0], __popcll(same));
 }
 
-struct SelectOut {
-    int32_t* index;
-    int32_t* kept;
-    float* weight;
+// What is known of a row's threshold.
+struct Threshold {
+    uint32_t prefix;  // its upper bits
+    int32_t shift;    // below which they end
+    int32_t need;     // how many of the tokens that equal it, so far, stay
+    bool over;        // nothing is left to find
 };
 
-template <bool R>
-__device__ __forceinline__ void select_row(const float* w, int32_t len, int32_t low, int32_t high,
-                                           int32_t need, const SelectOut& out, int32_t* hist,
-                                           int32_t* scratch, int32_t* found)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    // this wave's tokens: first + step * kSelStep + 4 * lane + e
-    const int32_t steps = ((len + kSelWaves - 1) / kSelWaves + kSelStep - 1) / kSelStep;
-    const int32_t first = wave * steps * kSelStep + 4 * lane;
-    auto load = [&](int32_t step) {
-        const int32_t t = first + step * kSelStep;
-        f4u v = {0, 0, 0, 0};
-        if (t + 4 <= len) {
-            v = *(const f4u*)(w + t);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (t + e < len) v[e] = w[t + e];
-        }
-        return v;
-    };
-    f4u held[kSelResident];
-    if (R) {
-#pragma unroll
-        for (int i = 0; i < kSelResident; ++i)
-            if (i < steps) held[i] = load(i);
-    }
-    auto each = [&](auto&& f) {
-        if (R) {
-#pragma unroll
-            for (int i = 0; i < kSelResident; ++i)
-                if (i < steps) f(first + i * kSelStep, held[i]);
-        } else {
-            int32_t i = 0;
-            for (; i + 4 <= steps; i += 4) {  // four loads in flight
-                f4u v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = load(i + k);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) f(first + (i + k) * kSelStep, v[k]);
-            }
-            for (; i < steps; ++i) f(first + i * kSelStep, load(i));
-        }
-    };
+// The row's tokens and what is chosen among them.
+struct Row {
+    const float* w;
+    int32_t len, low, high;  // chosen by weight: tokens low .. high - 1
+    Threshold start;
+};
 
-    uint32_t prefix = 0;  // the threshold's upper bits, found so far
-    int shift = 32;       // below which they end
-    const bool search = high > low && need > 0;
-    for (int pass = 0; search && pass < 3; ++pass) {
-        const int above = shift;
-        shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t mask = (1u << (above - shift)) - 1;
-        for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        each([&](int32_t t, const f4u& v) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t key = weight_key(v[e]);
-                count_bin(hist, (key >> shift) & mask,
-                          t + e >= low && t + e < high && (pass == 0 || (key >> above) == prefix));
-            }
-        });
-        __syncthreads();
-        // the bin of the need-th largest: two bins to a thread, from the top
-        const int32_t h0 = hist[kBins - 1 - 2 * threadIdx.x], h1 = hist[kBins - 2 - 2 * threadIdx.x];
-        const int32_t before = block_scan(h0 + h1, scratch);
-        if (before < need && need <= before + h0 + h1) {
-            const bool second = need > before + h0;
-            found[0] = kBins - 1 - 2 * (int32_t)threadIdx.x - (second ? 1 : 0);
-            found[1] = before + (second ? h0 : 0);
-            found[2] = second ? h1 : h0;
-        }
-        __syncthreads();
-        prefix = (prefix << (above - shift)) | (uint32_t)found[0];
-        need -= found[1];
-        if (need == found[2]) break;  // (alike in every thread)
+__device__ __forceinline__ Row row_of(const SelectArgs& a, int64_t row)
+{
+    Row r;
+    r.len = checked_len(a.from.lens[row / a.from.heads], a.from.maxPages * a.from.pageSize);
+    if (r.len < 0) {
+        if (threadIdx.x == 0) report(a.err);
+        r.len = 0;
     }
-    // need: how many of the tokens that equal the threshold, as far as it is known, stay
-    auto votes = [&](int32_t t, const f4u& v, uint64_t* sure, uint64_t* equal) {
+    r.w = a.from.weight + row * a.from.weightStride;
+    r.low = r.len > a.budget ? a.sinks : 0;
+    r.high = r.len > a.budget ? r.len - a.recent : 0;
+    const int32_t need = a.budget - a.sinks - a.recent;
+    r.start = Threshold{0, 32, need, !(r.high > r.low && need > 0)};
+    return r;
+}
+
+// Whether a token stays for sure, and whether it equals the threshold.
+__device__ __forceinline__ void judge(const Row& r, const Threshold& th, int32_t t, float w, bool& sure,
+                                      bool& equal)
+{
+    const bool middle = t >= r.low && t < r.high;
+    const bool search = th.shift < 32;  // else none of the middle stays
+    const uint32_t key = search ? weight_key(w) >> th.shift : 0u;
+    sure = t < r.len && (!middle || (search && key > th.prefix));
+    equal = middle && search && key == th.prefix;
+}
+
+// Four weights, those at and past `end` 0.
+__device__ __forceinline__ f4u load4(const float* w, int32_t t, int32_t end)
+{
+    f4u v = {0, 0, 0, 0};
+    if (t + 4 <= end) {
+        v = *(const f4u*)(w + t);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (t + e < end) v[e] = w[t + e];
+    }
+    return v;
+}
+
+// Counts the bits [below, th.shift) of the tokens that share the threshold's
+// upper bits; `each` goes over the workgroup's tokens.
+template <class Each>
+__device__ __forceinline__ void count_bits(const Row& r, const Threshold& th, int below, int32_t* hist,
+                                           Each&& each)
+{
+    const uint32_t mask = (1u << (th.shift - below)) - 1;
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    each([&](int32_t t, const f4u& v) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const bool middle = t + e >= low && t + e < high;
-            const uint32_t key = search ? weight_key(v[e]) >> shift : 0u;
-            sure[e] = __ballot(t + e < len && (middle ? search && key > prefix : true));
-            equal[e] = __ballot(middle && search && key == prefix);
+            const uint32_t key = weight_key(v[e]);
+            count_bin(hist, (key >> below) & mask,
+                      t + e >= r.low && t + e < r.high &&
+                          (th.shift == 32 || (key >> (th.shift & 31)) == th.prefix));
         }
-    };
-    int32_t nSure = 0, nEqual = 0;
-    each([&](int32_t t, const f4u& v) {
-        uint64_t sure[4], equal[4];
-        votes(t, v, sure, equal);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) nSure += __popcll(sure[e]), nEqual += __popcll(equal[e]);
     });
     __syncthreads();
-    if (lane == 0) hist[wave] = nSure, hist[kSelWaves + wave] = nEqual;
+}
+
+// The bin of the need-th largest, given this thread's two bins from the top.
+__device__ __forceinline__ void find_bin(Threshold& th, int below, int32_t h0, int32_t h1, int32_t* scratch,
+                                         int32_t* found)
+{
+    const int32_t before = block_scan(h0 + h1, scratch);
+    if (before < th.need && th.need <= before + h0 + h1) {
+        const bool second = th.need > before + h0;
+        found[0] = kBins - 1 - 2 * (int32_t)threadIdx.x - (second ? 1 : 0);
+        found[1] = before + (second ? h0 : 0);
+        found[2] = second ? h1 : h0;
+    }
     __syncthreads();
-    int32_t sureBefore = 0, equalBefore = 0;
-    for (int i = 0; i < wave; ++i) sureBefore += hist[i], equalBefore += hist[kSelWaves + i];
+    th.prefix = (th.shift == 32 ? 0u : th.prefix << (th.shift - below)) | (uint32_t)found[0];
+    th.need -= found[1];
+    th.shift = below;
+    th.over = below == 0 || th.need == found[2];
+}
+
+// This wave's tokens that stay for sure, and that equal the threshold.
+template <class Each>
+__device__ __forceinline__ int2 count_kept(const Row& r, const Threshold& th, Each&& each)
+{
+    int2 n = make_int2(0, 0);
+    each([&](int32_t t, const f4u& v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bool s, q;
+            judge(r, th, t + e, v[e], s, q);
+            n.x += __popcll(__ballot(s)), n.y += __popcll(__ballot(q));
+        }
+    });
+    return n;
+}
+
+// Writes the workgroup's kept tokens; `before` counts those ahead of them.
+template <class Each>
+__device__ __forceinline__ void write_kept(const SelectArgs& a, const Row& r, const Threshold& th, int64_t row,
+                                           int2 before, int2* scratch, Each&& each)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int2 n = count_kept(r, th, each);
+    if (lane == 0) scratch[wave] = n;
+    __syncthreads();
+    for (int i = 0; i < wave; ++i) before.x += scratch[i].x, before.y += scratch[i].y;
+    int32_t* index = a.index + row * a.budget;
+    int32_t* kept = a.kept != nullptr ? a.kept + row * a.budget : nullptr;
+    float* weight = a.to.weight != nullptr ? a.to.weight + row * a.to.weightStride : nullptr;
     const uint64_t below = ((uint64_t)1 << lane) - 1;
     each([&](int32_t t, const f4u& v) {
         uint64_t sure[4], equal[4];
-        votes(t, v, sure, equal);
-        int32_t s = sureBefore, q = equalBefore;
+        int32_t s = before.x, q = before.y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bool isSure, isEqual;
+            judge(r, th, t + e, v[e], isSure, isEqual);
+            sure[e] = __ballot(isSure), equal[e] = __ballot(isEqual);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) s += __popcll(sure[e] & below), q += __popcll(equal[e] & below);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const bool isSure = (sure[e] >> lane) & 1, isEqual = (equal[e] >> lane) & 1;
-            if (isSure || (isEqual && q < need)) {
-                const int32_t slot = s + (q < need ? q : need);
-                out.index[slot] = t + e;
-                if (out.kept != nullptr) out.kept[slot] = t + e;
-                if (out.weight != nullptr) out.weight[slot] = v[e];
+            if (isSure || (isEqual && q < th.need)) {
+                const int32_t slot = s + (q < th.need ? q : th.need);
+                index[slot] = t + e;
+                if (kept != nullptr) kept[slot] = t + e;
+                if (weight != nullptr) weight[slot] = v[e];
             }
             s += isSure, q += isEqual;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sureBefore += __popcll(sure[e]), equalBefore += __popcll(equal[e]);
+        for (int e = 0; e < 4; ++e) before.x += __popcll(sure[e]), before.y += __popcll(equal[e]);
     });
 }
 
-__global__ __launch_bounds__(kSelThreads) void kv8_k_select(ccbKv8Cache from, ccbKv8Cache to,
-                                                            int32_t budget, int32_t recent,
-                                                            int32_t sinks, int32_t* index,
-                                                            int32_t* kept, int32_t* err)
+// The end of a row: its length, and places that nothing was kept for.
+__device__ __forceinline__ void finish_row(const SelectArgs& a, const Row& r, int64_t row)
+{
+    const int32_t stay = r.len < a.budget ? r.len : a.budget;
+    if (threadIdx.x == 0 && row % a.from.heads == 0) a.to.lens[row / a.from.heads] = stay;
+    for (int32_t i = stay + (int)threadIdx.x; i < a.budget; i += kSelThreads) {
+        if (a.kept != nullptr) a.kept[row * a.budget + i] = -1;
+        if (a.to.weight != nullptr) a.to.weight[row * a.to.weightStride + i] = 0.0f;
+    }
+}
+
+__global__ __launch_bounds__(kSelThreads) void kv8_k_select_short(SelectArgs a)
 {
     __shared__ int32_t hist[kBins];
     __shared__ int32_t scratch[kSelWaves];
+    __shared__ int2 places[kSelWaves];
     __shared__ int32_t found[3];
-    const int32_t b = blockIdx.x / (uint32_t)from.heads;
-    int32_t len = checked_len(from.lens[b], from.maxPages * from.pageSize);
-    if (len < 0) {
-        if (threadIdx.x == 0) report(err);
-        len = 0;
-    }
     const int64_t row = blockIdx.x;
-    const float* w = from.weight + row * from.weightStride;
-    SelectOut out;
-    out.index = index + row * budget;
-    out.kept = kept != nullptr ? kept + row * budget : nullptr;
-    out.weight = to.weight != nullptr ? to.weight + row * to.weightStride : nullptr;
-    const int32_t stay = len < budget ? len : budget;
-    if (threadIdx.x == 0 && row % from.heads == 0) to.lens[b] = stay;
-    // chosen by weight: `need` of the tokens between low and high
-    const int32_t low = len > budget ? sinks : 0, high = len > budget ? len - recent : 0;
-    const int32_t need = budget - sinks - recent;
-    if (len <= kSelWaves * kSelResident * kSelStep)
-        select_row<true>(w, len, low, high, need, out, hist, scratch, found);
-    else
-        select_row<false>(w, len, low, high, need, out, hist, scratch, found);
-    for (int32_t i = stay + (int)threadIdx.x; i < budget; i += kSelThreads) {
-        if (out.kept != nullptr) out.kept[i] = -1;
-        if (out.weight != nullptr) out.weight[i] = 0.0f;
+    const Row r = row_of(a, row);
+    // this wave's tokens: first + step * kSelStep + 4 * lane + e
+    const int32_t steps = (r.len + kSelWaves * kSelStep - 1) / (kSelWaves * kSelStep);
+    const int32_t first = (threadIdx.x >> 6) * steps * kSelStep + 4 * (threadIdx.x & 63);
+    f4u held[kSelResident];
+#pragma unroll
+    for (int i = 0; i < kSelResident; ++i)
+        if (i < steps) held[i] = load4(r.w, first + i * kSelStep, r.len);
+    auto each = [&](auto&& f) {
+#pragma unroll
+        for (int i = 0; i < kSelResident; ++i)
+            if (i < steps) f(first + i * kSelStep, held[i]);
+    };
+    Threshold th = r.start;
+#pragma unroll 1
+    for (int below = 21; !th.over; below = below == 21 ? 10 : 0) {
+        count_bits(r, th, below, hist, each);
+        const int32_t h0 = hist[kBins - 1 - 2 * threadIdx.x], h1 = hist[kBins - 2 - 2 * threadIdx.x];
+        find_bin(th, below, h0, h1, scratch, found);
+    }
+    write_kept(a, r, th, row, make_int2(0, 0), places, each);
+    finish_row(a, r, row);
+}
+
+// One stage of a long row: 0, 1 and 2 count 11, 11 and 10 bits, 3 writes.
+template <int S>
+__global__ __launch_bounds__(kSelThreads) void kv8_k_select_long(SelectArgs a)
+{
+    __shared__ int32_t hist[kBins];
+    __shared__ int32_t scratch[kSelWaves];
+    __shared__ int2 places[kSelWaves];
+    __shared__ int32_t found[3];
+    const int64_t row = blockIdx.x / (uint32_t)a.segments;
+    const int32_t seg = blockIdx.x % (uint32_t)a.segments;
+    const int64_t rows = (int64_t)a.from.batch * a.from.heads;
+    const Row r = row_of(a, row);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int32_t unit = kSelWaves * kSelStep;
+    const int32_t size = (int32_t)(((r.len + (int64_t)a.segments * unit - 1) / ((int64_t)a.segments * unit)) * unit);
+    const int64_t begin64 = (int64_t)seg * size;
+    const int32_t begin = begin64 < r.len ? (int32_t)begin64 : r.len;
+    const int32_t end = r.len - begin < size ? r.len : begin + size;
+    const int32_t steps = (end - begin + unit - 1) / unit;
+    const int32_t first = begin + wave * steps * kSelStep + 4 * lane;
+    auto each = [&](auto&& f) {
+        int32_t i = 0;
+        for (; i + 2 <= steps; i += 2) {  // two loads in flight
+            const f4u v0 = load4(r.w, first + i * kSelStep, end);
+            const f4u v1 = load4(r.w, first + (i + 1) * kSelStep, end);
+            f(first + i * kSelStep, v0);
+            f(first + (i + 1) * kSelStep, v1);
+        }
+        if (i < steps) f(first + i * kSelStep, load4(r.w, first + i * kSelStep, end));
+    };
+    // tokens past the segment's end belong to the next one
+    Row mine = r;
+    mine.len = end;
+    mine.high = r.high < end ? r.high : end;
+
+    // the threshold, from the histograms of the stage before
+    Threshold th = r.start;
+    if (S > 1 && !th.over) {
+        const int32_t* st = a.state + ((int64_t)((S + 1) & 1) * rows + row) * kState;
+        th.prefix = (uint32_t)st[0], th.shift = st[1], th.need = st[2], th.over = st[3] != 0;
+    }
+    const bool fresh = S > 0 && !th.over;
+    int2 ahead = make_int2(0, 0);  // this thread's two bins in the segments before
+    if (fresh) {
+        int2 h = make_int2(0, 0);  // lower bin, higher bin
+        const int32_t* in = a.hist + ((int64_t)((S + 1) & 1) * rows + row) * a.segments * kBins + kBins - 2 -
+                            2 * (int32_t)threadIdx.x;
+#pragma unroll 8
+        for (int32_t i = 0; i < a.segments; ++i) {
+            const int2 x = *(const int2*)(in + (int64_t)i * kBins);
+            h.x += x.x, h.y += x.y;
+            if (S == 3 && i < seg) ahead.x += x.x, ahead.y += x.y;
+        }
+        find_bin(th, S == 1 ? 21 : S == 2 ? 10 : 0, h.y, h.x, scratch, found);
+    }
+    if ((S == 1 || S == 2) && seg == 0 && threadIdx.x == 0) {
+        int32_t* st = a.state + ((int64_t)(S & 1) * rows + row) * kState;
+        st[0] = (int32_t)th.prefix, st[1] = th.shift, st[2] = th.need, st[3] = th.over;
+    }
+    int2* counts = a.counts + row * a.segments;
+    if constexpr (S == 2) {
+        const int2 n = count_kept(mine, th, each);
+        if (lane == 0) places[wave] = n;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int2 sum = make_int2(0, 0);
+            for (int i = 0; i < kSelWaves; ++i) sum.x += places[i].x, sum.y += places[i].y;
+            counts[seg] = sum;
+        }
+    }
+    if constexpr (S < 3) {
+        if (th.over) return;
+        count_bits(mine, th, S == 0 ? 21 : S == 1 ? 10 : 0, hist, each);
+        int32_t* out = a.hist + (((int64_t)(S & 1) * rows + row) * a.segments + seg) * kBins;
+        for (int i = threadIdx.x; i < kBins; i += kSelThreads) out[i] = hist[i];
+    } else {
+        // kept in the segments before: what stage 2 was sure of, and by the last bits
+        int2 before = make_int2(0, 0);
+        if (fresh) {
+            const int32_t low = kBins - 2 - 2 * (int32_t)threadIdx.x, bin = found[0];
+            before.x = (low > bin ? ahead.x : 0) + (low + 1 > bin ? ahead.y : 0);
+            before.y = low == bin ? ahead.x : low + 1 == bin ? ahead.y : 0;
+        }
+        for (int32_t i = threadIdx.x; i < seg; i += kSelThreads) {
+            const int2 x = counts[i];
+            before.x += x.x, before.y += fresh ? 0 : x.y;
+        }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) {
+            before.x += __shfl_xor(before.x, d, 64);
+            before.y += __shfl_xor(before.y, d, 64);
+        }
+        if (lane == 0) places[wave] = before;
+        __syncthreads();
+        before = make_int2(0, 0);
+        for (int i = 0; i < kSelWaves; ++i) before.x += places[i].x, before.y += places[i].y;
+        __syncthreads();
+        write_kept(a, mine, th, row, before, places, each);
+        if (seg == 0) finish_row(a, r, row);
     }
 }
 
@@ -542,23 +698,63 @@ hipError_t kv8_read(const ccbKv8Cache& c, const ccbKv8Rows* k, const ccbKv8Rows*
     return hipGetLastError();
 }
 
+// Segments of a row, 0 where one workgroup chooses by itself, and the
+// workspace's parts; returns its bytes.
+static size_t select_plan(SelectArgs& a, const ccbKv8Cache& from, int32_t budget, void* ws)
+{
+    const int64_t rows = (int64_t)from.batch * from.heads;
+    const int64_t room = (int64_t)from.maxPages * from.pageSize;
+    a.segments = 0;
+    if (room > kSelShort) {
+        // 8192 tokens and more for each, two workgroups on a CU at most
+        const int64_t most = rows < 256 ? 512 / rows : 2;
+        int64_t n = (room + 8191) / 8192;
+        n = n < most ? n : most;
+        a.segments = (int32_t)(n < 64 ? n : 64);
+    }
+    size_t bytes = 0;
+    auto take = [&](int64_t n, size_t each) {
+        char* here = (char*)ws + bytes;
+        bytes += ((size_t)n * each + 127) / 128 * 128;
+        return here;
+    };
+    a.index = (int32_t*)take(rows * budget, sizeof(int32_t));
+    a.hist = (int32_t*)take(2 * rows * a.segments * kBins, sizeof(int32_t));
+    a.state = (int32_t*)take(a.segments ? 2 * rows * kState : 0, sizeof(int32_t));
+    a.counts = (int2*)take(rows * a.segments, sizeof(int2));
+    return bytes;
+}
+
 size_t kv8_evict_bytes(const ccbKv8Cache& from, int32_t budget)
 {
-    return (size_t)from.batch * from.heads * budget * sizeof(int32_t);
+    SelectArgs a;
+    return select_plan(a, from, budget, nullptr);
 }
 
 hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t budget, int32_t recent,
                      int32_t sinks, int32_t* kept, void* ws, int32_t* err, int numCUs, hipStream_t s)
 {
     (void)numCUs;
-    int32_t* index = (int32_t*)ws;
+    SelectArgs a;
+    select_plan(a, from, budget, ws);
+    a.from = from, a.to = to;
+    a.budget = budget, a.recent = recent, a.sinks = sinks;
+    a.kept = kept, a.err = err;
+    int32_t* index = a.index;
     const int32_t nPages = (budget + from.pageSize - 1) / from.pageSize;
     const int64_t rows = (int64_t)from.batch * from.heads;
     const int64_t blocks = rows * nPages * 2;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    kv8_k_select<<<dim3((unsigned)rows), dim3(kSelThreads), 0, s>>>(from, to, budget, recent, sinks,
-                                                                   index, kept, err);
-    hipError_t e = hipGetLastError();
+    if (blocks > INT32_MAX || rows * (a.segments + 1) > INT32_MAX) return hipErrorInvalidValue;
+    if (a.segments == 0) {
+        kv8_k_select_short<<<dim3((unsigned)rows), dim3(kSelThreads), 0, s>>>(a);
+    } else {
+        const dim3 grid((unsigned)(rows * a.segments));
+        kv8_k_select_long<0><<<grid, dim3(kSelThreads), 0, s>>>(a);
+        kv8_k_select_long<1><<<grid, dim3(kSelThreads), 0, s>>>(a);
+        kv8_k_select_long<2><<<grid, dim3(kSelThreads), 0, s>>>(a);
+        kv8_k_select_long<3><<<grid, dim3(kSelThreads), 0, s>>>(a);
+    }
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
 #define KV8_MOVE(F, D) \
     (kv8_k_move<F, D><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(from, to, budget, nPages, index, err), 0)

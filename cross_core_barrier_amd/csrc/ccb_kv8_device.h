@@ -72,13 +72,24 @@ __device__ __forceinline__ uint32_t narrow(float x)
     }
 }
 
-// Four quotients x / s as codes of one word, and whether any of them is too
-// near a border between two codes to be sure (then encode() has to decide).
-// t = x * inv is within 2^-22 of the quotient; int8: 2^-14 around a border,
-// e4m3: 16 units of t's last place, and every quotient below 2^-6, where the
-// step no longer follows the exponent.
+// Whether quotients were too near a border between two codes to be sure.
+// t = x * inv is within 2^-22 of the quotient; unsure is, for int8, within
+// 2^-14 of a border, and for e4m3 within 16 units of t's last place, or below
+// 2^-6, where the step no longer follows the exponent.
 template <int F>
-__device__ __forceinline__ uint32_t encode4_near(const float* t, bool& unsure)
+struct Near {
+    float d = 0.0f;                     // int8: largest distance to a code
+    uint32_t border = ~0u, small = ~0u;  // e4m3: place above a border's zone, size
+    __device__ __forceinline__ bool unsure() const
+    {
+        if constexpr (F == kInt8) return d > 0.5f - 0x1p-14f;
+        return border <= 32u << 12 || small < (0x3c800000u << 1) - 1;
+    }
+};
+
+// Four quotients as the codes of one word.
+template <int F>
+__device__ __forceinline__ uint32_t encode4_near(const float* t, Near<F>& near)
 {
     if constexpr (F == kInt8) {
         uint32_t n[4];
@@ -86,7 +97,7 @@ __device__ __forceinline__ uint32_t encode4_near(const float* t, bool& unsure)
         for (int i = 0; i < 4; ++i) {
             const float c = __builtin_amdgcn_fmed3f(t[i], -127.0f, 127.0f);
             const float r = __builtin_rintf(c);
-            unsure |= fabsf(c - r) > 0.5f - 0x1p-14f;
+            near.d = fmaxf(near.d, fabsf(c - r));
             n[i] = (uint32_t)(int32_t)r;
         }
         const uint32_t a = __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400u);
@@ -98,10 +109,13 @@ __device__ __forceinline__ uint32_t encode4_near(const float* t, bool& unsure)
         for (int i = 0; i < 4; ++i) {
             c[i] = __builtin_amdgcn_fmed3f(t[i], -448.0f, 448.0f);
             const uint32_t u = bits(c[i]);
-            unsure |= (u & 0xfffffu) - (0x80000u - 16u) <= 32u;
-            unsure |= fabsf(c[i]) < 0x1p-6f && c[i] != 0.0f;
+            // the 20 bits below e4m3's three, 0 at 16 units before the border
+            const uint32_t above = (u - (0x80000u - 16u)) << 12;
+            const uint32_t size = (u << 1) - 1;  // a 0 is not small
+            near.border = above < near.border ? above : near.border;
+            near.small = size < near.small ? size : near.small;
         }
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
         return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
     }
 }
@@ -111,12 +125,15 @@ template <int F>
 __device__ __forceinline__ uint2 encode8(const float* x, float inv, float s)
 {
     if (!(s > 0.0f)) return make_uint2(0, 0);
-    float t[8];
-    bool unsure = s > 0x1p120f;  // there 1 / s loses bits
+    float t[8], odd = 0.0f;
+    Near<F> near;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = x[i] != x[i] ? 0.0f : x[i] * inv;
-    uint2 u = make_uint2(encode4_near<F>(t, unsure), encode4_near<F>(t + 4, unsure));
-    if (unsure) {
+    for (int i = 0; i < 8; ++i) {
+        t[i] = x[i] * inv;
+        odd = fmaf(x[i], 0.0f, odd);  // NaN if any value is NaN or infinite
+    }
+    uint2 u = make_uint2(encode4_near<F>(t, near), encode4_near<F>(t + 4, near));
+    if (near.unsure() || odd != odd || s > 0x1p120f) {  // (there 1 / s loses bits)
         u = make_uint2(0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -135,11 +152,12 @@ __device__ __forceinline__ uint2 encode8_again(const uint2& w, float sOld, float
     float v[8], t[8];
     decode4<F>(w.x, v);
     decode4<F>(w.y, v + 4);
-    bool unsure = s > 0x1p120f;
+    const float ratio = sOld * inv;
+    Near<F> near;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = v[i] * sOld * inv;
-    uint2 u = make_uint2(encode4_near<F>(t, unsure), encode4_near<F>(t + 4, unsure));
-    if (unsure) {
+    for (int i = 0; i < 8; ++i) t[i] = v[i] * ratio;
+    uint2 u = make_uint2(encode4_near<F>(t, near), encode4_near<F>(t + 4, near));
+    if (near.unsure() || s > 0x1p120f) {
         u = make_uint2(0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -148,6 +166,20 @@ __device__ __forceinline__ uint2 encode8_again(const uint2& w, float sOld, float
         }
     }
     return u;
+}
+
+// The largest size among 16-bit values, two to a word, kept as bits: sizes
+// order like whole numbers.
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t larger16(uint32_t m, const uint4& u)
+{
+    us2 x = __builtin_bit_cast(us2, m);
+    x = __builtin_elementwise_max(x, __builtin_bit_cast(us2, u.x & 0x7fff7fffu));
+    x = __builtin_elementwise_max(x, __builtin_bit_cast(us2, u.y & 0x7fff7fffu));
+    x = __builtin_elementwise_max(x, __builtin_bit_cast(us2, u.z & 0x7fff7fffu));
+    x = __builtin_elementwise_max(x, __builtin_bit_cast(us2, u.w & 0x7fff7fffu));
+    return __builtin_bit_cast(uint32_t, x);
 }
 
 // The largest of a value over the workgroup (256 threads); x is not NaN.

@@ -495,6 +495,92 @@ def test_evict_long(kv8):
     _say("evict 40001 tokens")
     _evict_case(kv8, 2, "int8", [40001, 9000], 2000, 64, 4, 3, 128, 64, ties=True)
 
+@pytest.mark.parametrize("kind", ["ties", "alike", "few", "spread"])
+@pytest.mark.parametrize("budget,recent,sinks", [(1, 0, 0), (900, 100, 4), (19000, 0, 0), (5000, 5000, 0)])
+def test_evict_rows_in_segments(kv8, kind, budget, recent, sinks):
+    """Rows that several workgroups share, beside short and empty ones: the
+    kept tokens of a segment start where the ones before it end."""
+    rng = np.random.default_rng(budget)
+    lens = [30011, 0, 700, 17000, 20480]
+    heads, P, D, width = 2, 128, 64, 240
+    w = rng.random((5, heads, width * P)).astype(np.float32) ** 8
+    if kind == "ties":
+        w = np.round(w * 8) / 8
+    elif kind == "alike":
+        w[:] = 0.25
+    elif kind == "few":  # most tokens never drew any weight
+        w[rng.random(w.shape) < 0.98] = 0
+    pages = torch.from_numpy(rng.permutation(5 * width).astype(np.int32).reshape(5, width)).cuda()
+    k = torch.zeros((5 * width, heads, P, D), dtype=torch.int8, device="cuda")
+    scales = [torch.ones((5 * width, heads), device="cuda") for _ in range(2)]
+    cache = kv8.Kv8Cache(k, k.clone(), *scales, pages, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                         torch.from_numpy(w).cuda())
+    rows = -(-budget // P)
+    to = kv8.Kv8Cache.allocate(5 * rows, heads, P, D, 5, rows, "int8", weights=True)
+    to.page_table.copy_(torch.arange(5 * rows, dtype=torch.int32).view(5, rows))
+    _say(f"evict rows in segments, {kind}, budget={budget} recent={recent} sinks={sinks}")
+    kept = torch.zeros((5, heads, budget), dtype=torch.int32, device="cuda")
+    cache.evict(to, budget, recent, sinks, kept=kept)
+    got, gw = kept.cpu().numpy(), to.weight.cpu().numpy()
+    for b, n in enumerate(lens):
+        for h in range(heads):
+            want = oracle.kept(w[b, h], n, budget, recent, sinks)
+            assert got[b, h].tolist() == want + [-1] * (budget - len(want)), (b, h)
+            assert np.array_equal(gw[b, h, :budget], np.r_[w[b, h, want], np.zeros(budget - len(want), np.float32)])
+    assert to.lens.tolist() == [min(n, budget) for n in lens]
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_append_on_borders(kv8, fmt, dtype):
+    """Values on the border between two codes, and a step to either side: with
+    a largest value of Q times a power of two the scale is that power, and
+    every border is a value of the type."""
+    D, P, n = 256, 16, 16
+    q = oracle.Q[fmt]
+    grid = np.arange(128.0) if fmt == "int8" else oracle._GRID
+    border = (grid[1:] + grid[:-1]) / 2
+    c = _host(np.random.default_rng(5), fmt, [n, n, n], 1, P, D)
+    cache = _device(kv8, c)
+    x = torch.zeros((3, n, 1, D), dtype=TYPES[dtype])
+    place = torch.from_numpy(border).to(TYPES[dtype])
+    assert torch.equal(place.double(), torch.from_numpy(border))  # exact
+    step = torch.finfo(TYPES[dtype]).eps
+    for i, scale in enumerate((1.0, 2.0 ** -5, 2.0 ** 4)):
+        for j, by in enumerate((1.0, 1 + step, 1 - step / 2, -1.0, -1 - step, -1 + step / 2)):
+            x[i, j, 0, :len(border)] = (place.double() * by * scale).to(TYPES[dtype])
+        x[i, 6, 0, 0] = q * scale
+    _say(f"append on borders {fmt} {dtype}")
+    oracle.append(c, x.double().numpy(), -x.double().numpy(), [n] * 3)
+    cache.append(x.cuda(), -x.cuda())
+    for which, codes in (("k", cache.k), ("v", cache.v)):
+        pages = c["table"][:, 0]
+        assert np.array_equal(oracle.values(_codes(codes)[pages], fmt), oracle.values(c[which][pages], fmt))
+    assert np.array_equal(cache.k_scale.cpu().numpy(), c["ks"], equal_nan=True)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("ratio", [1.5, 2.0, 3.0, 4.0, 6.0, 64.0])
+def test_append_rescales_older_codes_on_borders(kv8, fmt, ratio):
+    """Every code of an older token under a scale that grows by a simple
+    ratio: many land exactly between two codes."""
+    D, P = 256, 16
+    c = _host(np.random.default_rng(6), fmt, [P], 1, P, D)
+    page = c["table"][0, 0]
+    ok = [x for x in range(256) if x not in ((0x80,) if fmt == "int8" else (0x7F, 0xFF))]
+    for w in ("k", "v"):
+        c[w][page, 0, :P - 1] = np.resize(np.array(ok, np.uint8), (P - 1, D))
+        c[w + "s"][page] = 0.375
+    cache = _device(kv8, c)
+    x = torch.zeros((1, 1, 1, D), dtype=torch.bfloat16)
+    x[0, 0, 0, 0] = oracle.Q[fmt] * 0.375 * ratio
+    _say(f"append rescales on borders {fmt} {ratio}")
+    oracle.append(c, x.double().numpy(), x.double().numpy(), [1])
+    cache.append(x.cuda(), x.cuda())
+    for which, codes, scales in (("k", cache.k, cache.k_scale), ("v", cache.v, cache.v_scale)):
+        assert np.array_equal(scales.cpu().numpy(), c[which + "s"], equal_nan=True)
+        assert np.array_equal(oracle.values(_codes(codes)[page], fmt), oracle.values(c[which][page], fmt))
+
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
