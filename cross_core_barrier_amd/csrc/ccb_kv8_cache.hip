@@ -594,19 +594,23 @@ __global__ __launch_bounds__(kThreads) void kv8_k_move(ccbKv8Cache from, ccbKv8C
     const int32_t b = rest / (uint32_t)nPages;
     const int32_t P = from.pageSize;
 
+    // (places past the kept tokens hold anything and are not used)
+    const int32_t mine = number * P + (int32_t)threadIdx.x;
+    const int32_t t = (int32_t)threadIdx.x < P && mine < budget
+                          ? index[((int64_t)b * from.heads + h) * budget + mine]
+                          : 0;
+    const int32_t page = checked_page(to.pageTable[b * to.tableStride + number], to.numPages);
     int32_t len = checked_len(from.lens[b], from.maxPages * P);
     if (len < 0) len = 0;  // the selection reports it
     const int32_t stay = len < budget ? len : budget;
     if (number * P >= stay) return;
     const int32_t n = stay - number * P < P ? stay - number * P : P;
-    const int32_t page = checked_page(to.pageTable[b * to.tableStride + number], to.numPages);
     if (page < 0) {
         if (threadIdx.x == 0) report(err);
         return;
     }
     const uint8_t* codes = (const uint8_t*)(isV ? from.v : from.k);
     if ((int32_t)threadIdx.x < n) {
-        const int32_t t = index[((int64_t)b * from.heads + h) * budget + number * P + threadIdx.x];
         const int32_t src = checked_page(from.pageTable[b * from.tableStride + t / P], from.numPages);
         if (src < 0) report(err);
         const int64_t block = (int64_t)(src < 0 ? 0 : src) * from.heads + h;

@@ -29,6 +29,7 @@ from .workloads import _enter, _leave
 
 _CODES = {torch.int8: ccb.CCB_KV8_INT8, torch.float8_e4m3fn: ccb.CCB_KV8_E4M3}
 _FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+_current_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: a tenth of the object's cost
 _ROWS = {torch.bfloat16: ccb.CCB_KV8_BF16, torch.float16: ccb.CCB_KV8_FP16, torch.float32: ccb.CCB_KV8_FP32}
 
 
@@ -65,6 +66,7 @@ class Kv8Cache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.page_table, self.lens, self.weight = page_table, lens, weight
         self.heads, self.head_dim, self.batch, self.device = heads, head_dim, batch, k.device
+        self._index = k.get_device()
         self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._c = ccb.ccbKv8Cache(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
@@ -87,19 +89,26 @@ class Kv8Cache:
         return cls(k, v, ks, vs, table, lens, weight)
 
     def _rows(self, t: torch.Tensor, heads: int, what: str):
-        _need(t.dim() == 4 and t.shape[0] == self.batch and t.shape[2] == heads and t.shape[3] == self.head_dim
-              and t.dtype in _ROWS and t.device == self.device and (t.stride(3) == 1 or t.numel() == 0),
-              f"{what}: [batch {self.batch}, tokens, heads {heads}, head_dim {self.head_dim}] on {self.device}, "
-              "bfloat16 or float16, the last dimension contiguous")
+        kind = _ROWS.get(t.dtype)
+        shape = t.shape
+        if kind is None or len(shape) != 4 or shape[0] != self.batch or shape[2] != heads \
+                or shape[3] != self.head_dim or t.get_device() != self._index:
+            kind = None
+        else:
+            sb, st, sh, sd = t.stride()
+            if sd != 1 and t.numel() != 0:
+                kind = None
+        if kind is None:
+            raise ValueError(f"{what}: [batch {self.batch}, tokens, heads {heads}, head_dim {self.head_dim}] on "
+                             f"{self.device}, bfloat16 or float16, the last dimension contiguous")
         # the stride of a dimension with one place is never used
-        n, c, h, _ = t.shape
-        sb, st, sh, _ = t.stride()
-        return ccb.ccbKv8Rows(t.data_ptr(), sb if n > 1 else 0, st if c > 1 else 0, sh if h > 1 else 0,
-                              _ROWS[t.dtype], 0)
+        return ccb.ccbKv8Rows(t.data_ptr(), sb if self.batch > 1 else 0, st if shape[1] > 1 else 0,
+                              sh if heads > 1 else 0, kind, 0)
 
     def _ints(self, t: Optional[torch.Tensor], shape: tuple, what: str):
-        _need(t is None or (tuple(t.shape) == shape and t.dtype == torch.int32 and t.is_contiguous()
-                            and t.device == self.device), f"{what}: {list(shape)} int32, contiguous")
+        if t is not None:
+            _need(t.shape == shape and t.dtype == torch.int32 and t.is_contiguous()
+                  and t.get_device() == self._index, f"{what}: {list(shape)} int32, contiguous")
         return t
 
     def _space(self, ws: Optional[torch.Tensor], need: int, s):
@@ -109,21 +118,23 @@ class Kv8Cache:
             if s is not None:
                 s.wait_stream(torch.cuda.current_stream(self.device))
                 ws.record_stream(s)
-        _need(ws.is_contiguous() and ws.device == self.device, "workspace: contiguous, on the cache's device")
+        _need(ws.is_contiguous() and ws.get_device() == self._index, "workspace: contiguous, on the cache's device")
         return ws, ws.numel() * ws.element_size()
 
     def _on(self, s):
-        return torch.cuda.current_stream(self.device) if s is None else s
+        """The stream a call runs on: `s`, or torch's current one."""
+        return _current_stream(self._index) if s is None else s
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts: Optional[torch.Tensor] = None,
                stream=None) -> None:
         """Write each sequence's counts[b] (None: all) new tokens as its last
         ones; lens counts them already.  k_new, v_new [batch, n, heads, head_dim]."""
         k, v = self._rows(k_new, self.heads, "k_new"), self._rows(v_new, self.heads, "v_new")
-        _need(k_new.shape == v_new.shape and k_new.dtype == v_new.dtype, "v_new: shape and dtype of k_new")
+        n = k_new.shape[1]
+        _need(n == v_new.shape[1] and k.type == v.type, "v_new: shape and dtype of k_new")
         self._ints(counts, (self.batch,), "counts")
         s = _enter(stream, self.device)
-        ccb.check(ccb.ccb_kv8_append(self._c, k, v, k_new.shape[1], counts, self.err, self._on(s)), "ccb_kv8_append")
+        ccb.check(ccb.ccb_kv8_append(self._c, k, v, n, counts, self.err, self._on(s)), "ccb_kv8_append")
         _leave(s, self.device)
 
     def attend_workspace(self, q_heads: int, queries: int = 1, accumulate: bool = False) -> torch.Tensor:
@@ -138,20 +149,21 @@ class Kv8Cache:
         """Attention of q [batch, queries, q_heads, head_dim], the sequences'
         last tokens; scale None is 1 / sqrt(head_dim).  Returns (out, lse)."""
         _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
-        queries, q_heads = q.shape[1], q.shape[2]
+        shape = q.shape
+        queries, q_heads = shape[1], shape[2]
         s = _enter(stream, self.device)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
             if s is not None:
                 out.record_stream(s)
         if lse is None:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
             if s is not None:
                 lse.record_stream(s)
-        _need(out.shape == q.shape and out.dtype == q.dtype, "out: shape and dtype of q")
-        _need(lse.shape == q.shape[:3] and lse.dtype == torch.float32 and lse.is_contiguous()
-              and lse.device == self.device, "lse: [batch, queries, q_heads] float32, contiguous")
         qr, outr = self._rows(q, q_heads, "q"), self._rows(out, q_heads, "out")
+        _need(out.shape[1] == queries and outr.type == qr.type, "out: shape and dtype of q")
+        _need(lse.shape == shape[:3] and lse.dtype == torch.float32 and lse.is_contiguous()
+              and lse.get_device() == self._index, "lse: [batch, queries, q_heads] float32, contiguous")
         need = 0 if workspace is not None else \
             ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
         ws, size = self._space(workspace, need, s)
@@ -173,7 +185,7 @@ class Kv8Cache:
         """Copy the budget tokens of each sequence and head with the largest
         weight (and its first `sinks` and last `recent`) into the cache `to`.
         kept [batch, heads, budget] int32 gets their numbers; it is returned."""
-        _need(to.device == self.device, "to: on the cache's device")
+        _need(to._index == self._index, "to: on the cache's device")
         self._ints(kept, (self.batch, self.heads, budget), "kept")
         s = _enter(stream, self.device)
         need = 0 if workspace is not None else ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
