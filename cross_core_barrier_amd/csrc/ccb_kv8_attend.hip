@@ -42,9 +42,8 @@ constexpr int kTile = 32;                     // tokens of a wave's step
 constexpr int kSegment = 32 * kWaves * kTile;  // tokens whose pages fit a wave's lanes
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kJoinRuns = 32;  // more of them are joined by a workgroup, not a wave
 constexpr float kSlack = 8.0f;  // how far (in powers of two) scores may pass the running maximum
-constexpr int kStoredRows = 16;  // up to here scores are kept for the weights, beyond they are computed again
-constexpr int kJoinTokens = 1024;
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef int i2 __attribute__((ext_vector_type(2)));
@@ -62,11 +61,13 @@ struct Plan {
     int32_t rowBlocks;  // workgroups that share a run of tokens
     int32_t chunk;      // tokens of a workgroup, a multiple of kWaves * kTile
     int32_t splits;     // runs a sequence may have
-    int32_t joinRows;   // workgroups of the join for a pair's rows
-    int32_t joinTokens; // and for its tokens
+    bool direct;        // one run: its workgroup writes the results
+    int32_t joinRows;   // workgroups of the join for the rows
+    int64_t joinBlocks; // all of the join's, those for the tokens among them,
+    int32_t joinSpan;   // so many each
     float* partO;   // [pair][split][row][D]
     float2* partML; // [pair][split][row]: maximum (base 2) and sum
-    float* scores;  // [pair][row][splits * chunk] (base 2), or null
+    float* scores;  // [pair][tile][row][kTile] (base 2), or null: see score_at
     float* lse2;    // [pair][row], +infinity for a row that sees nothing; or null
 };
 
@@ -128,6 +129,14 @@ __device__ __forceinline__ void pieces(float a, float b, uint32_t& hi, uint32_t&
 }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The score of a pair's row and token (counted from base).  A tile's rows lie
+// side by side, so that what a wave stores is one piece of memory.
+__device__ __forceinline__ float* score_at(const Plan& p, int32_t pair, int32_t row, int32_t t)
+{
+    const int64_t tile = (int64_t)pair * ((int64_t)p.splits * (p.chunk / kTile)) + t / kTile;
+    return p.scores + (tile * p.rows + row) * kTile + t % kTile;
+}
 
 // Sequence, head and what the rows of a workgroup may see.
 struct Range {
@@ -198,8 +207,31 @@ __device__ __forceinline__ int dim_at(int j, int g)
     return (D % 64 != 0 && j == D / 32 - 1) ? 32 * j + 8 * g : 64 * (j >> 1) + 16 * g + 8 * (j & 1);
 }
 
+// Writes a row's results from the sum of its weighted values: 4 of its
+// dimensions from each thread that asks, lse from the one with d4 = 0.
+template <int T>
+__device__ __forceinline__ void write_row(const Plan& p, int32_t b, int32_t h, int32_t pair, int32_t row,
+                                          int32_t d4, const f4& o, float top, float all)
+{
+    const ccb::Kv8AttendArgs& a = p.a;
+    const int32_t group = a.headsQ / a.c.heads;
+    uint2 u = make_uint2(0, 0);
+    if (all != 0.0f) {
+        u.x = narrow<T>(o.x / all) | (narrow<T>(o.y / all) << 16);
+        u.y = narrow<T>(o.z / all) | (narrow<T>(o.w / all) << 16);
+    }
+    *(uint2*)((uint16_t*)a.out.data + row_at(a.out, b, h, row, group) + d4 * 4) = u;
+    if (d4 == 0) {
+        const float lse = all != 0.0f ? top + log2f(all) : INFINITY;
+        if (p.lse2 != nullptr) p.lse2[(int64_t)pair * p.rows + row] = lse;
+        if (a.lse != nullptr)
+            a.lse[((int64_t)b * a.nQuery + row / group) * a.headsQ + h * group + row % group] =
+                all != 0.0f ? lse * kLn2 : -INFINITY;
+    }
+}
+
 template <int F, int T, int D, int NT>
-__global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(Plan p)
+__global__ __launch_bounds__(kThreads, 2) void kv8_k_attend(Plan p)
 {
     constexpr int C = D / 16;             // chunks of 16 codes in a token
     constexpr int NI = kTile * C / 64;    // loads of a wave for a tile of keys
@@ -223,13 +255,24 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
 
+    // lane i's place in a segment: the wave's i-th half tile
+    const int32_t shift = __builtin_ctz(P);
+    const int32_t laneAt = ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
+    // without a window the runs' places do not depend on the length: the first
+    // page numbers are fetched beside it (they may be of pages past the end)
+    int32_t entry = -1;
+    const int64_t entryAt = (int64_t)split * p.chunk + laneAt;
+    const int32_t* table = c.pageTable + b * c.tableStride;
+    if (a.window == 0 && entryAt < (int64_t)c.maxPages * P) entry = table[entryAt >> shift];
+
     const Range r = range_of(a, b);
     const int64_t lo64 = (int64_t)r.base + (int64_t)split * p.chunk;
     if (p.splits > 1 && lo64 >= r.len) return;  // the join knows
     const int32_t lo = (int32_t)lo64;
     const int32_t hi = r.len - lo < p.chunk ? r.len : lo + p.chunk;
 
-    // queries, 8 values of a row per lane and step
+    // queries, 8 values of a row per lane and step (a row that is not there
+    // computes row0's again, for nothing)
     u4 q[NT][NJ];
     int32_t begin[NT], end[NT];
 #pragma unroll
@@ -238,10 +281,7 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
         seen_by(a, r, row, p.rows, group, begin[nt], end[nt]);
         const uint16_t* src = (const uint16_t*)a.q.data + row_at(a.q, b, h, row < p.rows ? row : row0, group);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            q[nt][j] = *(const u4*)(src + dim_at<D>(j, g));
-            if (row >= p.rows) q[nt][j] = u4{0, 0, 0, 0};
-        }
+        for (int j = 0; j < NJ; ++j) q[nt][j] = *(const u4*)(src + dim_at<D>(j, g));
     }
     // tokens in [allBegin, allEnd) are seen by every row of the workgroup
     int32_t allBegin, allEnd, unused;
@@ -251,6 +291,7 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
         seen_by(a, r, row0, p.rows, group, unused, allEnd);
     }
 
+    const float scale2 = a.scale * kLog2e;  // scores in powers of two
     f4 o[NT][NB];
     float m[NT], ref[NT], l[NT];
 #pragma unroll
@@ -277,17 +318,17 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
         const int32_t segEnd = hi - seg < kSegment ? hi : seg + kSegment;
         // lane i holds page and scales of the wave's i-th half tile
         int32_t page = -1;
-        float kf = 0.0f, vf = 0.0f;
+        float kScale = 0.0f, vScale = 0.0f;
         {
-            const int32_t t = seg + ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
+            const int32_t t = seg + laneAt;
             if (t < segEnd && t + 16 > r.first) {
-                page = checked_page(c.pageTable[b * c.tableStride + t / P], c.numPages);
+                page = checked_page(a.window == 0 && seg == lo ? entry : table[t >> shift], c.numPages);
                 if (page < 0) {
                     report(a.err);
                 } else {
                     const int64_t block = (int64_t)page * c.heads + h;
-                    kf = c.kScale[block] * (a.scale * kLog2e);
-                    vf = c.vScale[block];
+                    kScale = c.kScale[block];
+                    vScale = c.vScale[block];
                 }
             }
         }
@@ -346,10 +387,10 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
             }
             const int32_t pg0 = __builtin_amdgcn_readlane(page, 2 * i);
             const int32_t pg1 = __builtin_amdgcn_readlane(page, 2 * i + 1);
-            const float kf0 = of_bits(__builtin_amdgcn_readlane(bits(kf), 2 * i));
-            const float kf1 = of_bits(__builtin_amdgcn_readlane(bits(kf), 2 * i + 1));
-            const float vf0 = of_bits(__builtin_amdgcn_readlane(bits(vf), 2 * i));
-            const float vf1 = of_bits(__builtin_amdgcn_readlane(bits(vf), 2 * i + 1));
+            const float kf0 = of_bits(__builtin_amdgcn_readlane(bits(kScale), 2 * i)) * scale2;
+            const float kf1 = of_bits(__builtin_amdgcn_readlane(bits(kScale), 2 * i + 1)) * scale2;
+            const float vf0 = of_bits(__builtin_amdgcn_readlane(bits(vScale), 2 * i));
+            const float vf1 = of_bits(__builtin_amdgcn_readlane(bits(vScale), 2 * i + 1));
             const bool whole = t0 >= allBegin && t0 + kTile <= allEnd && (pg0 | pg1) >= 0;
             bool grows = false;
 #pragma unroll
@@ -364,10 +405,8 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
                             s[nt][1][e] = -INFINITY;
                     }
                 }
-                if (p.scores != nullptr && n + nt * 16 < p.rows) {
-                    float* dst = p.scores +
-                                 ((int64_t)pair * p.rows + nt * 16 + n) * ((int64_t)p.splits * p.chunk) +
-                                 (t0 - r.base) + 4 * g;
+                if (p.scores != nullptr && row0 + nt * 16 + n < p.rows) {
+                    float* dst = score_at(p, pair, row0 + nt * 16 + n, t0 - r.base) + 4 * g;
                     *(f4*)dst = s[nt][0];
                     *(f4*)(dst + 16) = s[nt][1];
                 }
@@ -452,7 +491,6 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
         if (g == 0) sm[wave][nt * 16 + n] = m[nt], sl[wave][nt * 16 + n] = l[nt];
     }
     __syncthreads();
-    const bool direct = p.splits == 1;
     const int64_t part = ((int64_t)pair * p.splits + split) * p.rows;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -479,21 +517,9 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
                 ll += sl[w][nt * 16 + i] == 0.0f ? 0.0f : sl[w][nt * 16 + i] * exp2_(sm[w][nt * 16 + i] - mm);
-            if (direct) {
-                uint2 u = make_uint2(0, 0);
-                if (ll != 0.0f) {
-                    u.x = narrow<T>(sum.x / ll) | (narrow<T>(sum.y / ll) << 16);
-                    u.y = narrow<T>(sum.z / ll) | (narrow<T>(sum.w / ll) << 16);
-                }
-                *(uint2*)((uint16_t*)a.out.data + row_at(a.out, b, h, row, group) + d4 * 4) = u;
-                if (d4 == 0) {
-                    const float lse = ll != 0.0f ? mm + log2f(ll) : INFINITY;
-                    slse[nt * 16 + i] = lse;
-                    if (p.lse2 != nullptr) p.lse2[(int64_t)pair * p.rows + row] = lse;
-                    if (a.lse != nullptr)
-                        a.lse[((int64_t)b * a.nQuery + row / group) * a.headsQ + h * group + row % group] =
-                            ll != 0.0f ? lse * kLn2 : -INFINITY;
-                }
+            if (p.direct) {
+                write_row<T>(p, b, h, pair, row, d4, sum, mm, ll);
+                if (d4 == 0) slse[nt * 16 + i] = ll != 0.0f ? mm + log2f(ll) : INFINITY;
             } else {
                 *(f4*)(p.partO + (part + row) * D + d4 * 4) = sum;
                 if (d4 == 0) p.partML[part + row] = make_float2(mm, ll);
@@ -501,14 +527,13 @@ __global__ __launch_bounds__(kThreads, D * NT <= 256 ? 2 : 1) void kv8_k_attend(
         }
         __syncthreads();
     }
-    if (direct && p.scores != nullptr) {
+    if (p.direct && p.scores != nullptr) {
         // this workgroup has all scores of its head: add the weights at once
-        const float* sc = p.scores + (int64_t)pair * p.rows * p.chunk;
         float* w = c.weight + (int64_t)pair * c.weightStride;
         for (int32_t t = r.first + (int32_t)threadIdx.x; t < r.len; t += kThreads) {
             float sum = 0.0f;
             for (int32_t i = 0; i < p.rows; ++i)
-                sum += exp2_(sc[(int64_t)i * p.chunk + (t - r.base)] - slse[i]);
+                sum += exp2_(score_at(p, pair, 0, t - r.base)[i * kTile] - slse[i]);
             w[t] += sum;
         }
     }
@@ -524,119 +549,118 @@ __device__ __forceinline__ void merge(float& top, float& all, float top2, float 
     all = x + y;
 }
 
-// Join the runs of a sequence's tokens.  A (sequence, cache head) has joinRows
-// workgroups that take its rows in turn (out and lse) and joinTokens that take
-// its tokens (weights, from the stored scores).
+// Join the runs of a sequence's tokens: rows (out and lse), four to a
+// workgroup, or one where there are many runs; and tokens (weights, from the
+// stored scores).  Starting the workgroups is most of the time, so they are
+// few: a workgroup a row took 10 us for 2048 rows of 2 runs.
 template <int T>
 __global__ __launch_bounds__(kThreads) void kv8_k_join(Plan p, int32_t D)
 {
     __shared__ f4 sum[kThreads];
     __shared__ float factor[kThreads];
-    __shared__ float wm[kWaves], wl[kWaves];
     const ccb::Kv8AttendArgs& a = p.a;
     const ccbKv8Cache& c = a.c;
-    const int32_t pair = blockIdx.x % (uint32_t)p.pairs;
-    const int32_t part = blockIdx.x / (uint32_t)p.pairs;
-    const int32_t h = pair % c.heads, b = pair / c.heads, group = a.headsQ / c.heads;
-    const int tid = threadIdx.x;
-    const Range r = range_of(a, b);
-    const int32_t n = (r.len - r.base + p.chunk - 1) / p.chunk;  // runs that hold tokens
-    const float2* ml = p.partML + (int64_t)pair * p.splits * p.rows;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int32_t V = D / 4;  // vectors of a row
+    const int64_t step = (int64_t)p.rows * D;
 
-    if (part < p.joinRows) {
-        const int32_t V = D / 4, groups = kThreads / V;  // vectors of a row, runs summed side by side
-        const int32_t d4 = tid % V, sg = tid / V;
-        for (int32_t row = part; row < p.rows; row += p.joinRows) {
-            float top = -INFINITY, all = 0.0f;
-            for (int32_t s = tid; s < n; s += kThreads) {
-                const float2 x = ml[(int64_t)s * p.rows + row];
-                merge(top, all, x.x, x.y);
-            }
+    if (blockIdx.x < (uint32_t)p.joinRows) {
+        const bool many = p.splits > kJoinRuns;
+        const int64_t at = many ? blockIdx.x : (int64_t)blockIdx.x * kWaves + wave;
+        const int32_t pair = (int32_t)(at / p.rows), row = (int32_t)(at % p.rows);
+        if (pair >= p.pairs) return;  // (not where the workgroup works together)
+        const int32_t h = pair % c.heads, b = pair / c.heads;
+        const Range r = range_of(a, b);
+        const int32_t n = (r.len - r.base + p.chunk - 1) / p.chunk;  // runs that hold tokens
+        const float2* ml = p.partML + (int64_t)pair * p.splits * p.rows + row;
+        float top = -INFINITY, all = 0.0f;
+        for (int32_t s = lane; s < n; s += 64) {
+            const float2 x = ml[(int64_t)s * p.rows];
+            merge(top, all, x.x, x.y);
+        }
 #pragma unroll
-            for (int d = 32; d >= 1; d >>= 1)
-                merge(top, all, __shfl_xor(top, d, 64), __shfl_xor(all, d, 64));
-            if ((tid & 63) == 0) wm[tid >> 6] = top, wl[tid >> 6] = all;
-            __syncthreads();
-            top = wm[0], all = wl[0];
+        for (int d = 32; d >= 1; d >>= 1) merge(top, all, __shfl_xor(top, d, 64), __shfl_xor(all, d, 64));
+        // threads of a row: V for the vectors, and runs side by side
+        const int32_t me = many ? tid : lane, groups = (many ? kThreads : 64) / V;
+        const int32_t d4 = me % V, sg = me / V;
+        const float* src = p.partO + ((int64_t)pair * p.splits * p.rows + row) * D + d4 * 4;
+        f4 o = {0, 0, 0, 0};
+        if (sg < groups) {
+            int32_t s = sg;
+            for (; s + 7 * groups < n; s += 8 * groups) {  // 8 loads in flight
+                f4 v[8];
+                float2 x[8];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) merge(top, all, wm[w], wl[w]);
-            f4 o = {0, 0, 0, 0};
-            for (int32_t s0 = 0; s0 < n; s0 += kThreads) {
-                const int32_t mine = s0 + tid;
-                const float2 x = mine < n ? ml[(int64_t)mine * p.rows + row] : make_float2(0.0f, 0.0f);
-                factor[tid] = x.y == 0.0f ? 0.0f : exp2_(x.x - top);
-                __syncthreads();
-                const int32_t here = n - s0 < kThreads ? n - s0 : kThreads;
-                const float* src = p.partO + (((int64_t)pair * p.splits + s0) * p.rows + row) * D + d4 * 4;
-                const int64_t step = (int64_t)p.rows * D;
-                if (sg < groups) {
-                    int32_t s = sg;
-                    for (; s + 7 * groups < here; s += 8 * groups) {  // 8 loads in flight
-                        f4 v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = *(const f4*)(src + (s + i * groups) * step);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o += v[i] * factor[s + i * groups];
-                    }
-                    for (; s < here; s += groups) o += *(const f4*)(src + s * step) * factor[s];
+                for (int i = 0; i < 8; ++i) {
+                    v[i] = *(const f4*)(src + (s + i * groups) * step);
+                    x[i] = ml[(int64_t)(s + i * groups) * p.rows];
                 }
-                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o += v[i] * (x[i].y == 0.0f ? 0.0f : exp2_(x[i].x - top));
             }
-            sum[tid] = o;
-            __syncthreads();
-            if (tid < V) {
-                for (int32_t i = 1; i < groups; ++i) o += sum[i * V + d4];
-                uint2 u = make_uint2(0, 0);
-                if (all != 0.0f) {
-                    u.x = narrow<T>(o.x / all) | (narrow<T>(o.y / all) << 16);
-                    u.y = narrow<T>(o.z / all) | (narrow<T>(o.w / all) << 16);
-                }
-                *(uint2*)((uint16_t*)a.out.data + row_at(a.out, b, h, row, group) + d4 * 4) = u;
-                if (tid == 0) {
-                    const float lse = all != 0.0f ? top + log2f(all) : INFINITY;
-                    if (p.lse2 != nullptr) p.lse2[(int64_t)pair * p.rows + row] = lse;
-                    if (a.lse != nullptr)
-                        a.lse[((int64_t)b * a.nQuery + row / group) * a.headsQ + h * group + row % group] =
-                            all != 0.0f ? lse * kLn2 : -INFINITY;
-                }
+            for (; s < n; s += groups) {
+                const float2 x = ml[(int64_t)s * p.rows];
+                o += *(const f4*)(src + s * step) * (x.y == 0.0f ? 0.0f : exp2_(x.x - top));
             }
-            __syncthreads();
+        }
+        sum[tid] = o;
+        if (many) __syncthreads();
+        if (me < V) {
+            for (int32_t i = 1; i < groups; ++i) o += sum[(tid - me) + i * V + d4];
+            write_row<T>(p, b, h, pair, row, d4, o, top, all);
         }
         return;
     }
-    const int32_t from = (part - p.joinRows) * kJoinTokens;  // from base
+    const int32_t pair = (blockIdx.x - p.joinRows) % (uint32_t)p.pairs;
+    const int32_t from = (int32_t)((blockIdx.x - p.joinRows) / (uint32_t)p.pairs) * p.joinSpan;  // from base
+    const Range r = range_of(a, pair / c.heads);
     if (r.base + (int64_t)from >= r.len) return;
-    // every row's lse, by 16 threads each
-    {
-        const int32_t row = tid >> 4;
+    const int32_t n = (r.len - r.base + p.chunk - 1) / p.chunk;
+    const float2* ml = p.partML + (int64_t)pair * p.splits * p.rows;
+    // every row's lse: 16 threads each, or one for many rows of few runs
+    const int32_t team = n <= 16 && p.rows > 16 ? 1 : 16;
+    for (int32_t row = tid / team; row < p.rows; row += kThreads / team) {
         float top = -INFINITY, all = 0.0f;
-        if (row < p.rows) {
 #pragma unroll 8
-            for (int32_t s = tid & 15; s < n; s += 16) {
-                const float2 x = ml[(int64_t)s * p.rows + row];
-                merge(top, all, x.x, x.y);
-            }
+        for (int32_t s = tid % team; s < n; s += team) {
+            const float2 x = ml[(int64_t)s * p.rows + row];
+            merge(top, all, x.x, x.y);
         }
-#pragma unroll
-        for (int d = 8; d >= 1; d >>= 1) merge(top, all, __shfl_xor(top, d, 64), __shfl_xor(all, d, 64));
-        if ((tid & 15) == 0) factor[row] = all != 0.0f ? top + log2f(all) : INFINITY;
+        for (int d = team >> 1; d >= 1; d >>= 1)
+            merge(top, all, __shfl_xor(top, d, 64), __shfl_xor(all, d, 64));
+        if (tid % team == 0) factor[row] = all != 0.0f ? top + log2f(all) : INFINITY;
     }
     __syncthreads();
-    const int64_t stride = (int64_t)p.splits * p.chunk;
-    const int32_t t = r.base + from + 4 * tid;
-    if (t >= r.len) return;
-    const float* sc = p.scores + (int64_t)pair * p.rows * stride + from + 4 * tid;
+    // A lane takes four tokens.  Few rows: every thread its own tokens and all
+    // rows; many: a wave takes every fourth row of the same 256 tokens, so that
+    // the loads of a row do not queue up behind each other.
+    const bool shared = p.joinSpan == 4 * 64;
+    const int32_t at = from + 4 * (shared ? lane : tid), by = shared ? kWaves : 1;
+    const float* sc = score_at(p, pair, 0, at);
     float* w = c.weight + (int64_t)pair * c.weightStride;
     f4 x = {0, 0, 0, 0};
+    if (r.base + (int64_t)at < r.len) {
 #pragma unroll 4
-    for (int32_t i = 0; i < p.rows; ++i) {
-        const f4 s = *(const f4*)(sc + i * stride);
+        for (int32_t i = shared ? wave : 0; i < p.rows; i += by) {
+            const f4 s = *(const f4*)(sc + i * kTile);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] += exp2_(s[e] - factor[i]);
+            for (int e = 0; e < 4; ++e) x[e] += exp2_(s[e] - factor[i]);
+        }
     }
+    if (shared) {
+        sum[tid] = x;
+        __syncthreads();
+        const int32_t t = r.base + from + tid;  // now a thread to a token
+        const float* one = (const float*)sum;
+        if (t >= r.first && t < r.len)
+            w[t] += (one[tid] + one[256 + tid]) + (one[512 + tid] + one[768 + tid]);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (t + e >= r.first && t + e < r.len) w[t + e] += x[e];
+        for (int e = 0; e < 4; ++e) {
+            const int32_t t = r.base + at + e;
+            if (t >= r.first && t < r.len) w[t] += x[e];
+        }
+    }
 }
 
 // Weights of many rows: the scores again, S = Q K^T so that a token's rows lie
@@ -717,8 +741,6 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
     const int64_t rows = (int64_t)nQuery * (headsQ / c.heads);
     p.pairs = (int32_t)pairs;
     p.rows = (int32_t)rows;
-    p.tilesN = rows <= 16 ? 1 : (rows <= 32 || c.headDim > 128) ? 2 : 4;
-    p.rowBlocks = (int32_t)((rows + 16 * p.tilesN - 1) / (16 * p.tilesN));
     // tokens that a sequence's queries may see, from a tile's border
     const int64_t room = (int64_t)c.maxPages * c.pageSize;
     int64_t span = room;
@@ -727,29 +749,46 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
     constexpr int64_t unit = kWaves * kTile;
     constexpr int64_t target = 1024;  // workgroups: four on a CU at head size 128
     auto up = [](int64_t x, int64_t by) { return (x + by - 1) / by; };
+    // Two tiles of rows share a key's conversion, which pays (10% for 64 rows)
+    // where their accumulators leave room for enough waves, and where a
+    // workgroup more for the other rows would have to wait for its place.
+    const int64_t tiles = up(rows, 16);
+    p.tilesN = rows > 16 && c.headDim <= 96 && pairs * up(span, unit) * tiles > target ? 2 : 1;
+    p.rowBlocks = (int32_t)up(rows, 16 * p.tilesN);
     int64_t most = target / (pairs * p.rowBlocks);
     if (most < 1) most = 1;
     p.chunk = (int32_t)(up(up(span, most), unit) * unit);
     if (span <= 256) p.chunk = (int32_t)(up(span, unit) * unit);
     p.splits = (int32_t)up(span, p.chunk);
-    const int64_t mostSplits = most < up(room, unit) ? most : up(room, unit);
-    const int64_t mostTokens = room + up(room, most) + unit;  // >= splits * chunk
+    // bounds over every window: on splits, and on splits * chunk
+    int64_t mostSplits = pairs < target ? target / pairs : 1;
+    mostSplits = mostSplits < up(room, unit) ? mostSplits : up(room, unit);
+    const int64_t extra = mostSplits * (unit + 1);
+    const int64_t mostTokens = room + unit + (extra < room ? extra : room);
     size_t bytes = 0;
     auto take = [&](int64_t n, size_t each) {
         char* here = (char*)ws + bytes;
         bytes += ((size_t)n * each + 127) / 128 * 128;
         return here;
     };
-    const int64_t parts = mostSplits > 1 ? pairs * mostSplits * rows : 0;
+    // Scores are kept for the weights where that moves less than reading the
+    // keys again (8 bytes a row and token against headDim a token), and for up
+    // to 64 rows where all of them stay in the caches: there a launch less
+    // counts for more.
+    const bool stored = accumulate && (rows <= 16 || (rows <= 64 && pairs * rows * room * 4 <= (32 << 20)));
+    p.direct = p.splits == 1 && (p.rowBlocks == 1 || !stored);
+    const int64_t parts = mostSplits > 1 || rows > 16 ? pairs * mostSplits * rows : 0;
     p.partO = (float*)take(parts * c.headDim, sizeof(float));
     p.partML = (float2*)take(parts, sizeof(float2));
     p.scores = nullptr, p.lse2 = nullptr;
-    if (accumulate && rows <= kStoredRows)
+    if (stored)
         p.scores = (float*)take(pairs * rows * (mostTokens / 4 + 1), 4 * sizeof(float));
     else if (accumulate)
         p.lse2 = (float*)take(pairs * rows, sizeof(float));
-    p.joinRows = (int32_t)(rows < 64 ? rows : 64);
-    p.joinTokens = p.scores != nullptr ? (int32_t)up((int64_t)p.splits * p.chunk, kJoinTokens) : 0;
+    const int64_t tokens = (int64_t)p.splits * p.chunk;
+    p.joinRows = (int32_t)(p.splits > kJoinRuns ? pairs * rows : up(pairs * rows, kWaves));
+    p.joinSpan = rows <= 16 ? 4 * kThreads : 4 * 64;
+    p.joinBlocks = p.joinRows + (p.scores != nullptr ? pairs * up(tokens, p.joinSpan) : 0);
     return bytes;
 }
 
@@ -759,13 +798,11 @@ hipError_t launch(const Plan& p, int64_t blocks, hipStream_t s)
     const dim3 grid((unsigned)blocks), block(kThreads);
     if (p.tilesN == 1)
         kv8_k_attend<F, T, D, 1><<<grid, block, 0, s>>>(p);
-    else if (p.tilesN == 2)
+    else if constexpr (D <= 96)
         kv8_k_attend<F, T, D, 2><<<grid, block, 0, s>>>(p);
-    else if constexpr (D <= 128)
-        kv8_k_attend<F, T, D, 4><<<grid, block, 0, s>>>(p);
     const int64_t pairs = (int64_t)p.a.c.batch * p.a.c.heads;
-    if (p.splits > 1)
-        kv8_k_join<T><<<dim3((unsigned)(pairs * (p.joinRows + p.joinTokens))), block, 0, s>>>(p, D);
+    if (!p.direct)
+        kv8_k_join<T><<<dim3((unsigned)p.joinBlocks), block, 0, s>>>(p, D);
     if (p.lse2 != nullptr) {
         const int64_t span = (int64_t)p.splits * p.chunk;
         int64_t each = (span + kWaves * kTile - 1) / (kWaves * kTile);
@@ -795,7 +832,7 @@ hipError_t kv8_attend(const Kv8AttendArgs& a, int numCUs, hipStream_t s)
     make_plan(p, c, a.headsQ, a.nQuery, a.window, a.accumulate, a.ws);
     const int64_t pairs = (int64_t)c.batch * c.heads;
     const int64_t blocks = pairs * p.rowBlocks * p.splits;
-    if (blocks > INT32_MAX || pairs * (p.joinRows + (int64_t)p.joinTokens) > INT32_MAX) return hipErrorInvalidValue;
+    if (blocks > INT32_MAX || pairs * p.rows > INT32_MAX || p.joinBlocks > INT32_MAX) return hipErrorInvalidValue;
 #define KV8_ATTEND_DIM(F, T) \
     switch (c.headDim) { \
     case 64: return launch<F, T, 64>(p, blocks, s); \

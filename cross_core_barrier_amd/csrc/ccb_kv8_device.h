@@ -73,17 +73,31 @@ __device__ __forceinline__ uint32_t narrow(float x)
 }
 
 // Whether quotients were too near a border between two codes to be sure.
-// t = x * inv is within 2^-22 of the quotient; unsure is, for int8, within
-// 2^-14 of a border, and for e4m3 within 16 units of t's last place, or below
-// 2^-6, where the step no longer follows the exponent.
+// t, a product with 1 / s, is off by three roundings at most: 3 * 2^-24 of it.
+// Unsure is, for int8, within 2^-15 of a border (t <= 127: 2^-15.4), and for
+// e4m3 within 4 units of t's last place.  e4m3's step is the exponent's from
+// 2^-6 on and stays 2^-9 below: smaller quotients are looked at again, raised
+// by 2^-6 into the binade that has this step.
 template <int F>
 struct Near {
-    float d = 0.0f;                     // int8: largest distance to a code
+    float d = 0.0f;                      // int8: largest distance to a code
     uint32_t border = ~0u, small = ~0u;  // e4m3: place above a border's zone, size
-    __device__ __forceinline__ bool unsure() const
+    static constexpr uint32_t kZone = 4;
+    __device__ __forceinline__ void look(uint32_t u)
     {
-        if constexpr (F == kInt8) return d > 0.5f - 0x1p-14f;
-        return border <= 32u << 12 || small < (0x3c800000u << 1) - 1;
+        // the 20 bits below e4m3's three, 0 where a border's zone begins
+        const uint32_t above = (u - (0x80000u - kZone)) << 12;
+        border = above < border ? above : border;
+    }
+    __device__ __forceinline__ bool unsure(const float* t)
+    {
+        if constexpr (F == kInt8) return d > 0.5f - 0x1p-15f;
+        if (small < (0x3c800000u << 1) - 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (fabsf(t[i]) < 0x1p-6f) look(bits(fabsf(t[i]) + 0x1p-6f));
+        }
+        return border <= (2 * kZone) << 12;
     }
 };
 
@@ -109,10 +123,8 @@ __device__ __forceinline__ uint32_t encode4_near(const float* t, Near<F>& near)
         for (int i = 0; i < 4; ++i) {
             c[i] = __builtin_amdgcn_fmed3f(t[i], -448.0f, 448.0f);
             const uint32_t u = bits(c[i]);
-            // the 20 bits below e4m3's three, 0 at 16 units before the border
-            const uint32_t above = (u - (0x80000u - 16u)) << 12;
             const uint32_t size = (u << 1) - 1;  // a 0 is not small
-            near.border = above < near.border ? above : near.border;
+            near.look(u);
             near.small = size < near.small ? size : near.small;
         }
         const int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
@@ -133,7 +145,7 @@ __device__ __forceinline__ uint2 encode8(const float* x, float inv, float s)
         odd = fmaf(x[i], 0.0f, odd);  // NaN if any value is NaN or infinite
     }
     uint2 u = make_uint2(encode4_near<F>(t, near), encode4_near<F>(t + 4, near));
-    if (near.unsure() || odd != odd || s > 0x1p120f) {  // (there 1 / s loses bits)
+    if (near.unsure(t) || odd != odd || s > 0x1p120f) {  // (there 1 / s loses bits)
         u = make_uint2(0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -157,7 +169,7 @@ __device__ __forceinline__ uint2 encode8_again(const uint2& w, float sOld, float
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = v[i] * ratio;
     uint2 u = make_uint2(encode4_near<F>(t, near), encode4_near<F>(t + 4, near));
-    if (near.unsure() || s > 0x1p120f) {
+    if (near.unsure(t) || s > 0x1p120f) {
         u = make_uint2(0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
