@@ -3,13 +3,11 @@
 //
 // The rows of one cache head (its queries and query heads) share every key
 // and value, so one workgroup takes a (sequence, cache head, run of tokens)
-// and up to 16 * NT rows.  Its four waves take 32-token tiles in turn and
+// and up to 16 * NT rows.  Its eight waves take 32-token tiles in turn and
 // never wait for one another in the loop: a wave streams its own tiles into
 // its own part of LDS (16 bytes per lane, straight from memory; the next
 // tile's keys are on their way as soon as this one's are read, and its values
-// likewise) and keeps its own running maximum, sum and weighted values.  Rings
-// of two tiles leave room for two workgroups on a CU instead of four and
-// measured slower: 32 against 24 us for 16 sequences of up to 4096 tokens.
+// likewise) and keeps its own running maximum, sum and weighted values.
 //
 // S^T = K Q^T and O^T = V^T P^T on 16x16x32 tiles.  In that order a row of
 // scores lies on one lane index (lane % 16), so the softmax needs no
@@ -38,8 +36,11 @@ using namespace kv8;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kTile = 32;                     // tokens of a wave's step
-constexpr int kSegment = 32 * kWaves * kTile;  // tokens whose pages fit a wave's lanes
+constexpr int kRunThreads = 512;  // of a workgroup that takes a run of tokens
+constexpr int kRunWaves = kRunThreads / 64;
+constexpr int kTile = 32;                        // tokens of a wave's step
+constexpr int kRunUnit = kRunWaves * kTile;
+constexpr int kSegment = 32 * kRunWaves * kTile;  // tokens whose pages fit a wave's lanes
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kJoinRuns = 32;  // more of them are joined by a workgroup, not a wave
@@ -59,8 +60,8 @@ struct Plan {
     int32_t rows;       // of a cache head
     int32_t tilesN;     // NT
     int32_t rowBlocks;  // workgroups that share a run of tokens
-    int32_t chunk;      // tokens of a workgroup, a multiple of kWaves * kTile
-    int32_t splits;     // runs a sequence may have
+    int32_t splits;     // runs of a sequence, see range_of
+    int32_t tiles;      // a sequence may have
     bool direct;        // one run: its workgroup writes the results
     int32_t joinRows;   // workgroups of the join for the rows
     int64_t joinBlocks; // all of the join's, those for the tokens among them,
@@ -134,19 +135,24 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 // side by side, so that what a wave stores is one piece of memory.
 __device__ __forceinline__ float* score_at(const Plan& p, int32_t pair, int32_t row, int32_t t)
 {
-    const int64_t tile = (int64_t)pair * ((int64_t)p.splits * (p.chunk / kTile)) + t / kTile;
+    const int64_t tile = (int64_t)pair * p.tiles + t / kTile;
     return p.scores + (tile * p.rows + row) * kTile + t % kTile;
 }
 
-// Sequence, head and what the rows of a workgroup may see.
+// What a sequence's queries may see, and its runs.  Every sequence has
+// p.splits of them, as long as its own length asks: the capacity, which is all
+// that the host knows, may be many times what a sequence holds.
 struct Range {
     int32_t len;    // 0 where the length is bad
     int32_t first;  // first token any query sees
     int32_t base;   // first, at a tile's border: where the runs start
+    int32_t chunk;  // tokens of a run, a multiple of kRunUnit
+    int32_t runs;   // that hold tokens
 };
 
-__device__ __forceinline__ Range range_of(const ccb::Kv8AttendArgs& a, int32_t b)
+__device__ __forceinline__ Range range_of(const Plan& p, int32_t b)
 {
+    const ccb::Kv8AttendArgs& a = p.a;
     Range r;
     r.len = checked_len(a.c.lens[b], a.c.maxPages * a.c.pageSize);
     if (r.len < 0) {
@@ -156,6 +162,9 @@ __device__ __forceinline__ Range range_of(const ccb::Kv8AttendArgs& a, int32_t b
     const int64_t f = a.window > 0 ? (int64_t)r.len - a.nQuery + 1 - a.window : 0;
     r.first = f > 0 ? (int32_t)f : 0;
     r.base = r.first & ~(kTile - 1);
+    const uint32_t held = (uint32_t)(r.len - r.base), splits = (uint32_t)p.splits;
+    r.chunk = (int32_t)(((held + splits * kRunUnit - 1) / (splits * kRunUnit)) * kRunUnit);
+    r.runs = r.chunk > 0 ? (int32_t)((held + (uint32_t)r.chunk - 1) / (uint32_t)r.chunk) : 0;
     return r;
 }
 
@@ -231,15 +240,15 @@ __device__ __forceinline__ void write_row(const Plan& p, int32_t b, int32_t h, i
 }
 
 template <int F, int T, int D, int NT>
-__global__ __launch_bounds__(kThreads, 2) void kv8_k_attend(Plan p)
+__global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_k_attend(Plan p)
 {
     constexpr int C = D / 16;             // chunks of 16 codes in a token
     constexpr int NI = kTile * C / 64;    // loads of a wave for a tile of keys
     constexpr int NB = D / 16;            // blocks of 16 dimensions
     constexpr int NJ = D / 32;            // steps of the first product
-    __shared__ __attribute__((aligned(16))) uint8_t kBuf[kWaves][kTile * D];
-    __shared__ __attribute__((aligned(16))) uint8_t vBuf[kWaves][kTile * D];
-    __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT], slse[16 * NT];
+    __shared__ __attribute__((aligned(16))) uint8_t kBuf[kRunWaves][kTile * D];
+    __shared__ __attribute__((aligned(16))) uint8_t vBuf[kRunWaves][kTile * D];
+    __shared__ float sm[kRunWaves][16 * NT], sl[kRunWaves][16 * NT], slse[16 * NT];
 
     const ccb::Kv8AttendArgs& a = p.a;
     const ccbKv8Cache& c = a.c;
@@ -257,19 +266,18 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_k_attend(Plan p)
 
     // lane i's place in a segment: the wave's i-th half tile
     const int32_t shift = __builtin_ctz(P);
-    const int32_t laneAt = ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
-    // without a window the runs' places do not depend on the length: the first
-    // page numbers are fetched beside it (they may be of pages past the end)
+    const int32_t laneAt = ((lane >> 1) * kRunWaves + wave) * kTile + (lane & 1) * 16;
+    // without a window a single run's place does not depend on the length: the
+    // first page numbers are fetched beside it (they may be of pages past the end)
     int32_t entry = -1;
-    const int64_t entryAt = (int64_t)split * p.chunk + laneAt;
+    const bool early = a.window == 0 && p.splits == 1;
     const int32_t* table = c.pageTable + b * c.tableStride;
-    if (a.window == 0 && entryAt < (int64_t)c.maxPages * P) entry = table[entryAt >> shift];
+    if (early && laneAt < c.maxPages * P) entry = table[laneAt >> shift];
 
-    const Range r = range_of(a, b);
-    const int64_t lo64 = (int64_t)r.base + (int64_t)split * p.chunk;
-    if (p.splits > 1 && lo64 >= r.len) return;  // the join knows
-    const int32_t lo = (int32_t)lo64;
-    const int32_t hi = r.len - lo < p.chunk ? r.len : lo + p.chunk;
+    const Range r = range_of(p, b);
+    if (split > 0 && split >= r.runs) return;  // the join knows
+    const int32_t lo = r.base + split * r.chunk;
+    const int32_t hi = r.len - lo < r.chunk ? r.len : lo + r.chunk;
 
     // queries, 8 values of a row per lane and step (a row that is not there
     // computes row0's again, for nothing)
@@ -322,7 +330,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_k_attend(Plan p)
         {
             const int32_t t = seg + laneAt;
             if (t < segEnd && t + 16 > r.first) {
-                page = checked_page(a.window == 0 && seg == lo ? entry : table[t >> shift], c.numPages);
+                page = checked_page(early && seg == lo ? entry : table[t >> shift], c.numPages);
                 if (page < 0) {
                     report(a.err);
                 } else {
@@ -332,10 +340,10 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_k_attend(Plan p)
                 }
             }
         }
-        const int32_t nTiles = ((segEnd - seg + kTile - 1) / kTile - wave + kWaves - 1) / kWaves;
+        const int32_t nTiles = ((segEnd - seg + kTile - 1) / kTile - wave + kRunWaves - 1) / kRunWaves;
 
         auto issue = [&](const void* codes, int32_t i, uint8_t* buf) {
-            const int32_t t = seg + (i * kWaves + wave) * kTile;
+            const int32_t t = seg + (i * kRunWaves + wave) * kTile;
             const uint8_t* src[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -353,7 +361,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_k_attend(Plan p)
         };
 
         auto step = [&](int32_t i, uint8_t* kb, uint8_t* vb) {
-            const int32_t t0 = seg + (i * kWaves + wave) * kTile;
+            const int32_t t0 = seg + (i * kRunWaves + wave) * kTile;
             const bool more = i + 1 < nTiles;
             // scores
             wait_loads<NI>();
@@ -496,26 +504,26 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_k_attend(Plan p)
     for (int nt = 0; nt < NT; ++nt) {
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][nt * 16 + n]);
+        for (int w = 0; w < kRunWaves; ++w) top = fmaxf(top, sm[w][nt * 16 + n]);
         const float f = l[nt] == 0.0f ? 0.0f : exp2_(m[nt] - top);  // (a NaN stays)
         // chunks of 4 dimensions are swapped so that rows fall on different banks
-        float* dst = (float*)(wave < 2 ? kBuf[0] : vBuf[0]) + ((wave & 1) * 16 + n) * D;
+        float* dst = (float*)(wave < kRunWaves / 2 ? kBuf[0] : vBuf[0]) + (wave % (kRunWaves / 2) * 16 + n) * D;
 #pragma unroll
         for (int d = 0; d < NB; ++d) *(f4*)(dst + (((4 * d + g) ^ (n & 7)) * 4)) = o[nt][d] * f;
         __syncthreads();
-        for (int32_t at = threadIdx.x; at < 4 * D; at += kThreads) {
+        for (int32_t at = threadIdx.x; at < 4 * D; at += kRunThreads) {
             const int32_t i = at / (D / 4), d4 = at % (D / 4), row = row0 + nt * 16 + i;
             if (row >= p.rows) continue;
             f4 sum = {0, 0, 0, 0};
             float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                sum += *(const f4*)((const float*)(w < 2 ? kBuf[0] : vBuf[0]) + ((w & 1) * 16 + i) * D +
+            for (int w = 0; w < kRunWaves; ++w) {
+                sum += *(const f4*)((const float*)(w < kRunWaves / 2 ? kBuf[0] : vBuf[0]) + (w % (kRunWaves / 2) * 16 + i) * D +
                                     ((d4 ^ (i & 7)) * 4));
                 mm = fmaxf(mm, sm[w][nt * 16 + i]);
             }
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
+            for (int w = 0; w < kRunWaves; ++w)
                 ll += sl[w][nt * 16 + i] == 0.0f ? 0.0f : sl[w][nt * 16 + i] * exp2_(sm[w][nt * 16 + i] - mm);
             if (p.direct) {
                 write_row<T>(p, b, h, pair, row, d4, sum, mm, ll);
@@ -530,7 +538,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv8_k_attend(Plan p)
     if (p.direct && p.scores != nullptr) {
         // this workgroup has all scores of its head: add the weights at once
         float* w = c.weight + (int64_t)pair * c.weightStride;
-        for (int32_t t = r.first + (int32_t)threadIdx.x; t < r.len; t += kThreads) {
+        for (int32_t t = r.first + (int32_t)threadIdx.x; t < r.len; t += kRunThreads) {
             float sum = 0.0f;
             for (int32_t i = 0; i < p.rows; ++i)
                 sum += exp2_(score_at(p, pair, 0, t - r.base)[i * kTile] - slse[i]);
@@ -570,8 +578,8 @@ __global__ __launch_bounds__(kThreads) void kv8_k_join(Plan p, int32_t D)
         const int32_t pair = (int32_t)(at / p.rows), row = (int32_t)(at % p.rows);
         if (pair >= p.pairs) return;  // (not where the workgroup works together)
         const int32_t h = pair % c.heads, b = pair / c.heads;
-        const Range r = range_of(a, b);
-        const int32_t n = (r.len - r.base + p.chunk - 1) / p.chunk;  // runs that hold tokens
+        const Range r = range_of(p, b);
+        const int32_t n = r.runs;
         const float2* ml = p.partML + (int64_t)pair * p.splits * p.rows + row;
         float top = -INFINITY, all = 0.0f;
         for (int32_t s = lane; s < n; s += 64) {
@@ -613,9 +621,9 @@ __global__ __launch_bounds__(kThreads) void kv8_k_join(Plan p, int32_t D)
     }
     const int32_t pair = (blockIdx.x - p.joinRows) % (uint32_t)p.pairs;
     const int32_t from = (int32_t)((blockIdx.x - p.joinRows) / (uint32_t)p.pairs) * p.joinSpan;  // from base
-    const Range r = range_of(a, pair / c.heads);
+    const Range r = range_of(p, pair / c.heads);
     if (r.base + (int64_t)from >= r.len) return;
-    const int32_t n = (r.len - r.base + p.chunk - 1) / p.chunk;
+    const int32_t n = r.runs;
     const float2* ml = p.partML + (int64_t)pair * p.splits * p.rows;
     // every row's lse: 16 threads each, or one for many rows of few runs
     const int32_t team = n <= 16 && p.rows > 16 ? 1 : 16;
@@ -676,7 +684,7 @@ __global__ __launch_bounds__(kThreads) void kv8_k_weights(Plan p, int32_t blocks
     const int32_t P = c.pageSize, group = a.headsQ / c.heads;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int n = lane & 15, g = lane >> 4;
-    const Range r = range_of(a, b);
+    const Range r = range_of(p, b);
     for (int64_t from = (int64_t)r.base + ((int64_t)part * kWaves + wave) * kTile;
          from < r.len; from += (int64_t)blocks * kWaves * kTile) {
         u4 k[2][NJ];
@@ -746,25 +754,30 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
     int64_t span = room;
     if (window > 0 && (int64_t)window + nQuery - 1 + kTile < span)
         span = (int64_t)window + nQuery - 1 + kTile;
-    constexpr int64_t unit = kWaves * kTile;
-    constexpr int64_t target = 1024;  // workgroups: four on a CU at head size 128
+    // One workgroup of 8 waves for each CU: starting workgroups takes about 5 ns
+    // each, a round of them as long as their first loads, and both happen once
+    // this way.  Against two (of 8 waves, or four of 4) a CU, 16 sequences of
+    // 4096 tokens take 28.5 us instead of 31.1; where lengths spread from 500 to
+    // 4096 it is 26.4 instead of 25.2.  More, up to 16 a CU, where a run could
+    // pass 2 MB of codes: many short sequences do not wait for a long one's end.
+    constexpr int64_t target = 256, limit = 16 * target;
     auto up = [](int64_t x, int64_t by) { return (x + by - 1) / by; };
+    auto runs = [&](int64_t tokens, int64_t groups) {
+        const int64_t byLength = up(tokens, (1 << 20) / c.headDim), mostHere = limit / groups;
+        int64_t n = byLength < mostHere ? byLength : mostHere;
+        n = n > target / groups ? n : target / groups;
+        n = n < up(tokens, kRunUnit) ? n : up(tokens, kRunUnit);
+        return n > 1 && tokens > 256 ? n : 1;
+    };
     // Two tiles of rows share a key's conversion, which pays (10% for 64 rows)
     // where their accumulators leave room for enough waves, and where a
     // workgroup more for the other rows would have to wait for its place.
-    const int64_t tiles = up(rows, 16);
-    p.tilesN = rows > 16 && c.headDim <= 96 && pairs * up(span, unit) * tiles > target ? 2 : 1;
+    const int64_t tilesOfRows = up(rows, 16);
+    p.tilesN = rows > 16 && c.headDim <= 96 && pairs * up(span, kRunUnit) * tilesOfRows > target ? 2 : 1;
     p.rowBlocks = (int32_t)up(rows, 16 * p.tilesN);
-    int64_t most = target / (pairs * p.rowBlocks);
-    if (most < 1) most = 1;
-    p.chunk = (int32_t)(up(up(span, most), unit) * unit);
-    if (span <= 256) p.chunk = (int32_t)(up(span, unit) * unit);
-    p.splits = (int32_t)up(span, p.chunk);
-    // bounds over every window: on splits, and on splits * chunk
-    int64_t mostSplits = pairs < target ? target / pairs : 1;
-    mostSplits = mostSplits < up(room, unit) ? mostSplits : up(room, unit);
-    const int64_t extra = mostSplits * (unit + 1);
-    const int64_t mostTokens = room + unit + (extra < room ? extra : room);
+    p.splits = (int32_t)runs(span, pairs * p.rowBlocks);
+    p.tiles = (int32_t)up(span, kTile);
+    const int64_t mostSplits = runs(room, pairs);  // over every window
     size_t bytes = 0;
     auto take = [&](int64_t n, size_t each) {
         char* here = (char*)ws + bytes;
@@ -782,13 +795,12 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
     p.partML = (float2*)take(parts, sizeof(float2));
     p.scores = nullptr, p.lse2 = nullptr;
     if (stored)
-        p.scores = (float*)take(pairs * rows * (mostTokens / 4 + 1), 4 * sizeof(float));
+        p.scores = (float*)take(pairs * rows * up(room, kTile), kTile * sizeof(float));
     else if (accumulate)
         p.lse2 = (float*)take(pairs * rows, sizeof(float));
-    const int64_t tokens = (int64_t)p.splits * p.chunk;
     p.joinRows = (int32_t)(p.splits > kJoinRuns ? pairs * rows : up(pairs * rows, kWaves));
     p.joinSpan = rows <= 16 ? 4 * kThreads : 4 * 64;
-    p.joinBlocks = p.joinRows + (p.scores != nullptr ? pairs * up(tokens, p.joinSpan) : 0);
+    p.joinBlocks = p.joinRows + (p.scores != nullptr ? pairs * up(span, p.joinSpan) : 0);
     return bytes;
 }
 
@@ -797,15 +809,14 @@ hipError_t launch(const Plan& p, int64_t blocks, hipStream_t s)
 {
     const dim3 grid((unsigned)blocks), block(kThreads);
     if (p.tilesN == 1)
-        kv8_k_attend<F, T, D, 1><<<grid, block, 0, s>>>(p);
+        kv8_k_attend<F, T, D, 1><<<grid, dim3(kRunThreads), 0, s>>>(p);
     else if constexpr (D <= 96)
-        kv8_k_attend<F, T, D, 2><<<grid, block, 0, s>>>(p);
+        kv8_k_attend<F, T, D, 2><<<grid, dim3(kRunThreads), 0, s>>>(p);
     const int64_t pairs = (int64_t)p.a.c.batch * p.a.c.heads;
     if (!p.direct)
         kv8_k_join<T><<<dim3((unsigned)p.joinBlocks), block, 0, s>>>(p, D);
     if (p.lse2 != nullptr) {
-        const int64_t span = (int64_t)p.splits * p.chunk;
-        int64_t each = (span + kWaves * kTile - 1) / (kWaves * kTile);
+        int64_t each = ((int64_t)p.tiles + kWaves - 1) / kWaves;
         const int64_t most = pairs < 4096 ? 8192 / pairs : 2;
         each = each < most ? each : most;
         kv8_k_weights<F, T, D><<<dim3((unsigned)(pairs * each)), block, 0, s>>>(p, (int32_t)each);
