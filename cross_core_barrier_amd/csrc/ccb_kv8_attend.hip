@@ -559,8 +559,8 @@ __device__ __forceinline__ void merge(float& top, float& all, float top2, float 
 
 // Join the runs of a sequence's tokens: rows (out and lse), four to a
 // workgroup, or one where there are many runs; and tokens (weights, from the
-// stored scores).  Starting the workgroups is most of the time, so they are
-// few: a workgroup a row took 10 us for 2048 rows of 2 runs.
+// stored scores).  A workgroup a row took 10 us for 2048 rows of 2 runs, a
+// wave a row takes 5.
 template <int T>
 __global__ __launch_bounds__(kThreads) void kv8_k_join(Plan p, int32_t D)
 {
@@ -754,12 +754,12 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
     int64_t span = room;
     if (window > 0 && (int64_t)window + nQuery - 1 + kTile < span)
         span = (int64_t)window + nQuery - 1 + kTile;
-    // One workgroup of 8 waves for each CU: starting workgroups takes about 5 ns
-    // each, a round of them as long as their first loads, and both happen once
-    // this way.  Against two (of 8 waves, or four of 4) a CU, 16 sequences of
-    // 4096 tokens take 28.5 us instead of 31.1; where lengths spread from 500 to
-    // 4096 it is 26.4 instead of 25.2.  More, up to 16 a CU, where a run could
-    // pass 2 MB of codes: many short sequences do not wait for a long one's end.
+    // One workgroup of 8 waves for each CU: a second one pays its first loads'
+    // latency once more and brings no bandwidth.  Against two (of 8 waves, or
+    // four of 4) a CU, 16 sequences of 4096 tokens take 28.5 us instead of 31.1;
+    // where lengths spread from 500 to 4096 it is 27.3 instead of 25.2.  More,
+    // up to 16 a CU, where a run could pass 2 MB of codes: many short sequences
+    // do not wait for a long one's end.
     constexpr int64_t target = 256, limit = 16 * target;
     auto up = [](int64_t x, int64_t by) { return (x + by - 1) / by; };
     auto runs = [&](int64_t tokens, int64_t groups) {

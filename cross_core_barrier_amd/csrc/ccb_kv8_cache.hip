@@ -478,8 +478,23 @@ __global__ __launch_bounds__(kSelThreads) void kv8_k_select_long(SelectArgs a)
     const int64_t row = blockIdx.x / (uint32_t)a.segments;
     const int32_t seg = blockIdx.x % (uint32_t)a.segments;
     const int64_t rows = (int64_t)a.from.batch * a.from.heads;
-    const Row r = row_of(a, row);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // What the stage before left is asked for before the length says whether
+    // there is a search at all (the workspace has the places in any case).
+    int2 h = make_int2(0, 0), ahead = make_int2(0, 0);  // lower bin, higher bin; those of the segments before
+    int4 st = make_int4(0, 0, 0, 0);
+    if constexpr (S > 0) {
+        const int32_t* in = a.hist + ((int64_t)((S + 1) & 1) * rows + row) * a.segments * kBins + kBins - 2 -
+                            2 * (int32_t)threadIdx.x;
+        if (S > 1) st = *(const int4*)(a.state + ((int64_t)((S + 1) & 1) * rows + row) * kState);
+#pragma unroll 16
+        for (int32_t i = 0; i < a.segments; ++i) {
+            const int2 x = *(const int2*)(in + (int64_t)i * kBins);
+            h.x += x.x, h.y += x.y;
+            if (S == 3 && i < seg) ahead.x += x.x, ahead.y += x.y;
+        }
+    }
+    const Row r = row_of(a, row);
     constexpr int32_t unit = kSelWaves * kSelStep;
     const int32_t size = (int32_t)(((r.len + (int64_t)a.segments * unit - 1) / ((int64_t)a.segments * unit)) * unit);
     const int64_t begin64 = (int64_t)seg * size;
@@ -487,44 +502,30 @@ __global__ __launch_bounds__(kSelThreads) void kv8_k_select_long(SelectArgs a)
     const int32_t end = r.len - begin < size ? r.len : begin + size;
     const int32_t steps = (end - begin + unit - 1) / unit;
     const int32_t first = begin + wave * steps * kSelStep + 4 * lane;
+    // the first two steps' weights come while the threshold is found
+    f4u held[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (i < steps) held[i] = load4(r.w, first + i * kSelStep, end);
     auto each = [&](auto&& f) {
-        int32_t i = 0;
-        for (; i + 2 <= steps; i += 2) {  // two loads in flight
-            const f4u v0 = load4(r.w, first + i * kSelStep, end);
-            const f4u v1 = load4(r.w, first + (i + 1) * kSelStep, end);
-            f(first + i * kSelStep, v0);
-            f(first + (i + 1) * kSelStep, v1);
-        }
-        if (i < steps) f(first + i * kSelStep, load4(r.w, first + i * kSelStep, end));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (i < steps) f(first + i * kSelStep, held[i]);
+        for (int32_t i = 2; i < steps; ++i) f(first + i * kSelStep, load4(r.w, first + i * kSelStep, end));
     };
     // tokens past the segment's end belong to the next one
     Row mine = r;
     mine.len = end;
     mine.high = r.high < end ? r.high : end;
 
-    // the threshold, from the histograms of the stage before
+    // the threshold, from the stage before
     Threshold th = r.start;
-    if (S > 1 && !th.over) {
-        const int32_t* st = a.state + ((int64_t)((S + 1) & 1) * rows + row) * kState;
-        th.prefix = (uint32_t)st[0], th.shift = st[1], th.need = st[2], th.over = st[3] != 0;
-    }
+    if (S > 1 && !th.over) th.prefix = (uint32_t)st.x, th.shift = st.y, th.need = st.z, th.over = st.w != 0;
     const bool fresh = S > 0 && !th.over;
-    int2 ahead = make_int2(0, 0);  // this thread's two bins in the segments before
-    if (fresh) {
-        int2 h = make_int2(0, 0);  // lower bin, higher bin
-        const int32_t* in = a.hist + ((int64_t)((S + 1) & 1) * rows + row) * a.segments * kBins + kBins - 2 -
-                            2 * (int32_t)threadIdx.x;
-#pragma unroll 8
-        for (int32_t i = 0; i < a.segments; ++i) {
-            const int2 x = *(const int2*)(in + (int64_t)i * kBins);
-            h.x += x.x, h.y += x.y;
-            if (S == 3 && i < seg) ahead.x += x.x, ahead.y += x.y;
-        }
-        find_bin(th, S == 1 ? 21 : S == 2 ? 10 : 0, h.y, h.x, scratch, found);
-    }
+    if (fresh) find_bin(th, S == 1 ? 21 : S == 2 ? 10 : 0, h.y, h.x, scratch, found);
     if ((S == 1 || S == 2) && seg == 0 && threadIdx.x == 0) {
-        int32_t* st = a.state + ((int64_t)(S & 1) * rows + row) * kState;
-        st[0] = (int32_t)th.prefix, st[1] = th.shift, st[2] = th.need, st[3] = th.over;
+        *(int4*)(a.state + ((int64_t)(S & 1) * rows + row) * kState) =
+            make_int4((int32_t)th.prefix, th.shift, th.need, th.over);
     }
     int2* counts = a.counts + row * a.segments;
     if constexpr (S == 2) {
@@ -587,17 +588,16 @@ __global__ __launch_bounds__(kThreads) void kv8_k_move(ccbKv8Cache from, ccbKv8C
     __shared__ int64_t place[128];    // where a token's codes start
     __shared__ float tokenScale[128];
     const bool isV = blockIdx.x & 1;
-    uint32_t rest = blockIdx.x >> 1;
-    const int32_t h = rest % (uint32_t)from.heads;
-    rest /= (uint32_t)from.heads;
-    const int32_t number = rest % (uint32_t)nPages;
-    const int32_t b = rest / (uint32_t)nPages;
-    const int32_t P = from.pageSize;
+    const uint32_t rows = (uint32_t)from.batch * (uint32_t)from.heads;
+    const int32_t number = (blockIdx.x >> 1) / rows;
+    const int32_t row = (blockIdx.x >> 1) - number * rows;
+    const int32_t b = row / (uint32_t)from.heads, h = row - b * from.heads;
+    const int32_t P = from.pageSize, shift = __builtin_ctz(P);
 
     // (places past the kept tokens hold anything and are not used)
     const int32_t mine = number * P + (int32_t)threadIdx.x;
     const int32_t t = (int32_t)threadIdx.x < P && mine < budget
-                          ? index[((int64_t)b * from.heads + h) * budget + mine]
+                          ? index[(int64_t)row * budget + mine]
                           : 0;
     const int32_t page = checked_page(to.pageTable[b * to.tableStride + number], to.numPages);
     int32_t len = checked_len(from.lens[b], from.maxPages * P);
@@ -611,10 +611,10 @@ __global__ __launch_bounds__(kThreads) void kv8_k_move(ccbKv8Cache from, ccbKv8C
     }
     const uint8_t* codes = (const uint8_t*)(isV ? from.v : from.k);
     if ((int32_t)threadIdx.x < n) {
-        const int32_t src = checked_page(from.pageTable[b * from.tableStride + t / P], from.numPages);
+        const int32_t src = checked_page(from.pageTable[b * from.tableStride + (t >> shift)], from.numPages);
         if (src < 0) report(err);
         const int64_t block = (int64_t)(src < 0 ? 0 : src) * from.heads + h;
-        place[threadIdx.x] = src < 0 ? -1 : (block * P + t % P) * D;
+        place[threadIdx.x] = src < 0 ? -1 : (block * P + (t & (P - 1))) * D;
         tokenScale[threadIdx.x] = src < 0 ? 0.0f : (isV ? from.vScale : from.kScale)[block];
     }
     __syncthreads();

@@ -101,7 +101,8 @@ struct Near {
     }
 };
 
-// Four quotients as the codes of one word.
+// Four quotients as the codes of one word.  None is further from 0 than the
+// largest code by more than its error: s is at least the largest value / Q.
 template <int F>
 __device__ __forceinline__ uint32_t encode4_near(const float* t, Near<F>& near)
 {
@@ -109,26 +110,23 @@ __device__ __forceinline__ uint32_t encode4_near(const float* t, Near<F>& near)
         uint32_t n[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float c = __builtin_amdgcn_fmed3f(t[i], -127.0f, 127.0f);
-            const float r = __builtin_rintf(c);
-            near.d = fmaxf(near.d, fabsf(c - r));
+            const float r = __builtin_rintf(t[i]);
+            near.d = fmaxf(near.d, fabsf(t[i] - r));
             n[i] = (uint32_t)(int32_t)r;
         }
         const uint32_t a = __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400u);
         const uint32_t b = __builtin_amdgcn_perm(n[3], n[2], 0x04000c0cu);
         return a | b;
     } else {
-        float c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            c[i] = __builtin_amdgcn_fmed3f(t[i], -448.0f, 448.0f);
-            const uint32_t u = bits(c[i]);
+            const uint32_t u = bits(t[i]);
             const uint32_t size = (u << 1) - 1;  // a 0 is not small
             near.look(u);
             near.small = size < near.small ? size : near.small;
         }
-        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
-        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w, true);
     }
 }
 
