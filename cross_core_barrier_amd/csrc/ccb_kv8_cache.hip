@@ -24,63 +24,67 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------------------
 // append
 //
-// One workgroup per touched page, head and side (K or V): the largest new
-// value gives the block's scale, then the new values are rounded and, where
-// the scale grew, the block's older codes are rounded again.  Blocks are
+// One team per touched page, head and side (K or V): the largest new value
+// gives the block's scale, then the new values are rounded and, where the
+// scale grew, the block's older codes are rounded again.  Blocks are
 // independent, so there is nothing to join.  Bound by the bytes of the new
-// values and codes; one-token steps by latency.
+// values and codes (8 prompts of 8192 tokens: 402 MB in 79 to 105 us); one-token
+// steps by latency (5 us).
 // ---------------------------------------------------------------------------
 template <int F, int T, int D>
 __global__ __launch_bounds__(kThreads) void kv8_k_append(ccbKv8Cache c, ccbKv8Rows kNew,
                                                          ccbKv8Rows vNew, int32_t nNew,
                                                          const int32_t* counts, int32_t span,
-                                                         int32_t* err)
+                                                         uint32_t units, int32_t* err)
 {
     __shared__ float scratch[4];
-    const bool isV = blockIdx.x & 1;
-    uint32_t rest = blockIdx.x >> 1;
+    const int32_t P = c.pageSize, shift = __builtin_ctz(P);
+    const Team team(P);
+    const uint32_t unit = team.unit < units ? team.unit : 0;
+    bool works = team.unit < units;  // (the teams of a workgroup stay together)
+    const bool isV = unit & 1;
+    uint32_t rest = unit >> 1;
     const int32_t h = rest % (uint32_t)c.heads;
     rest /= (uint32_t)c.heads;
     const int32_t local = rest % (uint32_t)span;
     const int32_t b = rest / (uint32_t)span;
-    const int32_t P = c.pageSize;
 
     const int32_t len = checked_len(c.lens[b], c.maxPages * P);
     const int32_t cnt = counts != nullptr ? counts[b] : nNew;
-    if (len < 0 || cnt < 0 || cnt > nNew || cnt > len) {
-        if (threadIdx.x == 0) report(err);
-        return;
+    if (works && (len < 0 || cnt < 0 || cnt > nNew || cnt > len)) {
+        if (team.id == 0) report(err);
+        works = false;
     }
-    const int32_t start = len - cnt;
-    const int32_t number = start / P + local;
-    if (cnt == 0 || number * P >= len) return;
-    const int32_t lo = start > number * P ? start - number * P : 0;  // new slots lo .. hi - 1
-    const int32_t hi = len - number * P < P ? len - number * P : P;
+    const int32_t start = works ? len - cnt : 0;
+    const int32_t number = (start >> shift) + local;
+    works = works && cnt > 0 && number * (int64_t)P < len;
+    const int32_t lo = works && start > number * P ? start - number * P : 0;  // new slots lo .. hi - 1
+    const int32_t hi = !works ? 0 : len - number * P < P ? len - number * P : P;
     if (!isV && c.weight != nullptr) {
         float* w = c.weight + ((int64_t)b * c.heads + h) * c.weightStride + (int64_t)number * P;
-        for (int32_t i = lo + (int)threadIdx.x; i < hi; i += kThreads) w[i] = 0.0f;
+        for (int32_t i = lo + team.id; i < hi; i += team.size) w[i] = 0.0f;
     }
-    const int32_t page = checked_page(c.pageTable[b * c.tableStride + number], c.numPages);
+    const int32_t page = works ? checked_page(c.pageTable[b * c.tableStride + number], c.numPages) : 0;
     if (page < 0) {
-        if (threadIdx.x == 0) report(err);
-        return;
+        if (team.id == 0) report(err);
+        works = false;
     }
     constexpr int V = D / 8;  // vectors of 8 values per token
     const ccbKv8Rows& rows = isV ? vNew : kNew;
     const uint16_t* src = (const uint16_t*)rows.data + b * rows.strideBatch + h * rows.strideHead +
                           (int64_t)(number * P + lo - start) * rows.strideToken;
-    const int64_t block = (int64_t)page * c.heads + h;
+    const int64_t block = (int64_t)(works ? page : 0) * c.heads + h;
     uint8_t* dst = (uint8_t*)(isV ? c.v : c.k) + block * P * D;
     float* scale = (isV ? c.vScale : c.kScale) + block;
 
     // the new values stay in registers between finding the scale and rounding
     constexpr int N = 128 * V / kThreads;  // vectors of a thread for the largest page
-    const int32_t nVec = (hi - lo) * V;
+    const int32_t nVec = works ? (hi - lo) * V : 0;
     uint4 raw[N];
     float a = 0.0f;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int32_t i = k * kThreads + (int32_t)threadIdx.x;
+        const int32_t i = k * team.size + team.id;
         raw[k] = make_uint4(0, 0, 0, 0);
         if (i < nVec) raw[k] = *(const uint4*)(src + (i / V) * rows.strideToken + (i % V) * 8);
     }
@@ -102,15 +106,16 @@ __global__ __launch_bounds__(kThreads) void kv8_k_append(ccbKv8Cache c, ccbKv8Ro
             }
         }
     }
-    const float s0 = lo > 0 ? *scale : 0.0f;
-    a = block_max(a, scratch);
+    const float s0 = works && lo > 0 ? *scale : 0.0f;
+    a = team.largest(a, scratch);
+    if (!works) return;
     const float s1 = block_scale<F>(a);
     const float s = s1 > s0 ? s1 : s0;
     const float inv = 1.0f / s;
-    if (threadIdx.x == 0) *scale = s;
+    if (team.id == 0) *scale = s;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int32_t i = k * kThreads + (int32_t)threadIdx.x;
+        const int32_t i = k * team.size + team.id;
         if (i < nVec) {
             float x[8];
             widen8<T>(raw[k], x);
@@ -118,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void kv8_k_append(ccbKv8Cache c, ccbKv8Ro
         }
     }
     if (lo > 0 && s > s0) {  // older codes of a block whose scale grew
-        for (int32_t i = threadIdx.x; i < lo * V; i += kThreads) {
+        for (int32_t i = team.id; i < lo * V; i += team.size) {
             uint2* p = (uint2*)(dst + (int64_t)i * 8);
             *p = encode8_again<F>(*p, s0, inv, s);
         }
@@ -128,7 +133,7 @@ __global__ __launch_bounds__(kThreads) void kv8_k_append(ccbKv8Cache c, ccbKv8Ro
 // ---------------------------------------------------------------------------
 // read
 //
-// One workgroup per page, head and side, so that page and scale are looked up
+// One team per page, head and side, so that page and scale are looked up
 // once; a thread's 4 codes become one store of 16 (8) bytes beside its
 // neighbours'.  Bound by the bytes written.
 // ---------------------------------------------------------------------------
@@ -136,20 +141,22 @@ template <int F, int T, int D>
 __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows kOut,
                                                        ccbKv8Rows vOut, int32_t count,
                                                        const int32_t* first, int32_t span,
-                                                       int32_t sides, int32_t* err)
+                                                       int32_t sides, uint32_t units, int32_t* err)
 {
     constexpr int V = D / 4;
-    uint32_t rest = blockIdx.x;
+    const int32_t P = c.pageSize;
+    const Team team(P);
+    if (team.unit >= units) return;
+    uint32_t rest = team.unit;
     const int32_t h = rest % (uint32_t)c.heads;
     rest /= (uint32_t)c.heads;
     const bool isV = sides == 2 || (sides == 3 && rest % 2 == 1);
     if (sides == 3) rest /= 2;
     const int32_t local = rest % (uint32_t)span;
     const int32_t b = rest / (uint32_t)span;
-    const int32_t P = c.pageSize;
     int32_t len = checked_len(c.lens[b], c.maxPages * P);
     if (len < 0) {
-        if (threadIdx.x == 0) report(err);
+        if (team.id == 0) report(err);
         len = 0;
     }
     const int64_t from = first != nullptr ? first[b] : 0;
@@ -162,9 +169,9 @@ __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows
     int64_t block = 0;
     float s = 0.0f;
     if (held > lo) {
-        const int32_t page = checked_page(c.pageTable[b * c.tableStride + start / P], c.numPages);
+        const int32_t page = checked_page(c.pageTable[b * c.tableStride + (start >> __builtin_ctz(P))], c.numPages);
         if (page < 0) {
-            if (threadIdx.x == 0) report(err);
+            if (team.id == 0) report(err);
             held = 0;
         } else {
             block = (int64_t)page * c.heads + h;
@@ -174,17 +181,17 @@ __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows
     const uint8_t* src = (const uint8_t*)(isV ? c.v : c.k) + block * P * D;
     const ccbKv8Rows& rows = isV ? vOut : kOut;
     const int64_t base = b * rows.strideBatch + h * rows.strideHead + (start - from) * rows.strideToken;
-    for (int32_t i0 = lo * V + (int32_t)threadIdx.x; i0 < hi * V; i0 += 8 * kThreads) {
+    for (int32_t i0 = lo * V + team.id; i0 < hi * V; i0 += 8 * team.size) {
         uint32_t w[8];  // eight loads in flight
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int32_t i = i0 + k * kThreads;
+            const int32_t i = i0 + k * team.size;
             w[k] = 0;
             if (i < held * V && i < hi * V) w[k] = *(const uint32_t*)(src + i * 4);
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int32_t i = i0 + k * kThreads;
+            const int32_t i = i0 + k * team.size;
             if (i < hi * V) {
                 float x[4];
                 decode4<F>(w[k], x);  // code 0 is 0
@@ -573,55 +580,59 @@ __global__ __launch_bounds__(kSelThreads) void kv8_k_select_long(SelectArgs a)
 // ---------------------------------------------------------------------------
 // evict: the kept tokens into their new pages
 //
-// One workgroup per new page, head and side: looks its tokens' places up once,
+// One team per new page, head and side: looks its tokens' places up once,
 // gathers their codes into registers, finds the new scale, rounds the codes
-// again and writes them.  Bound by the gathered and written bytes.
+// again and writes them.  Half bound by instructions (about 20 a code, 8 of
+// them for rounding), half by the chain token -> page -> codes: 66 MB in 27 us.
 // ---------------------------------------------------------------------------
 template <int F, int D>
 __global__ __launch_bounds__(kThreads) void kv8_k_move(ccbKv8Cache from, ccbKv8Cache to,
-                                                       int32_t budget, int32_t nPages,
+                                                       int32_t budget, uint32_t units,
                                                        const int32_t* index, int32_t* err)
 {
     constexpr int V = D / 16;              // vectors of 16 codes in a token
     constexpr int N = 128 * V / kThreads;  // of a thread for the largest page
     __shared__ float scratch[4];
-    __shared__ int64_t place[128];    // where a token's codes start
-    __shared__ float tokenScale[128];
-    const bool isV = blockIdx.x & 1;
-    const uint32_t rows = (uint32_t)from.batch * (uint32_t)from.heads;
-    const int32_t number = (blockIdx.x >> 1) / rows;
-    const int32_t row = (blockIdx.x >> 1) - number * rows;
-    const int32_t b = row / (uint32_t)from.heads, h = row - b * from.heads;
+    __shared__ int64_t places[128];  // where a token's codes start
+    __shared__ float scales[128];
     const int32_t P = from.pageSize, shift = __builtin_ctz(P);
+    const Team team(P);
+    // a team's part of the arrays: a wave of a team of one has 16 places
+    int64_t* place = places + ((int32_t)threadIdx.x / team.size) * P;
+    float* tokenScale = scales + ((int32_t)threadIdx.x / team.size) * P;
+    const uint32_t unit = team.unit < units ? team.unit : 0;
+    const bool isV = unit & 1;
+    const uint32_t rows = (uint32_t)from.batch * (uint32_t)from.heads;
+    const int32_t number = (unit >> 1) / rows;
+    const int32_t row = (unit >> 1) - number * rows;
+    const int32_t b = row / (uint32_t)from.heads, h = row - b * from.heads;
 
     // (places past the kept tokens hold anything and are not used)
-    const int32_t mine = number * P + (int32_t)threadIdx.x;
-    const int32_t t = (int32_t)threadIdx.x < P && mine < budget
-                          ? index[(int64_t)row * budget + mine]
-                          : 0;
+    const int32_t mine = number * P + team.id;
+    const int32_t t = team.id < P && mine < budget ? index[(int64_t)row * budget + mine] : 0;
     const int32_t page = checked_page(to.pageTable[b * to.tableStride + number], to.numPages);
     int32_t len = checked_len(from.lens[b], from.maxPages * P);
     if (len < 0) len = 0;  // the selection reports it
     const int32_t stay = len < budget ? len : budget;
-    if (number * P >= stay) return;
-    const int32_t n = stay - number * P < P ? stay - number * P : P;
-    if (page < 0) {
-        if (threadIdx.x == 0) report(err);
-        return;
+    bool works = team.unit < units && number * P < stay;  // (the teams of a workgroup stay together)
+    if (works && page < 0) {
+        if (team.id == 0) report(err);
+        works = false;
     }
+    const int32_t n = !works ? 0 : stay - number * P < P ? stay - number * P : P;
     const uint8_t* codes = (const uint8_t*)(isV ? from.v : from.k);
-    if ((int32_t)threadIdx.x < n) {
+    if (team.id < n) {
         const int32_t src = checked_page(from.pageTable[b * from.tableStride + (t >> shift)], from.numPages);
         if (src < 0) report(err);
         const int64_t block = (int64_t)(src < 0 ? 0 : src) * from.heads + h;
-        place[threadIdx.x] = src < 0 ? -1 : (block * P + (t & (P - 1))) * D;
-        tokenScale[threadIdx.x] = src < 0 ? 0.0f : (isV ? from.vScale : from.kScale)[block];
+        place[team.id] = src < 0 ? -1 : (block * P + (t & (P - 1))) * D;
+        tokenScale[team.id] = src < 0 ? 0.0f : (isV ? from.vScale : from.kScale)[block];
     }
     __syncthreads();
     uint4 raw[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int32_t i = k * kThreads + (int32_t)threadIdx.x;
+        const int32_t i = k * team.size + team.id;
         raw[k] = make_uint4(0, 0, 0, 0);
         if (i < n * V) {
             const int64_t at = place[i / V];
@@ -631,7 +642,7 @@ __global__ __launch_bounds__(kThreads) void kv8_k_move(ccbKv8Cache from, ccbKv8C
     float a = 0.0f;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int32_t i = k * kThreads + (int32_t)threadIdx.x;
+        const int32_t i = k * team.size + team.id;
         if (i < n * V) {
             float x[16], m = 0.0f;
             decode4<F>(raw[k].x, x);
@@ -643,15 +654,16 @@ __global__ __launch_bounds__(kThreads) void kv8_k_move(ccbKv8Cache from, ccbKv8C
             a = fmaxf(a, m * tokenScale[i / V]);
         }
     }
-    a = block_max(a, scratch);
+    a = team.largest(a, scratch);
+    if (!works) return;
     const float s = block_scale<F>(a);
     const float inv = 1.0f / s;
     const int64_t block = (int64_t)page * to.heads + h;
-    if (threadIdx.x == 0) (isV ? to.vScale : to.kScale)[block] = s;
+    if (team.id == 0) (isV ? to.vScale : to.kScale)[block] = s;
     uint4* dst = (uint4*)((uint8_t*)(isV ? to.v : to.k) + block * P * D);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int32_t i = k * kThreads + (int32_t)threadIdx.x;
+        const int32_t i = k * team.size + team.id;
         if (i < n * V) {
             const float sOld = tokenScale[i / V];
             const uint2 x = encode8_again<F>(make_uint2(raw[k].x, raw[k].y), sOld, inv, s);
@@ -673,7 +685,7 @@ hipError_t kv8_append(const ccbKv8Cache& c, const ccbKv8Rows& k, const ccbKv8Row
     const int64_t blocks = (int64_t)c.batch * span * c.heads * 2;
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
 #define KV8_APPEND(F, T, D) \
-    (kv8_k_append<F, T, D><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(c, k, v, nNew, counts, span, err), 0)
+    (kv8_k_append<F, T, D><<<dim3(team_groups(blocks, c.pageSize)), dim3(kThreads), 0, s>>>(c, k, v, nNew, counts, span, (uint32_t)blocks, err), 0)
 #define KV8_APPEND_DIM(D) \
     (c.format == CCB_KV8_INT8 \
          ? (k.type == CCB_KV8_BF16 ? KV8_APPEND(kInt8, CCB_KV8_BF16, D) : KV8_APPEND(kInt8, CCB_KV8_FP16, D)) \
@@ -692,7 +704,7 @@ hipError_t kv8_read(const ccbKv8Cache& c, const ccbKv8Rows* k, const ccbKv8Rows*
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
     const ccbKv8Rows kr = k != nullptr ? *k : *v, vr = v != nullptr ? *v : *k;
 #define KV8_READ(F, T, D) \
-    (kv8_k_read<F, T, D><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(c, kr, vr, count, first, span, sides, err), 0)
+    (kv8_k_read<F, T, D><<<dim3(team_groups(blocks, c.pageSize)), dim3(kThreads), 0, s>>>(c, kr, vr, count, first, span, sides, (uint32_t)blocks, err), 0)
 #define KV8_READ_T(F, D) \
     (kr.type == CCB_KV8_BF16   ? KV8_READ(F, CCB_KV8_BF16, D) \
      : kr.type == CCB_KV8_FP16 ? KV8_READ(F, CCB_KV8_FP16, D) \
@@ -761,7 +773,7 @@ hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t bud
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
 #define KV8_MOVE(F, D) \
-    (kv8_k_move<F, D><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(from, to, budget, nPages, index, err), 0)
+    (kv8_k_move<F, D><<<dim3(team_groups(blocks, from.pageSize)), dim3(kThreads), 0, s>>>(from, to, budget, (uint32_t)blocks, index, err), 0)
 #define KV8_MOVE_DIM(D) (from.format == CCB_KV8_INT8 ? KV8_MOVE(kInt8, D) : KV8_MOVE(kE4m3, D))
     (void)KV8_BY_DIM(from.headDim, KV8_MOVE_DIM);
     return hipGetLastError();

@@ -192,16 +192,42 @@ __device__ __forceinline__ uint32_t larger16(uint32_t m, const uint4& u)
     return __builtin_bit_cast(uint32_t, x);
 }
 
-// The largest of a value over the workgroup (256 threads); x is not NaN.
-__device__ __forceinline__ float block_max(float x, float* scratch)
-{
+// The threads of a workgroup of 256 in teams, each for one block of a page: a
+// wave for 16 tokens, two for 32, all four for 64 and 128.  With a workgroup
+// for every block of 16 tokens, appending 65536 tokens took 135 us instead of
+// 57, and moving 240,000 took 317 us instead of 225.
+struct Team {
+    int32_t size;   // threads
+    int32_t id;     // of this thread in its team
+    uint32_t unit;  // the team's number in the grid, alike in a wave
+
+    __device__ __forceinline__ explicit Team(int32_t pageSize)
+    {
+        size = pageSize >= 64 ? 256 : pageSize * 4;
+        id = (int32_t)threadIdx.x & (size - 1);
+        const int32_t sub = __builtin_amdgcn_readfirstlane((int32_t)threadIdx.x / size);
+        unit = blockIdx.x * (uint32_t)(256 / size) + (uint32_t)sub;
+    }
+
+    // The largest of a value over the team; x is not NaN.  Every thread of the
+    // workgroup calls it.
+    __device__ __forceinline__ float largest(float x, float* scratch) const
+    {
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();  // scratch may still be read from an earlier use
-    if ((threadIdx.x & 63) == 0) scratch[wave] = x;
-    __syncthreads();
-    return fmaxf(fmaxf(scratch[0], scratch[1]), fmaxf(scratch[2], scratch[3]));
+        for (int d = 32; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
+        if (size == 64) return x;
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) scratch[wave] = x;
+        __syncthreads();
+        x = fmaxf(scratch[wave], scratch[wave ^ 1]);
+        return size == 128 ? x : fmaxf(x, fmaxf(scratch[wave ^ 2], scratch[wave ^ 3]));
+    }
+};
+
+inline unsigned team_groups(int64_t units, int32_t pageSize)
+{
+    const int32_t teams = pageSize >= 64 ? 1 : 64 / pageSize;
+    return (unsigned)((units + teams - 1) / teams);
 }
 
 }  // namespace kv8
