@@ -17,6 +17,7 @@
 
 #include "ccb.h"
 #include "ccb_internal.h"
+#include "ccb_kv8_internal.h"
 
 namespace {
 
@@ -84,13 +85,7 @@ ccbStatus current_device(int* devOut, DeviceInfo* infoOut)
 
 }  // namespace
 
-ccbStatus ccb::device_ready(int* numCUs)
-{
-    DeviceInfo info;
-    const ccbStatus st = current_device(nullptr, &info);
-    if (st == CCB_OK) *numCUs = info.numCUs;
-    return st;
-}
+ccbStatus ccb::device_ready() { return current_device(nullptr, nullptr); }
 
 namespace {
 

@@ -6,13 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "ccb.h"
-
 namespace ccb {
-
-// Checks that the current device is gfx950 (CCB_OK, CCB_ERR_UNSUPPORTED_DEVICE
-// or CCB_ERR_HIP) and stores its number of compute units.
-ccbStatus device_ready(int* numCUs);
 
 // Tuning constants of the kernels.
 // Stencil: non-temporal loads of the input (+7%); plain stores of the output

@@ -6,7 +6,6 @@
 #include <math.h>
 #include <stdint.h>
 
-#include "ccb_internal.h"
 #include "ccb_kv8_internal.h"
 
 namespace {
@@ -82,8 +81,7 @@ CCB_API ccbStatus ccb_kv8_append(const ccbKv8Cache* cache, const ccbKv8Rows* kNe
     if ((st = check_rows(kNew, false)) != CCB_OK) return st;
     if ((st = check_rows(vNew, false)) != CCB_OK) return st;
     if (kNew->type != vNew->type) return CCB_ERR_INVALID_VALUE;
-    int cus = 0;
-    if ((st = ccb::device_ready(&cus)) != CCB_OK) return st;
+    if ((st = ccb::device_ready()) != CCB_OK) return st;
     return done(ccb::kv8_append(*cache, *kNew, *vNew, nNew, counts, err, (hipStream_t)stream));
 }
 
@@ -114,8 +112,7 @@ CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
     if (ws == nullptr) return CCB_ERR_NULL_POINTER;
     if (wsBytes < ccb_kv8_attend_workspace_bytes(cache, headsQ, nQuery, accumulate))
         return CCB_ERR_INVALID_VALUE;
-    int cus = 0;
-    if ((st = ccb::device_ready(&cus)) != CCB_OK) return st;
+    if ((st = ccb::device_ready()) != CCB_OK) return st;
     ccb::Kv8AttendArgs a;
     a.c = *cache;
     a.q = *q;
@@ -128,7 +125,7 @@ CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
     a.scale = scale;
     a.ws = ws;
     a.err = err;
-    return done(ccb::kv8_attend(a, cus, (hipStream_t)stream));
+    return done(ccb::kv8_attend(a, (hipStream_t)stream));
 }
 
 CCB_API size_t ccb_kv8_evict_workspace_bytes(const ccbKv8Cache* from, int32_t budget)
@@ -157,10 +154,8 @@ CCB_API ccbStatus ccb_kv8_evict(const ccbKv8Cache* from, const ccbKv8Cache* to, 
     if (to->lens == from->lens || to->weight == from->weight || to->pageTable == from->pageTable)
         return CCB_ERR_INVALID_VALUE;
     if (wsBytes < ccb_kv8_evict_workspace_bytes(from, budget)) return CCB_ERR_INVALID_VALUE;
-    int cus = 0;
-    if ((st = ccb::device_ready(&cus)) != CCB_OK) return st;
-    return done(ccb::kv8_evict(*from, *to, budget, recent, sinks, kept, ws, err, cus,
-                               (hipStream_t)stream));
+    if ((st = ccb::device_ready()) != CCB_OK) return st;
+    return done(ccb::kv8_evict(*from, *to, budget, recent, sinks, kept, ws, err, (hipStream_t)stream));
 }
 
 CCB_API ccbStatus ccb_kv8_read(const ccbKv8Cache* cache, const ccbKv8Rows* kOut,
@@ -176,8 +171,7 @@ CCB_API ccbStatus ccb_kv8_read(const ccbKv8Cache* cache, const ccbKv8Rows* kOut,
     if (kOut != nullptr && (st = check_rows(kOut, true)) != CCB_OK) return st;
     if (vOut != nullptr && (st = check_rows(vOut, true)) != CCB_OK) return st;
     if (kOut != nullptr && vOut != nullptr && kOut->type != vOut->type) return CCB_ERR_INVALID_VALUE;
-    int cus = 0;
-    if ((st = ccb::device_ready(&cus)) != CCB_OK) return st;
+    if ((st = ccb::device_ready()) != CCB_OK) return st;
     return done(ccb::kv8_read(*cache, kOut, vOut, count, first, err, (hipStream_t)stream));
 }
 

@@ -834,9 +834,8 @@ size_t kv8_attend_bytes(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, in
     return make_plan(p, c, headsQ, nQuery, 0, accumulate, nullptr);
 }
 
-hipError_t kv8_attend(const Kv8AttendArgs& a, int numCUs, hipStream_t s)
+hipError_t kv8_attend(const Kv8AttendArgs& a, hipStream_t s)
 {
-    (void)numCUs;
     const ccbKv8Cache& c = a.c;
     Plan p;
     p.a = a;

@@ -748,9 +748,8 @@ size_t kv8_evict_bytes(const ccbKv8Cache& from, int32_t budget)
 }
 
 hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t budget, int32_t recent,
-                     int32_t sinks, int32_t* kept, void* ws, int32_t* err, int numCUs, hipStream_t s)
+                     int32_t sinks, int32_t* kept, void* ws, int32_t* err, hipStream_t s)
 {
-    (void)numCUs;
     SelectArgs a;
     select_plan(a, from, budget, ws);
     a.from = from, a.to = to;

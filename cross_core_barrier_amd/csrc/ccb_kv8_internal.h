@@ -10,6 +10,10 @@
 
 namespace ccb {
 
+// Checks that the current device is gfx950 (CCB_OK, CCB_ERR_UNSUPPORTED_DEVICE
+// or CCB_ERR_HIP); in ccb_api.hip, beside the cached device properties.
+ccbStatus device_ready();
+
 struct Kv8AttendArgs {
     ccbKv8Cache c;
     ccbKv8Rows q, out;
@@ -21,11 +25,11 @@ struct Kv8AttendArgs {
 };
 
 size_t kv8_attend_bytes(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, int32_t accumulate);
-hipError_t kv8_attend(const Kv8AttendArgs& a, int numCUs, hipStream_t s);
+hipError_t kv8_attend(const Kv8AttendArgs& a, hipStream_t s);
 
 size_t kv8_evict_bytes(const ccbKv8Cache& from, int32_t budget);
 hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t budget, int32_t recent,
-                     int32_t sinks, int32_t* kept, void* ws, int32_t* err, int numCUs, hipStream_t s);
+                     int32_t sinks, int32_t* kept, void* ws, int32_t* err, hipStream_t s);
 
 hipError_t kv8_append(const ccbKv8Cache& c, const ccbKv8Rows& k, const ccbKv8Rows& v, int32_t nNew,
                       const int32_t* counts, int32_t* err, hipStream_t s);
