@@ -707,3 +707,49 @@ def test_pages_past_32_bits(kv8):
         results.append([*got, kept, dst.weight, *dst.read(100), *c.read(300)])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_decoding_session(kv8, fmt):
+    """Prompts, steps and evictions together (the example's session): replayed
+    from a graph and made eagerly they end in the same bits, and a step's
+    attention is the oracle's over what the cache holds."""
+    from cross_core_barrier_amd.kv8_decode import Session
+    ends = []
+    for graph in (True, False):
+        s = Session(batch=3, heads=2, q_heads=6, head_dim=64, page_size=16, limit=96, budget=40, fmt=fmt, seed=3)
+        gen = torch.Generator(device="cuda").manual_seed(7)
+        s.prefill([torch.randn((n, s.x.shape[1]), generator=gen, device="cuda").to(s.x.dtype) for n in (70, 5, 33)])
+        _say(f"decoding session {fmt} graph={graph}")
+        for _ in range(100):
+            s.step(graph)
+        s.cache.check()
+        s.cut.check()
+        assert s.evictions == 2 and s.cache.lens.tolist() == s.lens
+        used = [p for pages in s.held for p in pages]
+        assert len(set(used + s.pages.free)) == len(used) + len(s.pages.free) == s.cache.k.shape[0]
+        ends.append((s.x.clone(), s.cache.lens.clone(), s.cache.weight.clone(), *s.cache.read(96)))
+    # weights past a sequence's end are whatever was there
+    for b, n in enumerate(ends[0][1].tolist()):
+        assert torch.equal(ends[0][2][b, :, :n], ends[1][2][b, :, :n])
+    for i in (0, 1, 3, 4):
+        assert torch.equal(ends[0][i], ends[1][i]), i
+    q = torch.randn((3, 1, 6, 64), generator=gen, device="cuda").half()
+    c = dict(fmt=fmt, lens=s.cache.lens.cpu().numpy(), table=s.cache.page_table.cpu().numpy(), k=_codes(s.cache.k),
+             v=_codes(s.cache.v), ks=s.cache.k_scale.cpu().numpy(), vs=s.cache.v_scale.cpu().numpy())
+    want, lse, _, mag, big = oracle.attend(c, q.double().cpu().numpy(), 0.125, 0)
+    out, got = s.cache.attend(q, accumulate=True, workspace=None)
+    _, tol_lse, tol = _bounds(64, 96, mag, big, lse)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol + 2.0 ** -11 * (np.abs(want) + tol) + 2.0 ** -25)
+    assert np.all(np.abs(got.double().cpu().numpy() - lse) <= tol_lse)
+
+
+def test_capacity_far_beyond_the_lengths(kv8):
+    """Short sequences in a cache with room for long ones: their runs are as
+    short as they are, and the workspace serves any window."""
+    rng = np.random.default_rng(30)
+    lens = [700, 0, 33, 4100]
+    for window in (0, 64, 3000):
+        c = _host(rng, "int8", lens, 2, 128, 64, width=200, extra=0)
+        _say(f"attend {lens} of 25600, window={window}")
+        _attend_case(kv8, 31, "int8", "fp16", lens, 2, 4, 64, 128, queries=2, window=window, c=c)
