@@ -198,15 +198,17 @@ class Kv8Cache:
     def read(self, count: int, first: Optional[torch.Tensor] = None, dtype=torch.float32, stream=None):
         """The values of `count` tokens of each sequence from first[b] (None: 0)
         as (k, v) [batch, count, heads, head_dim]; zeros where there is none."""
-        _need(dtype in _ROWS, "dtype: float32, bfloat16 or float16")
+        kind = _ROWS.get(dtype)
+        _need(kind is not None, "dtype: float32, bfloat16 or float16")
         self._ints(first, (self.batch,), "first")
-        shape = (self.batch, count, self.heads, self.head_dim)
         s = _enter(stream, self.device)
-        k, v = (torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+        both = torch.empty((2, self.batch, count, self.heads, self.head_dim), dtype=dtype, device=self.device)
         if s is not None:
-            k.record_stream(s)
-            v.record_stream(s)
-        ccb.check(ccb.ccb_kv8_read(self._c, self._rows(k, self.heads, "k"), self._rows(v, self.heads, "v"), count,
+            both.record_stream(s)
+        k, v = both.unbind(0)
+        row = self.heads * self.head_dim
+        ccb.check(ccb.ccb_kv8_read(self._c, ccb.ccbKv8Rows(k.data_ptr(), count * row, row, self.head_dim, kind, 0),
+                                   ccb.ccbKv8Rows(v.data_ptr(), count * row, row, self.head_dim, kind, 0), count,
                                    first, self.err, self._on(s)), "ccb_kv8_read")
         _leave(s, self.device)
         return k, v
