@@ -114,7 +114,7 @@ class Kv8Cache:
     def _space(self, ws: Optional[torch.Tensor], need: int, s):
         """The caller's workspace, or a new one for this call."""
         if ws is None:
-            ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             if s is not None:
                 s.wait_stream(torch.cuda.current_stream(self.device))
                 ws.record_stream(s)
@@ -141,7 +141,7 @@ class Kv8Cache:
         """A workspace for attend() calls of these sizes that follow each other."""
         n = ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
         _need(n > 0, "attend: sizes that ccb_kv8_attend refuses")
-        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def attend(self, q: torch.Tensor, scale: Optional[float] = None, window: int = 0, accumulate: bool = False,
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
@@ -177,7 +177,7 @@ class Kv8Cache:
         """A workspace for evict() calls with this budget that follow each other."""
         n = ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
         _need(n > 0, "evict: sizes that ccb_kv8_evict refuses")
-        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def evict(self, to: "Kv8Cache", budget: int, recent: int = 0, sinks: int = 0,
               kept: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,

@@ -117,8 +117,7 @@ CCB_API ccbStatus ccb_kv8_append(const ccbKv8Cache* cache, const ccbKv8Rows* kNe
  *   q, out  [batch][nQuery][headsQ][headDim], of one type
  *   lse     device float [batch][nQuery][headsQ], or NULL
  *   ws      device, ccb_kv8_attend_workspace_bytes(...) bytes, 128-B aligned,
- *           zeroed by the caller before its first use; every call leaves it
- *           ready for the next.  Calls that overlap in time need their own.
+ *           whatever it holds.  Calls that overlap in time need their own.
  * Errors: NULL_POINTER (also accumulate without weight), INVALID_VALUE (as
  * above; headsQ not a multiple of heads, nQuery or window < 0, more than 2^20 rows
  * (headsQ / heads * nQuery), a scale that is not finite, a workspace too small), UNSUPPORTED_DEVICE, HIP. */
@@ -127,7 +126,8 @@ CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
                                  float scale, int32_t window, int32_t accumulate, void* ws,
                                  size_t wsBytes, int32_t* err, ccbStream stream);
 
-/* Bytes of ccb_kv8_attend's workspace (0 for arguments it refuses). */
+/* Bytes of ccb_kv8_attend's workspace, whatever the window (0 for arguments it
+ * refuses). */
 CCB_API size_t ccb_kv8_attend_workspace_bytes(const ccbKv8Cache* cache, int32_t headsQ,
                                               int32_t nQuery, int32_t accumulate);
 
@@ -149,8 +149,7 @@ CCB_API size_t ccb_kv8_attend_workspace_bytes(const ccbKv8Cache* cache, int32_t 
  *   kept  device int32 [batch][heads][budget]: the kept tokens' numbers in
  *         `from`, then -1; or NULL
  *   ws    device, ccb_kv8_evict_workspace_bytes(...) bytes, 128-B aligned,
- *         zeroed by the caller before its first use; every call leaves it ready
- *         for the next.  Calls that overlap in time need their own.
+ *         whatever it holds.  Calls that overlap in time need their own.
  * Errors: NULL_POINTER (also from->weight), INVALID_VALUE (as above; budget <
  * 1, recent or sinks < 0, recent + sinks > budget, a workspace too small),
  * UNSUPPORTED_DEVICE, HIP. */

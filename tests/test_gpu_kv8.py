@@ -744,6 +744,56 @@ def test_decoding_session(kv8, fmt):
     assert np.all(np.abs(got.double().cpu().numpy() - lse) <= tol_lse)
 
 
+@pytest.mark.parametrize("D,group,queries", [(64, 5, 4), (96, 11, 3), (96, 3, 16), (128, 5, 4)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_attend_rows_in_pairs_of_tiles(kv8, D, group, queries, window):
+    """More rows than one tile holds in a batch large enough for a workgroup
+    to take two tiles of them."""
+    _say(f"attend 80 sequences, {group * queries} rows, D={D} window={window}")
+    lens = [(i * 29) % 130 for i in range(80)]
+    _attend_case(kv8, D + group, "e4m3" if D == 96 else "int8", "bf16", lens, 2, group, D, 32, queries, window)
+
+
+@pytest.mark.parametrize("window", [0, 2000])
+@pytest.mark.parametrize("fmt,dtype", [("int8", "fp16"), ("e4m3", "bf16")])
+def test_attend_weights_of_many_rows(kv8, fmt, dtype, window):
+    """Rows whose scores are not kept, over several runs of a sequence."""
+    _say(f"attend 96 rows, long, {fmt} window={window}")
+    _attend_case(kv8, 40, fmt, dtype, [3001, 0, 50, 700], 1, 8, 128, 64, 12, window)
+
+
+def test_attend_one_run_of_many_pages(kv8):
+    """A run longer than the pages a wave can hold at once: many sequences,
+    one of them long."""
+    _say("attend 130 sequences, one of 12000 tokens")
+    _attend_case(kv8, 41, "int8", "bf16", [12000] + [(i * 7) % 90 for i in range(129)], 1, 2, 64, 64)
+
+
+def test_evict_many_rows_of_few_segments(kv8):
+    """So many rows that each has two segments of several steps."""
+    rng = np.random.default_rng(42)
+    batch, heads, P, D, width = 128, 2, 128, 64, 160
+    lens = [20000, 17001, 0, 5, 16385] + [int(x) for x in rng.integers(0, 300, batch - 5)]
+    w = rng.random((batch, heads, width * P)).astype(np.float32)
+    w[1] = np.round(w[1] * 4)
+    k = torch.zeros((50, heads, P, D), dtype=torch.int8, device="cuda")
+    scales = [torch.ones((50, heads), device="cuda") for _ in range(2)]
+    table = torch.from_numpy(rng.integers(0, 50, (batch, width)).astype(np.int32)).cuda()
+    cache = kv8.Kv8Cache(k, k.clone(), *scales, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                         torch.from_numpy(w).cuda())
+    to = kv8.Kv8Cache.allocate(batch * 2, heads, P, D, batch, 2, "int8", weights=True)
+    to.page_table.copy_(torch.arange(batch * 2, dtype=torch.int32).view(batch, 2))
+    kept = torch.zeros((batch, heads, 200), dtype=torch.int32, device="cuda")
+    _say("evict 256 rows, a few of them long")
+    cache.evict(to, 200, 20, 4, kept=kept)
+    got = kept.cpu().numpy()
+    for b, n in enumerate(lens):
+        for h in range(heads):
+            want = oracle.kept(w[b, h], n, 200, 20, 4)
+            assert got[b, h].tolist() == want + [-1] * (200 - len(want)), (b, h)
+    assert to.lens.tolist() == [min(n, 200) for n in lens]
+
+
 def test_capacity_far_beyond_the_lengths(kv8):
     """Short sequences in a cache with room for long ones: their runs are as
     short as they are, and the workspace serves any window."""
