@@ -117,6 +117,7 @@ def check(status: int, what: str = "ccb call") -> None:
 
 _V = ctypes.c_void_p
 _SZ, _F32 = ctypes.c_size_t, ctypes.c_float
+_KC, _KR = ctypes.POINTER(ccbKv8Cache), ctypes.POINTER(ccbKv8Rows)
 _I32, _U32, _I64, _U64 = ctypes.c_int32, ctypes.c_uint32, ctypes.c_int64, ctypes.c_uint64
 
 
@@ -169,14 +170,14 @@ _f = {
     "ccb_cnt_notify_query": _sig("ccb_cnt_notify_query", _I32, _V, _V, _V, _V),
     "ccb_cnt_notify_batch": _sig("ccb_cnt_notify_batch", _I32, _V, _V, _I64, _I32, _V, _V, _I32, _V,
                                  _V),
-    "ccb_kv8_append": _sig("ccb_kv8_append", _I32, _V, _V, _V, _I32, _V, _V, _V),
-    "ccb_kv8_attend": _sig("ccb_kv8_attend", _I32, _V, _V, _V, _V, _I32, _I32, _F32, _I32, _I32, _V,
+    "ccb_kv8_append": _sig("ccb_kv8_append", _I32, _KC, _KR, _KR, _I32, _V, _V, _V),
+    "ccb_kv8_attend": _sig("ccb_kv8_attend", _I32, _KC, _KR, _KR, _V, _I32, _I32, _F32, _I32, _I32, _V,
                            _SZ, _V, _V),
-    "ccb_kv8_attend_workspace_bytes": _sig("ccb_kv8_attend_workspace_bytes", _SZ, _V, _I32, _I32,
+    "ccb_kv8_attend_workspace_bytes": _sig("ccb_kv8_attend_workspace_bytes", _SZ, _KC, _I32, _I32,
                                            _I32),
-    "ccb_kv8_evict": _sig("ccb_kv8_evict", _I32, _V, _V, _I32, _I32, _I32, _V, _V, _SZ, _V, _V),
-    "ccb_kv8_evict_workspace_bytes": _sig("ccb_kv8_evict_workspace_bytes", _SZ, _V, _I32),
-    "ccb_kv8_read": _sig("ccb_kv8_read", _I32, _V, _V, _V, _I32, _V, _V, _V),
+    "ccb_kv8_evict": _sig("ccb_kv8_evict", _I32, _KC, _KC, _I32, _I32, _I32, _V, _V, _SZ, _V, _V),
+    "ccb_kv8_evict_workspace_bytes": _sig("ccb_kv8_evict_workspace_bytes", _SZ, _KC, _I32),
+    "ccb_kv8_read": _sig("ccb_kv8_read", _I32, _KC, _KR, _KR, _I32, _V, _V, _V),
 }
 
 EXPORTED = sorted(_f)
@@ -379,32 +380,28 @@ def wait_info(mode: int, value: int, timeout: int = 0, is_clear: int = 0, rev=(0
 # --- 8-bit key/value cache ------------------------------------------------------------
 # cache arguments are ccbKv8Cache structures, rows ccbKv8Rows structures (or None)
 
-def _r(x):
-    return None if x is None else ctypes.byref(x)
-
-
 def ccb_kv8_append(cache, k_new, v_new, n_new, counts=None, err=None, stream=None) -> int:
-    return _f["ccb_kv8_append"](_r(cache), _r(k_new), _r(v_new), n_new, _p(counts), _p(err), _s(stream))
+    return _f["ccb_kv8_append"](cache, k_new, v_new, n_new, _p(counts), _p(err), _s(stream))
 
 
 def ccb_kv8_attend(cache, q, out, lse, heads_q, n_query, scale, window, accumulate, ws, ws_bytes,
                    err=None, stream=None) -> int:
-    return _f["ccb_kv8_attend"](_r(cache), _r(q), _r(out), _p(lse), heads_q, n_query, scale, window,
+    return _f["ccb_kv8_attend"](cache, q, out, _p(lse), heads_q, n_query, scale, window,
                                 accumulate, _p(ws), ws_bytes, _p(err), _s(stream))
 
 
 def ccb_kv8_attend_workspace_bytes(cache, heads_q: int, n_query: int, accumulate: int) -> int:
-    return int(_f["ccb_kv8_attend_workspace_bytes"](_r(cache), heads_q, n_query, accumulate))
+    return int(_f["ccb_kv8_attend_workspace_bytes"](cache, heads_q, n_query, accumulate))
 
 
 def ccb_kv8_evict(src, dst, budget, recent, sinks, kept, ws, ws_bytes, err=None, stream=None) -> int:
-    return _f["ccb_kv8_evict"](_r(src), _r(dst), budget, recent, sinks, _p(kept), _p(ws), ws_bytes,
+    return _f["ccb_kv8_evict"](src, dst, budget, recent, sinks, _p(kept), _p(ws), ws_bytes,
                                _p(err), _s(stream))
 
 
 def ccb_kv8_evict_workspace_bytes(src, budget: int) -> int:
-    return int(_f["ccb_kv8_evict_workspace_bytes"](_r(src), budget))
+    return int(_f["ccb_kv8_evict_workspace_bytes"](src, budget))
 
 
 def ccb_kv8_read(cache, k_out, v_out, count, first=None, err=None, stream=None) -> int:
-    return _f["ccb_kv8_read"](_r(cache), _r(k_out), _r(v_out), count, _p(first), _p(err), _s(stream))
+    return _f["ccb_kv8_read"](cache, k_out, v_out, count, _p(first), _p(err), _s(stream))

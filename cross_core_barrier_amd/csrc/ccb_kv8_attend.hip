@@ -1,5 +1,6 @@
 // ccb_kv8_attend.hip -- attention of a decoding step over the 8-bit
-// key/value cache: flash decoding on the matrix cores, split over tokens.
+// key/value cache, in one pass over the codes on the matrix cores, split over
+// tokens.
 //
 // The rows of one cache head (its queries and query heads) share every key
 // and value, so one workgroup takes a (sequence, cache head, run of tokens)
@@ -21,8 +22,14 @@
 // scale) go into the second product as two bf16 pieces, together within 2^-18
 // of p; one piece would cost 2^-9.
 //
-// Bound by memory: a tile of 32 tokens costs a wave about 350 instructions
-// for 64 * D bytes.
+// A tile of 32 tokens costs a wave about 350 instructions for 64 * D bytes, so
+// large calls are bound by memory (64 sequences of 8192 tokens, D = 128: 1.06
+// GB in 188 us, 5.6 TB/s; one of 131071 with its scores kept: 65 us, 4.6 TB/s)
+// and short ones by the start of a kernel: about 4 us until all XCDs run it, 3
+// until the first tile is there (length -> page -> codes; scales and queries
+// are asked for meanwhile), 2 for the join of the waves.  A second tile in
+// flight for each wave changed nothing (22.3 us against 22.2 for 16 sequences
+// of up to 4096 tokens).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -538,11 +545,25 @@ __global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_
     if (p.direct && p.scores != nullptr) {
         // this workgroup has all scores of its head: add the weights at once
         float* w = c.weight + (int64_t)pair * c.weightStride;
-        for (int32_t t = r.first + (int32_t)threadIdx.x; t < r.len; t += kRunThreads) {
-            float sum = 0.0f;
+        for (int32_t t0 = r.first + (int32_t)threadIdx.x; t0 < r.len; t0 += 4 * kRunThreads) {
+            float old[4], x[4];  // four tokens' loads in flight
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int32_t t = t0 + k * kRunThreads;
+                old[k] = t < r.len ? w[t] : 0.0f;
+                x[k] = 0.0f;
+            }
             for (int32_t i = 0; i < p.rows; ++i)
-                sum += exp2_(score_at(p, pair, 0, t - r.base)[i * kTile] - slse[i]);
-            w[t] += sum;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int32_t t = t0 + k * kRunThreads;
+                    if (t < r.len) x[k] += exp2_(score_at(p, pair, i, t - r.base)[0] - slse[i]);
+                }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int32_t t = t0 + k * kRunThreads;
+                if (t < r.len) w[t] = old[k] + x[k];
+            }
         }
     }
 }

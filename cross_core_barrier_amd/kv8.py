@@ -19,7 +19,6 @@ lengths and counts are met on the device: they set `cache.err`, which
 
 from __future__ import annotations
 
-import math
 from typing import Optional
 
 import torch
@@ -119,11 +118,14 @@ class Kv8Cache:
                 s.wait_stream(torch.cuda.current_stream(self.device))
                 ws.record_stream(s)
         _need(ws.is_contiguous() and ws.get_device() == self._index, "workspace: contiguous, on the cache's device")
-        return ws, ws.numel() * ws.element_size()
+        return ws, ws.nbytes
 
-    def _on(self, s):
-        """The stream a call runs on: `s`, or torch's current one."""
-        return _current_stream(self._index) if s is None else s
+    def _finish(self, status: int, what: str, s) -> None:
+        """Raise a call's error; order torch's stream after a call on `s`."""
+        if status != ccb.CCB_OK:
+            raise ccb.CcbError(status, what)
+        if s is not None:
+            _leave(s, self.device)
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts: Optional[torch.Tensor] = None,
                stream=None) -> None:
@@ -133,9 +135,9 @@ class Kv8Cache:
         n = k_new.shape[1]
         _need(n == v_new.shape[1] and k.type == v.type, "v_new: shape and dtype of k_new")
         self._ints(counts, (self.batch,), "counts")
-        s = _enter(stream, self.device)
-        ccb.check(ccb.ccb_kv8_append(self._c, k, v, n, counts, self.err, self._on(s)), "ccb_kv8_append")
-        _leave(s, self.device)
+        s = None if stream is None else _enter(stream, self.device)
+        self._finish(ccb.ccb_kv8_append(self._c, k, v, n, counts, self.err, s or _current_stream(self._index)),
+                     "ccb_kv8_append", s)
 
     def attend_workspace(self, q_heads: int, queries: int = 1, accumulate: bool = False) -> torch.Tensor:
         """A workspace for attend() calls of these sizes that follow each other."""
@@ -151,7 +153,7 @@ class Kv8Cache:
         _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
         shape = q.shape
         queries, q_heads = shape[1], shape[2]
-        s = _enter(stream, self.device)
+        s = None if stream is None else _enter(stream, self.device)
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=q.device)
             if s is not None:
@@ -167,10 +169,9 @@ class Kv8Cache:
         need = 0 if workspace is not None else \
             ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
         ws, size = self._space(workspace, need, s)
-        ccb.check(ccb.ccb_kv8_attend(self._c, qr, outr, lse, q_heads, queries,
-                                     1.0 / math.sqrt(self.head_dim) if scale is None else scale, window,
-                                     int(accumulate), ws, size, self.err, self._on(s)), "ccb_kv8_attend")
-        _leave(s, self.device)
+        self._finish(ccb.ccb_kv8_attend(self._c, qr, outr, lse, q_heads, queries,
+                                        self.head_dim ** -0.5 if scale is None else scale, window, int(accumulate), ws,
+                                        size, self.err, s or _current_stream(self._index)), "ccb_kv8_attend", s)
         return out, lse
 
     def evict_workspace(self, budget: int) -> torch.Tensor:
@@ -187,12 +188,11 @@ class Kv8Cache:
         kept [batch, heads, budget] int32 gets their numbers; it is returned."""
         _need(to._index == self._index, "to: on the cache's device")
         self._ints(kept, (self.batch, self.heads, budget), "kept")
-        s = _enter(stream, self.device)
+        s = None if stream is None else _enter(stream, self.device)
         need = 0 if workspace is not None else ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
         ws, size = self._space(workspace, need, s)
-        ccb.check(ccb.ccb_kv8_evict(self._c, to._c, budget, recent, sinks, kept, ws, size, self.err, self._on(s)),
-                  "ccb_kv8_evict")
-        _leave(s, self.device)
+        self._finish(ccb.ccb_kv8_evict(self._c, to._c, budget, recent, sinks, kept, ws, size, self.err,
+                                       s or _current_stream(self._index)), "ccb_kv8_evict", s)
         return kept
 
     def read(self, count: int, first: Optional[torch.Tensor] = None, dtype=torch.float32, stream=None):
@@ -201,16 +201,15 @@ class Kv8Cache:
         kind = _ROWS.get(dtype)
         _need(kind is not None, "dtype: float32, bfloat16 or float16")
         self._ints(first, (self.batch,), "first")
-        s = _enter(stream, self.device)
+        s = None if stream is None else _enter(stream, self.device)
         both = torch.empty((2, self.batch, count, self.heads, self.head_dim), dtype=dtype, device=self.device)
         if s is not None:
             both.record_stream(s)
         k, v = both.unbind(0)
         row = self.heads * self.head_dim
-        ccb.check(ccb.ccb_kv8_read(self._c, ccb.ccbKv8Rows(k.data_ptr(), count * row, row, self.head_dim, kind, 0),
-                                   ccb.ccbKv8Rows(v.data_ptr(), count * row, row, self.head_dim, kind, 0), count,
-                                   first, self.err, self._on(s)), "ccb_kv8_read")
-        _leave(s, self.device)
+        self._finish(ccb.ccb_kv8_read(self._c, ccb.ccbKv8Rows(k.data_ptr(), count * row, row, self.head_dim, kind, 0),
+                                      ccb.ccbKv8Rows(v.data_ptr(), count * row, row, self.head_dim, kind, 0), count,
+                                      first, self.err, s or _current_stream(self._index)), "ccb_kv8_read", s)
         return k, v
 
     def check(self) -> None:
