@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kThreads) void kv8_k_append(ccbKv8Cache c, ccbKv8Ro
 {
     __shared__ float scratch[4];
     const int32_t P = c.pageSize, shift = __builtin_ctz(P);
-    const Team team(P);
+    const Team team(P, blockIdx.x);
     const uint32_t unit = team.unit < units ? team.unit : 0;
     bool works = team.unit < units;  // (the teams of a workgroup stay together)
     const bool isV = unit & 1;
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows
 {
     constexpr int V = D / 4;
     const int32_t P = c.pageSize;
-    const Team team(P);
+    const Team team(P, blockIdx.x);
     if (team.unit >= units) return;
     uint32_t rest = team.unit;
     const int32_t h = rest % (uint32_t)c.heads;
@@ -207,6 +207,119 @@ __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows
             }
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// evict: the kept tokens into their new pages
+//
+// One team per new page, head and side: looks its tokens' places up once,
+// gathers their codes into registers, finds the new scale, rounds the codes
+// again and writes them.  Half bound by instructions (about 20 a code, 8 of
+// them for rounding), half by the chain token -> page -> codes: 66 MB in 27 us.
+// ---------------------------------------------------------------------------
+struct MoveLds {
+    int64_t place[128];  // where a token's codes start
+    float scale[128];
+    float reduce[4];
+};
+
+// One team's work: side isV of page `number` of a row, which is page `page` of
+// the pool; the row's i-th kept token is token(i), `stay` stay.  Every thread
+// of the workgroup calls this; a team that is not `valid` has nothing to do.
+template <int F, int D, class Token>
+__device__ __forceinline__ void move_page(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t budget,
+                                          const Team& team, bool valid, int32_t row, int32_t number, bool isV,
+                                          int32_t page, int32_t stay, int32_t* err, MoveLds& lds,
+                                          Token&& token)
+{
+    constexpr int V = D / 16;              // vectors of 16 codes in a token
+    constexpr int N = 128 * V / kThreads;  // of a thread for the largest page
+    const int32_t P = from.pageSize, shift = __builtin_ctz(P);
+    const int32_t b = row / (uint32_t)from.heads, h = row - b * from.heads;
+    int64_t* place = lds.place + team.sub * P;
+    float* tokenScale = lds.scale + team.sub * P;
+
+    // (places past the kept tokens hold anything and are not used)
+    const int32_t mine = number * P + team.id;
+    const int32_t t = valid && team.id < P && mine < budget ? token(mine) : 0;
+    page = checked_page(page, to.numPages);
+    bool works = valid && number * P < stay;
+    if (works && page < 0) {
+        if (team.id == 0) report(err);
+        works = false;
+    }
+    const int32_t n = !works ? 0 : stay - number * P < P ? stay - number * P : P;
+    const uint8_t* codes = (const uint8_t*)(isV ? from.v : from.k);
+    if (team.id < n) {
+        const int32_t src = checked_page(from.pageTable[b * from.tableStride + (t >> shift)], from.numPages);
+        if (src < 0) report(err);
+        const int64_t block = (int64_t)(src < 0 ? 0 : src) * from.heads + h;
+        place[team.id] = src < 0 ? -1 : (block * P + (t & (P - 1))) * D;
+        tokenScale[team.id] = src < 0 ? 0.0f : (isV ? from.vScale : from.kScale)[block];
+    }
+    __syncthreads();
+    uint4 raw[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int32_t i = k * team.size + team.id;
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if (i < n * V) {
+            const int64_t at = place[i / V];
+            if (at >= 0) raw[k] = *(const uint4*)(codes + at + i % V * 16);
+        }
+    }
+    float a = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int32_t i = k * team.size + team.id;
+        if (i < n * V) {
+            float x[16], m = 0.0f;
+            decode4<F>(raw[k].x, x);
+            decode4<F>(raw[k].y, x + 4);
+            decode4<F>(raw[k].z, x + 8);
+            decode4<F>(raw[k].w, x + 12);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
+            a = fmaxf(a, m * tokenScale[i / V]);
+        }
+    }
+    a = team.largest(a, lds.reduce);
+    if (!works) return;
+    const float s = block_scale<F>(a);
+    const float inv = 1.0f / s;
+    const int64_t block = (int64_t)page * to.heads + h;
+    if (team.id == 0) (isV ? to.vScale : to.kScale)[block] = s;
+    uint4* dst = (uint4*)((uint8_t*)(isV ? to.v : to.k) + block * P * D);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int32_t i = k * team.size + team.id;
+        if (i < n * V) {
+            const float sOld = tokenScale[i / V];
+            const uint2 x = encode8_again<F>(make_uint2(raw[k].x, raw[k].y), sOld, inv, s);
+            const uint2 y = encode8_again<F>(make_uint2(raw[k].z, raw[k].w), sOld, inv, s);
+            dst[i] = make_uint4(x.x, x.y, y.x, y.y);
+        }
+    }
+}
+
+template <int F, int D>
+__global__ __launch_bounds__(kThreads) void kv8_k_move(ccbKv8Cache from, ccbKv8Cache to,
+                                                       int32_t budget, uint32_t units,
+                                                       const int32_t* index, int32_t* err)
+{
+    __shared__ MoveLds lds;
+    const Team team(from.pageSize, blockIdx.x);
+    const bool valid = team.unit < units;  // (the teams of a workgroup stay together)
+    const uint32_t unit = valid ? team.unit >> 1 : 0;
+    const uint32_t rows = (uint32_t)from.batch * (uint32_t)from.heads;
+    const int32_t number = unit / rows, row = unit - number * rows;
+    const int32_t* list = index + (int64_t)row * budget;
+    const int32_t b = row / (uint32_t)from.heads;
+    const int32_t page = to.pageTable[b * to.tableStride + number];
+    int32_t len = checked_len(from.lens[b], from.maxPages * from.pageSize);
+    if (len < 0) len = 0;  // the selection reports it
+    move_page<F, D>(from, to, budget, team, valid, row, number, team.unit & 1, page, len < budget ? len : budget,
+                    err, lds, [&](int32_t i) { return list[i]; });
 }
 
 // ---------------------------------------------------------------------------
@@ -391,17 +504,17 @@ __device__ __forceinline__ int2 count_kept(const Row& r, const Threshold& th, Ea
     return n;
 }
 
-// Writes the workgroup's kept tokens; `before` counts those ahead of them.
+// Writes the workgroup's kept tokens to `index` (the row's list) and to the
+// results; `before` counts those ahead of them.
 template <class Each>
 __device__ __forceinline__ void write_kept(const SelectArgs& a, const Row& r, const Threshold& th, int64_t row,
-                                           int2 before, int2* scratch, Each&& each)
+                                           int32_t* index, int2 before, int2* scratch, Each&& each)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int2 n = count_kept(r, th, each);
     if (lane == 0) scratch[wave] = n;
     __syncthreads();
     for (int i = 0; i < wave; ++i) before.x += scratch[i].x, before.y += scratch[i].y;
-    int32_t* index = a.index + row * a.budget;
     int32_t* kept = a.kept != nullptr ? a.kept + row * a.budget : nullptr;
     float* weight = a.to.weight != nullptr ? a.to.weight + row * a.to.weightStride : nullptr;
     const uint64_t below = ((uint64_t)1 << lane) - 1;
@@ -443,14 +556,14 @@ __device__ __forceinline__ void finish_row(const SelectArgs& a, const Row& r, in
     }
 }
 
-__global__ __launch_bounds__(kSelThreads) void kv8_k_select_short(SelectArgs a)
+// A row that one workgroup chooses from; `index` may lie in `hist`, which holds
+// nothing any more when the list is written.
+__device__ __forceinline__ void select_row(const SelectArgs& a, const Row& r, int64_t row, int32_t* index,
+                                           int32_t* hist)
 {
-    __shared__ int32_t hist[kBins];
     __shared__ int32_t scratch[kSelWaves];
     __shared__ int2 places[kSelWaves];
     __shared__ int32_t found[3];
-    const int64_t row = blockIdx.x;
-    const Row r = row_of(a, row);
     // this wave's tokens: first + step * kSelStep + 4 * lane + e
     const int32_t steps = (r.len + kSelWaves * kSelStep - 1) / (kSelWaves * kSelStep);
     const int32_t first = (threadIdx.x >> 6) * steps * kSelStep + 4 * (threadIdx.x & 63);
@@ -470,8 +583,38 @@ __global__ __launch_bounds__(kSelThreads) void kv8_k_select_short(SelectArgs a)
         const int32_t h0 = hist[kBins - 1 - 2 * threadIdx.x], h1 = hist[kBins - 2 - 2 * threadIdx.x];
         find_bin(th, below, h0, h1, scratch, found);
     }
-    write_kept(a, r, th, row, make_int2(0, 0), places, each);
+    write_kept(a, r, th, row, index, make_int2(0, 0), places, each);
     finish_row(a, r, row);
+}
+
+__global__ __launch_bounds__(kSelThreads) void kv8_k_select_short(SelectArgs a)
+{
+    __shared__ int32_t hist[kBins];
+    const int64_t row = blockIdx.x;
+    select_row(a, row_of(a, row), row, a.index + row * a.budget, hist);
+}
+
+// The same, and the move of what was kept, where the workgroup's teams are as
+// many as the row's new blocks (128 tokens, 256 in pages of 128): a launch less
+// counts for more than other CUs' help.  204 rows that keep 28 tokens take 15
+// us with the read after it instead of 18.7; with two rounds of blocks for a
+// team, 12 rows of 138 tokens took 22.6 instead of 18.7.
+template <int F, int D>
+__global__ __launch_bounds__(kSelThreads) void kv8_k_select_move(SelectArgs a, int32_t nPages)
+{
+    __shared__ int32_t hist[kBins];
+    __shared__ MoveLds lds[kSelThreads / kThreads];
+    const int32_t row = blockIdx.x;
+    const int32_t group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    const Team team(a.from.pageSize, (uint32_t)group);
+    const int32_t number = (int32_t)(team.unit >> 1);
+    const bool valid = number < nPages;
+    const int32_t page = a.to.pageTable[row / a.from.heads * a.to.tableStride + (valid ? number : 0)];
+    const Row r = row_of(a, row);
+    select_row(a, r, row, hist, hist);
+    __syncthreads();  // the list is written
+    move_page<F, D>(a.from, a.to, a.budget, team, valid, row, number, team.unit & 1, page,
+                    r.len < a.budget ? r.len : a.budget, a.err, lds[group], [&](int32_t i) { return hist[i]; });
 }
 
 // One stage of a long row: 0, 1 and 2 count 11, 11 and 10 bits, 3 writes.
@@ -572,104 +715,8 @@ __global__ __launch_bounds__(kSelThreads) void kv8_k_select_long(SelectArgs a)
         before = make_int2(0, 0);
         for (int i = 0; i < kSelWaves; ++i) before.x += places[i].x, before.y += places[i].y;
         __syncthreads();
-        write_kept(a, mine, th, row, before, places, each);
+        write_kept(a, mine, th, row, a.index + row * a.budget, before, places, each);
         if (seg == 0) finish_row(a, r, row);
-    }
-}
-
-// ---------------------------------------------------------------------------
-// evict: the kept tokens into their new pages
-//
-// One team per new page, head and side: looks its tokens' places up once,
-// gathers their codes into registers, finds the new scale, rounds the codes
-// again and writes them.  Half bound by instructions (about 20 a code, 8 of
-// them for rounding), half by the chain token -> page -> codes: 66 MB in 27 us.
-// ---------------------------------------------------------------------------
-template <int F, int D>
-__global__ __launch_bounds__(kThreads) void kv8_k_move(ccbKv8Cache from, ccbKv8Cache to,
-                                                       int32_t budget, uint32_t units,
-                                                       const int32_t* index, int32_t* err)
-{
-    constexpr int V = D / 16;              // vectors of 16 codes in a token
-    constexpr int N = 128 * V / kThreads;  // of a thread for the largest page
-    __shared__ float scratch[4];
-    __shared__ int64_t places[128];  // where a token's codes start
-    __shared__ float scales[128];
-    const int32_t P = from.pageSize, shift = __builtin_ctz(P);
-    const Team team(P);
-    // a team's part of the arrays: a wave of a team of one has 16 places
-    int64_t* place = places + ((int32_t)threadIdx.x / team.size) * P;
-    float* tokenScale = scales + ((int32_t)threadIdx.x / team.size) * P;
-    const uint32_t unit = team.unit < units ? team.unit : 0;
-    const bool isV = unit & 1;
-    const uint32_t rows = (uint32_t)from.batch * (uint32_t)from.heads;
-    const int32_t number = (unit >> 1) / rows;
-    const int32_t row = (unit >> 1) - number * rows;
-    const int32_t b = row / (uint32_t)from.heads, h = row - b * from.heads;
-
-    // (places past the kept tokens hold anything and are not used)
-    const int32_t mine = number * P + team.id;
-    const int32_t t = team.id < P && mine < budget ? index[(int64_t)row * budget + mine] : 0;
-    const int32_t page = checked_page(to.pageTable[b * to.tableStride + number], to.numPages);
-    int32_t len = checked_len(from.lens[b], from.maxPages * P);
-    if (len < 0) len = 0;  // the selection reports it
-    const int32_t stay = len < budget ? len : budget;
-    bool works = team.unit < units && number * P < stay;  // (the teams of a workgroup stay together)
-    if (works && page < 0) {
-        if (team.id == 0) report(err);
-        works = false;
-    }
-    const int32_t n = !works ? 0 : stay - number * P < P ? stay - number * P : P;
-    const uint8_t* codes = (const uint8_t*)(isV ? from.v : from.k);
-    if (team.id < n) {
-        const int32_t src = checked_page(from.pageTable[b * from.tableStride + (t >> shift)], from.numPages);
-        if (src < 0) report(err);
-        const int64_t block = (int64_t)(src < 0 ? 0 : src) * from.heads + h;
-        place[team.id] = src < 0 ? -1 : (block * P + (t & (P - 1))) * D;
-        tokenScale[team.id] = src < 0 ? 0.0f : (isV ? from.vScale : from.kScale)[block];
-    }
-    __syncthreads();
-    uint4 raw[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int32_t i = k * team.size + team.id;
-        raw[k] = make_uint4(0, 0, 0, 0);
-        if (i < n * V) {
-            const int64_t at = place[i / V];
-            if (at >= 0) raw[k] = *(const uint4*)(codes + at + i % V * 16);
-        }
-    }
-    float a = 0.0f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int32_t i = k * team.size + team.id;
-        if (i < n * V) {
-            float x[16], m = 0.0f;
-            decode4<F>(raw[k].x, x);
-            decode4<F>(raw[k].y, x + 4);
-            decode4<F>(raw[k].z, x + 8);
-            decode4<F>(raw[k].w, x + 12);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
-            a = fmaxf(a, m * tokenScale[i / V]);
-        }
-    }
-    a = team.largest(a, scratch);
-    if (!works) return;
-    const float s = block_scale<F>(a);
-    const float inv = 1.0f / s;
-    const int64_t block = (int64_t)page * to.heads + h;
-    if (team.id == 0) (isV ? to.vScale : to.kScale)[block] = s;
-    uint4* dst = (uint4*)((uint8_t*)(isV ? to.v : to.k) + block * P * D);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int32_t i = k * team.size + team.id;
-        if (i < n * V) {
-            const float sOld = tokenScale[i / V];
-            const uint2 x = encode8_again<F>(make_uint2(raw[k].x, raw[k].y), sOld, inv, s);
-            const uint2 y = encode8_again<F>(make_uint2(raw[k].z, raw[k].w), sOld, inv, s);
-            dst[i] = make_uint4(x.x, x.y, y.x, y.y);
-        }
     }
 }
 
@@ -760,6 +807,14 @@ hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t bud
     const int64_t rows = (int64_t)from.batch * from.heads;
     const int64_t blocks = rows * nPages * 2;
     if (blocks > INT32_MAX || rows * (a.segments + 1) > INT32_MAX) return hipErrorInvalidValue;
+    const int32_t teams = kSelThreads / kThreads * (from.pageSize >= 64 ? 1 : 64 / from.pageSize);
+    if (a.segments == 0 && 2 * nPages <= teams) {
+#define KV8_SELECT_MOVE(F, D) (kv8_k_select_move<F, D><<<dim3((unsigned)rows), dim3(kSelThreads), 0, s>>>(a, nPages), 0)
+#define KV8_SELECT_MOVE_DIM(D) \
+    (from.format == CCB_KV8_INT8 ? KV8_SELECT_MOVE(kInt8, D) : KV8_SELECT_MOVE(kE4m3, D))
+        (void)KV8_BY_DIM(from.headDim, KV8_SELECT_MOVE_DIM);
+        return hipGetLastError();
+    }
     if (a.segments == 0) {
         kv8_k_select_short<<<dim3((unsigned)rows), dim3(kSelThreads), 0, s>>>(a);
     } else {

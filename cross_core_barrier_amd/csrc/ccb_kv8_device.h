@@ -192,31 +192,32 @@ __device__ __forceinline__ uint32_t larger16(uint32_t m, const uint4& u)
     return __builtin_bit_cast(uint32_t, x);
 }
 
-// The threads of a workgroup of 256 in teams, each for one block of a page: a
+// The threads of a group of 256 (a workgroup, or a quarter of one) in teams, each for one block of a page: a
 // wave for 16 tokens, two for 32, all four for 64 and 128.  With a workgroup
 // for every block of 16 tokens, appending 65536 tokens took 135 us instead of
 // 57, and moving 240,000 took 317 us instead of 225.
 struct Team {
     int32_t size;   // threads
     int32_t id;     // of this thread in its team
-    uint32_t unit;  // the team's number in the grid, alike in a wave
+    int32_t sub;    // the team's place in its group
+    uint32_t unit;  // the team's number among all of group 0, 1, ..., alike in a wave
 
-    __device__ __forceinline__ explicit Team(int32_t pageSize)
+    __device__ __forceinline__ Team(int32_t pageSize, uint32_t group)
     {
         size = pageSize >= 64 ? 256 : pageSize * 4;
         id = (int32_t)threadIdx.x & (size - 1);
-        const int32_t sub = __builtin_amdgcn_readfirstlane((int32_t)threadIdx.x / size);
-        unit = blockIdx.x * (uint32_t)(256 / size) + (uint32_t)sub;
+        sub = __builtin_amdgcn_readfirstlane(((int32_t)threadIdx.x & 255) / size);
+        unit = group * (uint32_t)(256 / size) + (uint32_t)sub;
     }
 
     // The largest of a value over the team; x is not NaN.  Every thread of the
-    // workgroup calls it.
+    // workgroup calls it, with its group's scratch.
     __device__ __forceinline__ float largest(float x, float* scratch) const
     {
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
         if (size == 64) return x;
-        const int wave = threadIdx.x >> 6;
+        const int wave = (threadIdx.x >> 6) & 3;
         if ((threadIdx.x & 63) == 0) scratch[wave] = x;
         __syncthreads();
         x = fmaxf(scratch[wave], scratch[wave ^ 1]);
