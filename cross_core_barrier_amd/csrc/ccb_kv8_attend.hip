@@ -24,12 +24,12 @@
 //
 // A tile of 32 tokens costs a wave about 350 instructions for 64 * D bytes, so
 // large calls are bound by memory (64 sequences of 8192 tokens, D = 128: 1.06
-// GB in 188 us, 5.6 TB/s; one of 131071 with its scores kept: 65 us, 4.6 TB/s)
+// GB in 183 us, 5.8 TB/s; one of 131071 with its scores kept: 65 us, 4.6 TB/s)
 // and short ones by the start of a kernel: about 4 us until all XCDs run it, 3
 // until the first tile is there (length -> page -> codes; scales and queries
 // are asked for meanwhile), 2 for the join of the waves.  A second tile in
 // flight for each wave changed nothing (22.3 us against 22.2 for 16 sequences
-// of up to 4096 tokens).
+// of up to 4096 tokens, before the reads of LDS stopped waiting for it).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -246,6 +246,126 @@ __device__ __forceinline__ void write_row(const Plan& p, int32_t b, int32_t h, i
     }
 }
 
+__device__ __forceinline__ uint32_t lds_at(const uint8_t* p)
+{
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
+}
+
+// A lane's keys of a tile: 16 codes for two steps of the first product, 8 for a
+// last odd one, of token n and token 16 + n.  In one block with the wait for
+// them: behind reads that it knows as such the compiler waits for every load
+// into LDS that is in flight, the values' too (64 sequences of 8192 tokens: 188
+// us instead of 183; 32 rows a head, 16 of 4096: 34.7 instead of 31).
+template <int D>
+__device__ __forceinline__ void read_keys(const uint8_t* buf, int at, int swap, int g, 
+                                          u4 (&key)[2][(D / 32 + 1) / 2])
+{
+    const uint32_t row = lds_at(buf) + (uint32_t)at;
+    const uint32_t a0 = row + ((g ^ swap) * 16), a1 = row + (((4 + g) ^ swap) * 16);
+    if constexpr (D == 64) {
+        asm volatile(
+            "ds_read_b128 %0, %2\n\t"
+            "ds_read_b128 %1, %2 offset:1024\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(key[0][0]), "=&v"(key[1][0]) : "v"(a0) : "memory");
+    } else if constexpr (D == 96) {
+        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+        const uint32_t t = row + (((4 + (g >> 1)) ^ swap) * 16 + 8 * (g & 1));
+        u2 x, y;
+        asm volatile(
+            "ds_read_b128 %0, %4\n\t"
+            "ds_read_b128 %1, %4 offset:1536\n\t"
+            "ds_read_b64 %2, %5\n\t"
+            "ds_read_b64 %3, %5 offset:1536\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(key[0][0]), "=&v"(key[1][0]), "=&v"(x), "=&v"(y) : "v"(a0), "v"(t) : "memory");
+        key[0][1] = u4{x.x, x.y, 0, 0};
+        key[1][1] = u4{y.x, y.y, 0, 0};
+    } else if constexpr (D == 128) {
+        asm volatile(
+            "ds_read_b128 %0, %4\n\t"
+            "ds_read_b128 %1, %5\n\t"
+            "ds_read_b128 %2, %4 offset:2048\n\t"
+            "ds_read_b128 %3, %5 offset:2048\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(key[0][0]), "=&v"(key[0][1]), "=&v"(key[1][0]), "=&v"(key[1][1])
+            : "v"(a0), "v"(a1) : "memory");
+    } else {
+        const uint32_t a2 = row + (((8 + g) ^ swap) * 16);
+        if constexpr (D == 192) {
+            asm volatile(
+                "ds_read_b128 %0, %6\n\t"
+                "ds_read_b128 %1, %7\n\t"
+                "ds_read_b128 %2, %8\n\t"
+                "ds_read_b128 %3, %6 offset:3072\n\t"
+                "ds_read_b128 %4, %7 offset:3072\n\t"
+                "ds_read_b128 %5, %8 offset:3072\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(key[0][0]), "=&v"(key[0][1]), "=&v"(key[0][2]), "=&v"(key[1][0]), "=&v"(key[1][1]),
+                  "=&v"(key[1][2])
+                : "v"(a0), "v"(a1), "v"(a2) : "memory");
+        } else {
+            const uint32_t a3 = row + (((12 + g) ^ swap) * 16);
+            asm volatile(
+                "ds_read_b128 %0, %8\n\t"
+                "ds_read_b128 %1, %9\n\t"
+                "ds_read_b128 %2, %10\n\t"
+                "ds_read_b128 %3, %11\n\t"
+                "ds_read_b128 %4, %8 offset:4096\n\t"
+                "ds_read_b128 %5, %9 offset:4096\n\t"
+                "ds_read_b128 %6, %10 offset:4096\n\t"
+                "ds_read_b128 %7, %11 offset:4096\n\t"
+                "s_waitcnt lgkmcnt(0)"
+                : "=&v"(key[0][0]), "=&v"(key[0][1]), "=&v"(key[0][2]), "=&v"(key[0][3]), "=&v"(key[1][0]),
+                  "=&v"(key[1][1]), "=&v"(key[1][2]), "=&v"(key[1][3])
+                : "v"(a0), "v"(a1), "v"(a2), "v"(a3) : "memory");
+        }
+    }
+}
+
+// Transposed reads of 16 dimensions of a lane's 8 tokens, N blocks of them; as
+// above in one block with the wait.
+template <int N>
+__device__ __forceinline__ void read_values(const uint32_t* at, i2* w)
+{
+    static_assert(N == 4 || N == 6 || N == 8, "blocks of 16 dimensions at once");
+    if constexpr (N == 4)
+        asm volatile("ds_read_b64_tr_b8 %0, %4\n\t"
+                     "ds_read_b64_tr_b8 %1, %5\n\t"
+                     "ds_read_b64_tr_b8 %2, %6\n\t"
+                     "ds_read_b64_tr_b8 %3, %7\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]), "=&v"(w[3])
+                     : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+                     : "memory");
+    else if constexpr (N == 6)
+        asm volatile("ds_read_b64_tr_b8 %0, %6\n\t"
+                     "ds_read_b64_tr_b8 %1, %7\n\t"
+                     "ds_read_b64_tr_b8 %2, %8\n\t"
+                     "ds_read_b64_tr_b8 %3, %9\n\t"
+                     "ds_read_b64_tr_b8 %4, %10\n\t"
+                     "ds_read_b64_tr_b8 %5, %11\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]), "=&v"(w[3]), "=&v"(w[4]), "=&v"(w[5])
+                     : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5])
+                     : "memory");
+    else
+        asm volatile("ds_read_b64_tr_b8 %0, %8\n\t"
+                     "ds_read_b64_tr_b8 %1, %9\n\t"
+                     "ds_read_b64_tr_b8 %2, %10\n\t"
+                     "ds_read_b64_tr_b8 %3, %11\n\t"
+                     "ds_read_b64_tr_b8 %4, %12\n\t"
+                     "ds_read_b64_tr_b8 %5, %13\n\t"
+                     "ds_read_b64_tr_b8 %6, %14\n\t"
+                     "ds_read_b64_tr_b8 %7, %15\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]), "=&v"(w[3]), "=&v"(w[4]), "=&v"(w[5]),
+                       "=&v"(w[6]), "=&v"(w[7])
+                     : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]),
+                       "v"(at[6]), "v"(at[7])
+                     : "memory");
+}
+
 template <int F, int T, int D, int NT>
 __global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_k_attend(Plan p)
 {
@@ -307,6 +427,7 @@ __global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_
     }
 
     const float scale2 = a.scale * kLog2e;  // scores in powers of two
+    const bool stored = p.scores != nullptr;
     f4 o[NT][NB];
     float m[NT], ref[NT], l[NT];
 #pragma unroll
@@ -336,15 +457,21 @@ __global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_
         float kScale = 0.0f, vScale = 0.0f;
         {
             const int32_t t = seg + laneAt;
-            if (t < segEnd && t + 16 > r.first) {
-                page = checked_page(early && seg == lo ? entry : table[t >> shift], c.numPages);
-                if (page < 0) {
-                    report(a.err);
-                } else {
-                    const int64_t block = (int64_t)page * c.heads + h;
-                    kScale = c.kScale[block];
-                    vScale = c.vScale[block];
-                }
+            const bool seen = t < segEnd && t + 16 > r.first;
+            if (seen) page = checked_page(early && seg == lo ? entry : table[t >> shift], c.numPages);
+            // The compiler has to know before the loop that the queries and the
+            // scales are there: left to the loop, the wait for them is one for every
+            // load, in every step.  The queries were asked for before the pages.
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int jj = 0; jj < NJ; ++jj) asm volatile("" : "+v"(q[nt][jj]));
+            if (page >= 0) {
+                const int64_t block = (int64_t)page * c.heads + h;
+                kScale = c.kScale[block];
+                vScale = c.vScale[block];
+            } else if (seen) {
+                report(a.err);
             }
         }
         const int32_t nTiles = ((segEnd - seg + kTile - 1) / kTile - wave + kRunWaves - 1) / kRunWaves;
@@ -370,35 +497,33 @@ __global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_
         auto step = [&](int32_t i, uint8_t* kb, uint8_t* vb) {
             const int32_t t0 = seg + (i * kRunWaves + wave) * kTile;
             const bool more = i + 1 < nTiles;
-            // scores
-            wait_loads<NI>();
+            // Scores.  Behind this tile's keys: its values, and between them the last
+            // step's stores of scores, two at least where they are kept (a wait that
+            // does not count them waits for the stores, and below for the next keys).
+            if (stored && i > 0) wait_loads<NI + 2>(); else wait_loads<NI>();
+            u4 key[2][(NJ + 1) / 2];
+            read_keys<D>(kb, kAt, kSwap, g, key);
+            if (more) {
+                issue(c.k, i + 1, kb);
+                asm volatile("" ::: "memory");  // the stores come after these loads
+            }
             f4 s[NT][2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) s[nt][half] = f4{0, 0, 0, 0};
-                const uint8_t* row = kb + kAt + half * 16 * C * 16;
 #pragma unroll
-                for (int j = 0; j + 1 < NJ; j += 2) {
-                    const u4 w = *(const u4*)(row + (((2 * j + g) ^ kSwap) * 16));
-                    const u4 x = codes16x8<F, T>(w.x, w.y), y = codes16x8<F, T>(w.z, w.w);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        s[nt][half] = mfma<T>(x, q[nt][j], s[nt][half]);
-                        s[nt][half] = mfma<T>(y, q[nt][j + 1], s[nt][half]);
-                    }
-                }
-                if constexpr (NJ % 2 == 1) {
-                    const uint2 w =
-                        *(const uint2*)(row + (((2 * (NJ - 1) + (g >> 1)) ^ kSwap) * 16 + 8 * (g & 1)));
+                for (int j = 0; j < NJ; j += 2) {
+                    const u4 w = key[half][j / 2];
                     const u4 x = codes16x8<F, T>(w.x, w.y);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) s[nt][half] = mfma<T>(x, q[nt][NJ - 1], s[nt][half]);
+                    for (int nt = 0; nt < NT; ++nt) s[nt][half] = mfma<T>(x, q[nt][j], s[nt][half]);
+                    if (j + 1 < NJ) {
+                        const u4 y = codes16x8<F, T>(w.z, w.w);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) s[nt][half] = mfma<T>(y, q[nt][j + 1], s[nt][half]);
+                    }
                 }
-            }
-            if (more) {
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the keys are read
-                issue(c.k, i + 1, kb);
             }
             const int32_t pg0 = __builtin_amdgcn_readlane(page, 2 * i);
             const int32_t pg1 = __builtin_amdgcn_readlane(page, 2 * i + 1);
@@ -420,7 +545,7 @@ __global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_
                             s[nt][1][e] = -INFINITY;
                     }
                 }
-                if (p.scores != nullptr && row0 + nt * 16 + n < p.rows) {
+                if (stored && row0 + nt * 16 + n < p.rows) {
                     float* dst = score_at(p, pair, row0 + nt * 16 + n, t0 - r.base) + 4 * g;
                     *(f4*)dst = s[nt][0];
                     *(f4*)(dst + 16) = s[nt][1];
@@ -462,7 +587,11 @@ __global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_
                 }
             }
             // values
-            if (more) wait_loads<NI>(); else wait_loads<0>();
+            if (stored) {
+                if (more) wait_loads<NI + 2>(); else wait_loads<2>();
+            } else {
+                if (more) wait_loads<NI>(); else wait_loads<0>();
+            }
             uint32_t keep0 = ~0u, keep1 = ~0u;  // e4m3: NaN codes where nothing is held
             if (F == kE4m3 && !whole) {
                 keep0 = keep1 = 0;
@@ -472,30 +601,34 @@ __global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_
                     keep1 |= (pg1 >= 0 && t0 + 16 + 4 * g + e < r.len) ? 0xffu << (8 * e) : 0u;
                 }
             }
+            constexpr int NR = NB <= 8 ? NB : NB / 2;  // blocks read at once
 #pragma unroll
-            for (int d = 0; d < NB; ++d) {
-                i2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                    (__attribute__((address_space(3))) i2*)(vb + vAt + ((d ^ vSwap) * 16)));
-                if (F == kE4m3 && !whole) w.x &= keep0, w.y &= keep1;
-                const u4 x = codes16x8<F, CCB_KV8_BF16>(w.x, w.y);
+            for (int d0 = 0; d0 < NB; d0 += NR) {
+                uint32_t at[NR];
+                i2 w[NR];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    o[nt][d] = mfma<CCB_KV8_BF16>(x, ph[nt], o[nt][d]);
-                    o[nt][d] = mfma<CCB_KV8_BF16>(x, pl[nt], o[nt][d]);
+                for (int d = 0; d < NR; ++d) at[d] = lds_at(vb) + (uint32_t)(vAt + (((d0 + d) ^ vSwap) * 16));
+                read_values<NR>(at, w);
+                if (more && d0 + NR == NB) issue(c.v, i + 1, vb);
+#pragma unroll
+                for (int d = 0; d < NR; ++d) {
+                    if (F == kE4m3 && !whole) w[d].x &= keep0, w[d].y &= keep1;
+                    const u4 x = codes16x8<F, CCB_KV8_BF16>(w[d].x, w[d].y);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        o[nt][d0 + d] = mfma<CCB_KV8_BF16>(x, ph[nt], o[nt][d0 + d]);
+                        o[nt][d0 + d] = mfma<CCB_KV8_BF16>(x, pl[nt], o[nt][d0 + d]);
+                    }
                 }
-            }
-            if (more) {
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the values are read
-                issue(c.v, i + 1, vb);
             }
         };
 
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last segment's reads
         if (nTiles > 0) {
             issue(c.k, 0, kBuf[wave]);
             issue(c.v, 0, vBuf[wave]);
+            asm volatile("" : "+v"(kScale), "+v"(vScale));
+            for (int32_t i = 0; i < nTiles; ++i) step(i, kBuf[wave], vBuf[wave]);
         }
-        for (int32_t i = 0; i < nTiles; ++i) step(i, kBuf[wave], vBuf[wave]);
     }
 
     // join the waves
@@ -525,8 +658,8 @@ __global__ __launch_bounds__(kRunThreads, D <= 128 && NT == 1 ? 4 : 2) void kv8_
             float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
             for (int w = 0; w < kRunWaves; ++w) {
-                sum += *(const f4*)((const float*)(w < kRunWaves / 2 ? kBuf[0] : vBuf[0]) + (w % (kRunWaves / 2) * 16 + i) * D +
-                                    ((d4 ^ (i & 7)) * 4));
+                const float* src = (const float*)(w < kRunWaves / 2 ? kBuf[0] : vBuf[0]);
+                sum += *(const f4*)(src + (w % (kRunWaves / 2) * 16 + i) * D + ((d4 ^ (i & 7)) * 4));
                 mm = fmaxf(mm, sm[w][nt * 16 + i]);
             }
 #pragma unroll

@@ -47,7 +47,8 @@ class Session:
         self.out_width = -(-budget // page_size)
         # every sequence at its limit, and one cut of the whole batch besides
         self.pages = Pages(batch * (width + self.out_width))
-        self.cache = Kv8Cache.allocate(len(self.pages.free), heads, page_size, head_dim, batch, width, fmt, weights=True)
+        self.cache = Kv8Cache.allocate(len(self.pages.free), heads, page_size, head_dim, batch, width, fmt,
+                                       weights=True)
         # the cut's own table, lengths and weights, over the same pool
         self.cut = Kv8Cache(self.cache.k, self.cache.v, self.cache.k_scale, self.cache.v_scale,
                             torch.zeros((batch, self.out_width), dtype=torch.int32, device=dev),
@@ -97,7 +98,8 @@ class Session:
             _, k, v = self.project(rows)
             self.cache.append(k, v, counts)
             ccb.check(ccb.ccb_cnt_notify_record(done, writer, ccb.record_info(ccb.CCB_CNT_RECORD_ADD, 1)), "record")
-        ccb.check(ccb.ccb_cnt_notify_wait(done, here, ccb.wait_info(ccb.CCB_CNT_WAIT_BIGGER_OR_EQUAL, 1, 10, 1)), "wait")
+        there = ccb.wait_info(ccb.CCB_CNT_WAIT_BIGGER_OR_EQUAL, 1, 10, 1)
+        ccb.check(ccb.ccb_cnt_notify_wait(done, here, there), "wait")
         here.wait_stream(writer)  # the prompt's tensors are torch's to reuse after this
         here.synchronize()
         ccb.check(ccb.ccb_cnt_notify_destroy(done), "ccb_cnt_notify_destroy")
@@ -188,8 +190,8 @@ def main(argv=None) -> None:
     t = time.perf_counter() - t
     s.cache.check()
     s.cut.check()
-    print(f"{a.batch} sequences, {a.steps} steps, {s.evictions} evictions: {t / max(1, a.steps - 1) * 1e6:.1f} us a step, "
-          f"{a.batch * (a.steps - 1) / t:.0f} tokens/s; lengths now {min(s.lens)} to {max(s.lens)}")
+    print(f"{a.batch} sequences, {a.steps} steps, {s.evictions} evictions: "
+          f"{t / max(1, a.steps - 1) * 1e6:.1f} us a step, {a.batch * (a.steps - 1) / t:.0f} tokens/s; lengths now {min(s.lens)} to {max(s.lens)}")
 
 
 if __name__ == "__main__":

@@ -110,8 +110,9 @@ CCB_API ccbStatus ccb_kv8_append(const ccbKv8Cache* cache, const ccbKv8Rows* kNe
  *   s_t = scale * q . k_t,  m = max s_t,  l = sum exp(s_t - m),
  *   out = sum exp(s_t - m) v_t / l,  lse = m + ln l;
  * a query that sees nothing (an empty sequence, or i < nQuery - n) gets out =
- * 0 and lse = -infinity.  Products are exact and sums are kept in 32 bits;
- * out is rounded once to its type.  accumulate != 0 adds to weight[b][head][t]
+ * 0 and lse = -infinity.  Products q k are exact, sums are kept in 32 bits, a
+ * weight times its block's scale enters the sum of values within 2^-18 of
+ * itself, and out is rounded once to its type.  accumulate != 0 adds to weight[b][head][t]
  * the sum of exp(s_t - lse) over the queries and the query heads of that head.
  * Results do not depend on timing: the same call gives the same bits.
  *   q, out  [batch][nQuery][headsQ][headDim], of one type
