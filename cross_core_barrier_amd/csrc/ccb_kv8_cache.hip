@@ -731,8 +731,10 @@ hipError_t kv8_append(const ccbKv8Cache& c, const ccbKv8Rows& k, const ccbKv8Row
     const int32_t span = (nNew + c.pageSize - 2) / c.pageSize + 1;
     const int64_t blocks = (int64_t)c.batch * span * c.heads * 2;
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    const uint32_t units = (uint32_t)blocks;
+    const dim3 grid(team_groups(blocks, c.pageSize));
 #define KV8_APPEND(F, T, D) \
-    (kv8_k_append<F, T, D><<<dim3(team_groups(blocks, c.pageSize)), dim3(kThreads), 0, s>>>(c, k, v, nNew, counts, span, (uint32_t)blocks, err), 0)
+    (kv8_k_append<F, T, D><<<grid, dim3(kThreads), 0, s>>>(c, k, v, nNew, counts, span, units, err), 0)
 #define KV8_APPEND_DIM(D) \
     (c.format == CCB_KV8_INT8 \
          ? (k.type == CCB_KV8_BF16 ? KV8_APPEND(kInt8, CCB_KV8_BF16, D) : KV8_APPEND(kInt8, CCB_KV8_FP16, D)) \
@@ -750,8 +752,10 @@ hipError_t kv8_read(const ccbKv8Cache& c, const ccbKv8Rows* k, const ccbKv8Rows*
     const int64_t blocks = (int64_t)c.batch * span * c.heads * (sides == 3 ? 2 : 1);
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
     const ccbKv8Rows kr = k != nullptr ? *k : *v, vr = v != nullptr ? *v : *k;
+    const uint32_t units = (uint32_t)blocks;
+    const dim3 grid(team_groups(blocks, c.pageSize));
 #define KV8_READ(F, T, D) \
-    (kv8_k_read<F, T, D><<<dim3(team_groups(blocks, c.pageSize)), dim3(kThreads), 0, s>>>(c, kr, vr, count, first, span, sides, (uint32_t)blocks, err), 0)
+    (kv8_k_read<F, T, D><<<grid, dim3(kThreads), 0, s>>>(c, kr, vr, count, first, span, sides, units, err), 0)
 #define KV8_READ_T(F, D) \
     (kr.type == CCB_KV8_BF16   ? KV8_READ(F, CCB_KV8_BF16, D) \
      : kr.type == CCB_KV8_FP16 ? KV8_READ(F, CCB_KV8_FP16, D) \
@@ -802,7 +806,7 @@ hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t bud
     a.from = from, a.to = to;
     a.budget = budget, a.recent = recent, a.sinks = sinks;
     a.kept = kept, a.err = err;
-    int32_t* index = a.index;
+    const int32_t* index = a.index;
     const int32_t nPages = (budget + from.pageSize - 1) / from.pageSize;
     const int64_t rows = (int64_t)from.batch * from.heads;
     const int64_t blocks = rows * nPages * 2;
@@ -818,16 +822,18 @@ hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t bud
     if (a.segments == 0) {
         kv8_k_select_short<<<dim3((unsigned)rows), dim3(kSelThreads), 0, s>>>(a);
     } else {
-        const dim3 grid((unsigned)(rows * a.segments));
-        kv8_k_select_long<0><<<grid, dim3(kSelThreads), 0, s>>>(a);
-        kv8_k_select_long<1><<<grid, dim3(kSelThreads), 0, s>>>(a);
-        kv8_k_select_long<2><<<grid, dim3(kSelThreads), 0, s>>>(a);
-        kv8_k_select_long<3><<<grid, dim3(kSelThreads), 0, s>>>(a);
+        const dim3 long_((unsigned)(rows * a.segments));
+        kv8_k_select_long<0><<<long_, dim3(kSelThreads), 0, s>>>(a);
+        kv8_k_select_long<1><<<long_, dim3(kSelThreads), 0, s>>>(a);
+        kv8_k_select_long<2><<<long_, dim3(kSelThreads), 0, s>>>(a);
+        kv8_k_select_long<3><<<long_, dim3(kSelThreads), 0, s>>>(a);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    const uint32_t units = (uint32_t)blocks;
+    const dim3 grid(team_groups(blocks, from.pageSize));
 #define KV8_MOVE(F, D) \
-    (kv8_k_move<F, D><<<dim3(team_groups(blocks, from.pageSize)), dim3(kThreads), 0, s>>>(from, to, budget, (uint32_t)blocks, index, err), 0)
+    (kv8_k_move<F, D><<<grid, dim3(kThreads), 0, s>>>(from, to, budget, units, index, err), 0)
 #define KV8_MOVE_DIM(D) (from.format == CCB_KV8_INT8 ? KV8_MOVE(kInt8, D) : KV8_MOVE(kE4m3, D))
     (void)KV8_BY_DIM(from.headDim, KV8_MOVE_DIM);
     return hipGetLastError();
