@@ -13,6 +13,9 @@ using namespace kv8;
 
 constexpr int kThreads = 256;
 
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
 // Picks the kernel instance for a cache's format and head size.
 #define KV8_BY_DIM(dim, CALL) \
     ((dim) == 64    ? CALL(64) \
@@ -135,7 +138,8 @@ __global__ __launch_bounds__(kThreads) void kv8_k_append(ccbKv8Cache c, ccbKv8Ro
 //
 // One team per page, head and side, so that page and scale are looked up
 // once; a thread's 4 codes become one store of 16 (8) bytes beside its
-// neighbours'.  Bound by the bytes written.
+// neighbours'.  Bound by the bytes written, which pass the caches by: 541 MB of
+// floats in 105 us (6.4 TB/s with the codes read), 115 through them.
 // ---------------------------------------------------------------------------
 template <int F, int T, int D>
 __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows kOut,
@@ -199,11 +203,11 @@ __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows
                 for (int e = 0; e < 4; ++e) x[e] *= s;
                 const int64_t at = base + (i / V) * rows.strideToken + i % V * 4;
                 if constexpr (T == CCB_KV8_FP32)
-                    *(float4*)((float*)rows.data + at) = make_float4(x[0], x[1], x[2], x[3]);
+                    __builtin_nontemporal_store(f4{x[0], x[1], x[2], x[3]}, (f4*)((float*)rows.data + at));
                 else
-                    *(uint2*)((uint16_t*)rows.data + at) =
-                        make_uint2(narrow<T>(x[0]) | (narrow<T>(x[1]) << 16),
-                                   narrow<T>(x[2]) | (narrow<T>(x[3]) << 16));
+                    __builtin_nontemporal_store(u2{narrow<T>(x[0]) | (narrow<T>(x[1]) << 16),
+                                                   narrow<T>(x[2]) | (narrow<T>(x[3]) << 16)},
+                                                (u2*)((uint16_t*)rows.data + at));
             }
         }
     }
