@@ -895,7 +895,7 @@ __global__ __launch_bounds__(kThreads) void kv8_k_weights(Plan p, int32_t blocks
 }
 
 // How a call is split, and where its workspace's parts lie; returns its bytes,
-// which do not depend on the window.
+// which do not depend on the window.  There is a sequence and a query.
 size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, int32_t window,
                  int32_t accumulate, void* ws)
 {
@@ -984,6 +984,7 @@ namespace ccb {
 
 size_t kv8_attend_bytes(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, int32_t accumulate)
 {
+    if (c.batch == 0 || nQuery == 0) return 0;
     Plan p;
     return make_plan(p, c, headsQ, nQuery, 0, accumulate, nullptr);
 }

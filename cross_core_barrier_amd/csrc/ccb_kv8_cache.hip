@@ -770,7 +770,7 @@ hipError_t kv8_read(const ccbKv8Cache& c, const ccbKv8Rows* k, const ccbKv8Rows*
 }
 
 // Segments of a row, 0 where one workgroup chooses by itself, and the
-// workspace's parts; returns its bytes.
+// workspace's parts; returns its bytes.  There is a sequence.
 static size_t select_plan(SelectArgs& a, const ccbKv8Cache& from, int32_t budget, void* ws)
 {
     const int64_t rows = (int64_t)from.batch * from.heads;
@@ -798,6 +798,7 @@ static size_t select_plan(SelectArgs& a, const ccbKv8Cache& from, int32_t budget
 
 size_t kv8_evict_bytes(const ccbKv8Cache& from, int32_t budget)
 {
+    if (from.batch == 0) return 0;
     SelectArgs a;
     return select_plan(a, from, budget, nullptr);
 }
@@ -826,11 +827,11 @@ hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t bud
     if (a.segments == 0) {
         kv8_k_select_short<<<dim3((unsigned)rows), dim3(kSelThreads), 0, s>>>(a);
     } else {
-        const dim3 long_((unsigned)(rows * a.segments));
-        kv8_k_select_long<0><<<long_, dim3(kSelThreads), 0, s>>>(a);
-        kv8_k_select_long<1><<<long_, dim3(kSelThreads), 0, s>>>(a);
-        kv8_k_select_long<2><<<long_, dim3(kSelThreads), 0, s>>>(a);
-        kv8_k_select_long<3><<<long_, dim3(kSelThreads), 0, s>>>(a);
+        const dim3 segments((unsigned)(rows * a.segments));
+        kv8_k_select_long<0><<<segments, dim3(kSelThreads), 0, s>>>(a);
+        kv8_k_select_long<1><<<segments, dim3(kSelThreads), 0, s>>>(a);
+        kv8_k_select_long<2><<<segments, dim3(kSelThreads), 0, s>>>(a);
+        kv8_k_select_long<3><<<segments, dim3(kSelThreads), 0, s>>>(a);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -260,6 +260,29 @@ def test_refuses_bad_arguments(ccb):
     assert ccb.ccb_kv8_read(c, None, None, 0) == ok
 
 
+def test_workspace_bytes_of_nothing(ccb):
+    """No sequence, no query: a size all the same, and calls that do nothing."""
+    long = dict(maxPages=4096, tableStride=4096, weightStride=65536)
+    for extra in ({}, long):
+        c, none = _cache(ccb, **extra), _cache(ccb, batch=0, **extra)
+        for acc in (0, 1):
+            assert ccb.ccb_kv8_attend_workspace_bytes(none, 4, 1, acc) > 0
+            assert ccb.ccb_kv8_attend_workspace_bytes(c, 4, 0, acc) > 0
+        assert ccb.ccb_kv8_evict_workspace_bytes(none, 32) > 0
+        assert ccb.ccb_kv8_attend(none, None, None, None, 4, 1, 0.1, 0, 0, None, 0) == ccb.CCB_OK
+        assert ccb.ccb_kv8_attend(c, None, None, None, 4, 0, 0.1, 0, 0, None, 0) == ccb.CCB_OK
+
+
+@pytest.mark.parametrize("batch,heads,pages", [(1, 1, 1), (1, 65536, 1), (100000, 8, 2), (1, 8, 1 << 23), (4096, 1, 1 << 20)])
+def test_workspace_bytes_of_extremes(ccb, batch, heads, pages):
+    """Sizes far from the usual ones: a number, the larger with weights."""
+    c = _cache(ccb, batch=batch, heads=heads, maxPages=pages, pageSize=128, tableStride=pages, weightStride=128 * pages)
+    for group, queries in ((1, 1), (8, 5), (1, 1 << 20)):
+        sizes = [ccb.ccb_kv8_attend_workspace_bytes(c, heads * group, queries, acc) for acc in (0, 1)]
+        assert 128 <= sizes[0] <= sizes[1]
+    assert ccb.ccb_kv8_evict_workspace_bytes(c, 128 * pages) >= 4 * batch * heads * 128 * pages
+
+
 def test_class_checks_its_tensors():
     torch = pytest.importorskip("torch")
     from cross_core_barrier_amd import kv8
