@@ -430,8 +430,8 @@ __device__ __forceinline__ Row row_of(const SelectArgs& a, int64_t row)
 }
 
 // Whether a token stays for sure, and whether it equals the threshold.
-__device__ __forceinline__ void judge(const Row& r, const Threshold& th, int32_t t, float w, bool& sure,
-                                      bool& equal)
+__device__ __forceinline__ void classify(const Row& r, const Threshold& th, int32_t t, float w, bool& sure,
+                                         bool& equal)
 {
     const bool middle = t >= r.low && t < r.high;
     const bool search = th.shift < 32;  // else none of the middle stays
@@ -502,7 +502,7 @@ __device__ __forceinline__ int2 count_kept(const Row& r, const Threshold& th, Ea
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             bool s, q;
-            judge(r, th, t + e, v[e], s, q);
+            classify(r, th, t + e, v[e], s, q);
             n.x += __popcll(__ballot(s)), n.y += __popcll(__ballot(q));
         }
     });
@@ -529,7 +529,7 @@ __device__ __forceinline__ void write_kept(const SelectArgs& a, const Row& r, co
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             bool isSure, isEqual;
-            judge(r, th, t + e, v[e], isSure, isEqual);
+            classify(r, th, t + e, v[e], isSure, isEqual);
             sure[e] = __ballot(isSure), equal[e] = __ballot(isEqual);
         }
 #pragma unroll
