@@ -72,64 +72,6 @@ __device__ __forceinline__ uint32_t narrow(float x)
     }
 }
 
-// Whether quotients were too near a border between two codes to be sure.
-// t, a product with 1 / s, is off by three roundings at most: 3 * 2^-24 of it.
-// Unsure is, for int8, within 2^-15 of a border (t <= 127: 2^-15.4), and for
-// e4m3 within 4 units of t's last place.  e4m3's step is the exponent's from
-// 2^-6 on and stays 2^-9 below: smaller quotients are looked at again, raised
-// by 2^-6 into the binade that has this step.
-template <int F>
-struct Near {
-    float d = 0.0f;                      // int8: largest distance to a code
-    uint32_t border = ~0u, small = ~0u;  // e4m3: place above a border's zone, size
-    static constexpr uint32_t kZone = 4;
-    __device__ __forceinline__ void look(uint32_t u)
-    {
-        // the 20 bits below e4m3's three, 0 where a border's zone begins
-        const uint32_t above = (u - (0x80000u - kZone)) << 12;
-        border = above < border ? above : border;
-    }
-    __device__ __forceinline__ bool unsure(const float* t)
-    {
-        if constexpr (F == kInt8) return d > 0.5f - 0x1p-15f;
-        if (small < (0x3c800000u << 1) - 1) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (fabsf(t[i]) < 0x1p-6f) look(bits(fabsf(t[i]) + 0x1p-6f));
-        }
-        return border <= (2 * kZone) << 12;
-    }
-};
-
-// Four quotients as the codes of one word.  None is further from 0 than the
-// largest code by more than its error: s is at least the largest value / Q.
-template <int F>
-__device__ __forceinline__ uint32_t encode4_near(const float* t, Near<F>& near)
-{
-    if constexpr (F == kInt8) {
-        uint32_t n[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float r = __builtin_rintf(t[i]);
-            near.d = fmaxf(near.d, fabsf(t[i] - r));
-            n[i] = (uint32_t)(int32_t)r;
-        }
-        const uint32_t a = __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400u);
-        const uint32_t b = __builtin_amdgcn_perm(n[3], n[2], 0x04000c0cu);
-        return a | b;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t u = bits(t[i]);
-            const uint32_t size = (u << 1) - 1;  // a 0 is not small
-            near.look(u);
-            near.small = size < near.small ? size : near.small;
-        }
-        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w, true);
-    }
-}
-
 // Eight new values as codes of the block scale s; inv is 1 / s.
 template <int F>
 __device__ __forceinline__ uint2 encode8(const float* x, float inv, float s)
@@ -158,24 +100,12 @@ __device__ __forceinline__ uint2 encode8(const float* x, float inv, float s)
 template <int F>
 __device__ __forceinline__ uint2 encode8_again(const uint2& w, float sOld, float inv, float s)
 {
-    if (!(s > 0.0f)) return make_uint2(0, 0);
-    float v[8], t[8];
+    float v[8];
     decode4<F>(w.x, v);
     decode4<F>(w.y, v + 4);
-    const float ratio = sOld * inv;
-    Near<F> near;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = v[i] * ratio;
-    uint2 u = make_uint2(encode4_near<F>(t, near), encode4_near<F>(t + 4, near));
-    if (near.unsure(t) || s > 0x1p120f) {
-        u = make_uint2(0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            u.x |= (uint32_t)encode_again<F>(v[i], sOld, inv, s) << (8 * i);
-            u.y |= (uint32_t)encode_again<F>(v[4 + i], sOld, inv, s) << (8 * i);
-        }
-    }
-    return u;
+    uint32_t u[2];
+    encode8_again<F>(v, sOld, inv, s, u);
+    return make_uint2(u[0], u[1]);
 }
 
 // The largest size among 16-bit values, two to a word, kept as bits: sizes

@@ -107,6 +107,99 @@ KV8_FN uint8_t encode_again(float v, float sOld, float inv, float s)
     return encode<F>(hi, fmaf(v, sOld, -hi), inv, s);
 }
 
+// Whether quotients were too near a border between two codes to be sure.
+// t, a product with 1 / s, is off by three roundings at most: 3 * 2^-24 of it.
+// Unsure is, for int8, within 2^-15 of a border (t <= 127: 2^-15.4), and for
+// e4m3 within 4 units of t's last place.  e4m3's step is the exponent's from
+// 2^-6 on and stays 2^-9 below: smaller quotients are looked at again, raised
+// by 2^-6 into the binade that has this step.
+template <int F>
+struct Near {
+    float d = 0.0f;                      // int8: largest distance to a code
+    uint32_t border = ~0u, small = ~0u;  // e4m3: place above a border's zone, size
+    static constexpr uint32_t kZone = 4;
+    KV8_FN void look(uint32_t u)
+    {
+        // the 20 bits below e4m3's three, 0 where a border's zone begins
+        const uint32_t above = (u - (0x80000u - kZone)) << 12;
+        border = above < border ? above : border;
+    }
+    KV8_FN bool unsure(const float* t)
+    {
+        if constexpr (F == kInt8) return d > 0.5f - 0x1p-15f;
+        if (small < (0x3c800000u << 1) - 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (fabsf(t[i]) < 0x1p-6f) look(bits(fabsf(t[i]) + 0x1p-6f));
+        }
+        return border <= (2 * kZone) << 12;
+    }
+};
+
+// Four quotients as the codes of one word (on the host: what the conversion
+// instructions give).  None is further from 0 than the largest code by more
+// than its error: s is at least the largest value / Q.
+template <int F>
+KV8_FN uint32_t encode4_near(const float* t, Near<F>& near)
+{
+    if constexpr (F == kInt8) {
+        uint32_t n[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float r = __builtin_rintf(t[i]);
+            near.d = fmaxf(near.d, fabsf(t[i] - r));
+            n[i] = (uint32_t)(int32_t)r;
+        }
+#ifdef __HIP_DEVICE_COMPILE__
+        const uint32_t a = __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400u);
+        const uint32_t b = __builtin_amdgcn_perm(n[3], n[2], 0x04000c0cu);
+        return a | b;
+#else
+        return (n[0] & 255) | (n[1] & 255) << 8 | (n[2] & 255) << 16 | n[3] << 24;
+#endif
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t u = bits(t[i]);
+            const uint32_t size = (u << 1) - 1;  // a 0 is not small
+            near.look(u);
+            near.small = size < near.small ? size : near.small;
+        }
+#ifdef __HIP_DEVICE_COMPILE__
+        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w, true);
+#else
+        uint32_t w = 0;
+        for (int i = 0; i < 4; ++i)
+            w |= (uint32_t)(t[i] != t[i] ? 0x7F : encode<F>(t[i], 0.0f, 1.0f, 1.0f)) << (8 * i);
+        return w;
+#endif
+    }
+}
+
+// Eight codes' values v of the block scale sOld as codes of the scale s, two
+// words; inv is 1 / s.
+template <int F>
+KV8_FN void encode8_again(const float* v, float sOld, float inv, float s, uint32_t* w)
+{
+    w[0] = w[1] = 0;
+    if (!(s > 0.0f)) return;
+    float t[8];
+    // Infinite only where every code is 0 (a code of 2^-9 would need an s above
+    // sOld * 2^-18), and 0 has to stay 0.
+    const float ratio = fminf(sOld * inv, 0x1.fffffep127f);
+    Near<F> near;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[i] * ratio;
+    w[0] = encode4_near<F>(t, near);
+    w[1] = encode4_near<F>(t + 4, near);
+    if (near.unsure(t) || s > 0x1p120f) {
+        w[0] = w[1] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)encode_again<F>(v[i], sOld, inv, s) << (8 * (i & 3));
+    }
+}
+
 // lens[b] where it is possible, else -1.
 KV8_FN int32_t checked_len(int32_t len, int32_t capacity)
 {

@@ -803,3 +803,36 @@ def test_capacity_far_beyond_the_lengths(kv8):
         c = _host(rng, "int8", lens, 2, 128, 64, width=200, extra=0)
         _say(f"attend {lens} of 25600, window={window}")
         _attend_case(kv8, 31, "int8", "fp16", lens, 2, 4, 64, 128, queries=2, window=window, c=c)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("P,D", [(16, 64), (128, 256)])
+def test_evict_zero_codes_of_a_loud_block(kv8, fmt, P, D):
+    """A token of zeros out of a block whose scale is 2^130 times the one its
+    new block gets: it stays zeros beside the quiet tokens."""
+    rng = np.random.default_rng(50)
+    lens = [2 * P, 2 * P]
+    c = _host(rng, fmt, lens, 2, P, D, extra=8)
+    for b in range(2):
+        for w in ("k", "v"):
+            c[w + "s"][c["table"][b, 0]] = np.float32(2.0 ** 66)
+            c[w + "s"][c["table"][b, 1]] = np.float32(2.0 ** -64)
+            c[w][c["table"][b, 0], :, 3] = 0
+    c["weight"] = np.zeros((2, 2, c["table"].shape[1] * P), np.float32)
+    c["weight"][:, :, [3, P + 5, P + 6]] = 1
+    free = np.setdiff1d(np.arange(c["k"].shape[0]), c["table"])[:2].astype(np.int32).reshape(2, 1)
+    cache = _device(kv8, c)
+    to = kv8.Kv8Cache(cache.k, cache.v, cache.k_scale, cache.v_scale, torch.from_numpy(free).cuda(),
+                      torch.zeros(2, dtype=torch.int32, device="cuda"))
+    kept = torch.zeros((2, 2, 3), dtype=torch.int32, device="cuda")
+    _say(f"evict zero codes of a loud block {fmt} P={P} D={D}")
+    cache.evict(to, 3, kept=kept)
+    assert kept.tolist() == [[[3, P + 5, P + 6]] * 2] * 2
+    dst = dict(c, table=free, lens=np.zeros(2, np.int32), weight=None)
+    oracle.evict(c, dst, 3, 0, 0)
+    for got, which in zip(to.read(3), ("k", "v")):
+        for b in range(2):
+            assert np.all(got[b, 0].cpu().numpy() == 0)
+            for h in range(2):
+                want = oracle.dense(dst, which, b, h, np.arange(3)).astype(np.float32)
+                assert np.array_equal(got[b, :, h].cpu().numpy(), want)

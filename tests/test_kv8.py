@@ -312,3 +312,49 @@ def test_class_checks_its_tensors():
         c.attend_workspace(3)
     with pytest.raises(ValueError):
         kv8.Kv8Cache.allocate(4, 2, 16, 64, 1, 2, fmt="int4", device="cpu")
+
+
+# --- codes under another scale, eight at a time ------------------------------------------
+
+@pytest.fixture(scope="module")
+def again(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("kv8again") / "again_driver")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-ffp-contract=off", "-Wno-unknown-pragmas", "-I",
+                    os.path.join(ROOT, "cross_core_barrier_amd", "csrc"),
+                    os.path.join(HERE, "kv8", "again_driver.cpp"), "-o", exe], check=True)
+
+    def run(fmt, v, s0, s1):
+        """Values [n, 8] of codes under the scales s0 [n], as codes under s1 [n]."""
+        rec = np.concatenate([v, np.stack([s0, s1], 1)], 1).astype(np.float32)
+        res = subprocess.run([exe, FMT[fmt]], input=rec.tobytes(), capture_output=True, check=True)
+        return np.frombuffer(res.stdout, np.uint8).reshape(-1, 8)
+    return run
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_zero_codes_of_a_loud_block_stay_zero(again, fmt):
+    """A token whose codes are all 0 fits every new scale, also one that its
+    own block's scale is 2^128 and more times as large as."""
+    s0 = 2.0 ** np.array([66, 100, 127, 64, 0, 60])
+    s1 = 2.0 ** np.array([-64, -64, -64, -64, -64, 60.0])
+    got = again(fmt, np.zeros((6, 8)), s0, s1)
+    assert np.array_equal(oracle.values(got, fmt), np.zeros((6, 8)))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_eight_codes_round_once(again, fmt):
+    """Every code at random scales and at ratios that put codes on borders."""
+    rng = np.random.default_rng(3)
+    codes = np.array([c for c in range(256) if c not in ((0x80,) if fmt == "int8" else (0x7F, 0xFF))], np.uint8)
+    values = oracle.values(codes, fmt)
+    rows, s0, s1 = [], [], []
+    for trial in range(40):
+        a = np.float32(rng.uniform(1, 2) * 2.0 ** int(rng.integers(-60, 60)))
+        b = np.float32(a * np.float32([1.0, 2.0, 3.0, 6.0, 5.0, 4.0, 1.5, 64.0][trial] if trial < 8 else rng.uniform(1, 30)))
+        rows.append(np.resize(values, (32, 8)))
+        s0 += [a] * 32
+        s1 += [b] * 32
+    v = np.concatenate(rows)
+    got = again(fmt, v, np.array(s0), np.array(s1))
+    want = [[oracle.nearest_code(_exact(x) * _exact(a) / _exact(b), fmt) for x in row] for row, a, b in zip(v, s0, s1)]
+    assert np.array_equal(oracle.values(got, fmt), oracle.values(np.array(want, np.uint8), fmt))
