@@ -109,6 +109,13 @@ CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
     if ((st = check_rows(q, false)) != CCB_OK) return st;
     if ((st = check_rows(out, false)) != CCB_OK) return st;
     if (q->type != out->type) return CCB_ERR_INVALID_VALUE;
+    if (q->data == out->data) {  // in place: row by row, and with nothing that needs the queries later
+        if ((cache->batch > 1 && q->strideBatch != out->strideBatch) ||
+            (nQuery > 1 && q->strideToken != out->strideToken) ||
+            (headsQ > 1 && q->strideHead != out->strideHead) ||
+            (accumulate != 0 && !ccb::kv8_attend_keeps_scores(*cache, headsQ, nQuery)))
+            return CCB_ERR_INVALID_VALUE;
+    }
     if (ws == nullptr) return CCB_ERR_NULL_POINTER;
     if (wsBytes < ccb_kv8_attend_workspace_bytes(cache, headsQ, nQuery, accumulate))
         return CCB_ERR_INVALID_VALUE;

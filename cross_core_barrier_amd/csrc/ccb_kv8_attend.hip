@@ -37,6 +37,16 @@
 #include "ccb_kv8_internal.h"
 #include "ccb_kv8_device.h"
 
+// Scores are kept for the weights where that moves less than reading the
+// keys again (8 bytes a row and token against headDim a token), and for up
+// to 64 rows where all of them stay in the caches: there a launch less
+// counts for more.
+bool ccb::kv8_attend_keeps_scores(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery)
+{
+    const int64_t pairs = (int64_t)c.batch * c.heads, rows = (int64_t)nQuery * (headsQ / c.heads);
+    return rows <= 16 || (rows <= 64 && pairs * rows * c.maxPages * c.pageSize * 4 <= (32 << 20));
+}
+
 namespace {
 
 using namespace kv8;
@@ -938,11 +948,7 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
         bytes += ((size_t)n * each + 127) / 128 * 128;
         return here;
     };
-    // Scores are kept for the weights where that moves less than reading the
-    // keys again (8 bytes a row and token against headDim a token), and for up
-    // to 64 rows where all of them stay in the caches: there a launch less
-    // counts for more.
-    const bool stored = accumulate && (rows <= 16 || (rows <= 64 && pairs * rows * room * 4 <= (32 << 20)));
+    const bool stored = accumulate && ccb::kv8_attend_keeps_scores(c, headsQ, nQuery);
     p.direct = p.splits == 1 && (p.rowBlocks == 1 || !stored);
     const int64_t parts = mostSplits > 1 || rows > 16 ? pairs * mostSplits * rows : 0;
     p.partO = (float*)take(parts * c.headDim, sizeof(float));

@@ -24,6 +24,9 @@ struct Kv8AttendArgs {
     int32_t* err;
 };
 
+// Whether a call that accumulates weights keeps its scores for them; else it
+// reads the queries again after the results are written.
+bool kv8_attend_keeps_scores(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery);
 size_t kv8_attend_bytes(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, int32_t accumulate);
 hipError_t kv8_attend(const Kv8AttendArgs& a, hipStream_t s);
 

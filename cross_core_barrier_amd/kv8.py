@@ -149,7 +149,9 @@ class Kv8Cache:
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None, stream=None):
         """Attention of q [batch, queries, q_heads, head_dim], the sequences'
-        last tokens; scale None is 1 / sqrt(head_dim).  Returns (out, lse)."""
+        last tokens; scale None is 1 / sqrt(head_dim).  Returns (out, lse).
+        out may be q itself, but for weights accumulated over many rows (more
+        than 64 a cache head, or 16 in a large cache; refused)."""
         _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
         shape = q.shape
         queries, q_heads = shape[1], shape[2]

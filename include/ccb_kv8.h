@@ -115,13 +115,18 @@ CCB_API ccbStatus ccb_kv8_append(const ccbKv8Cache* cache, const ccbKv8Rows* kNe
  * itself, and out is rounded once to its type.  accumulate != 0 adds to weight[b][head][t]
  * the sum of exp(s_t - lse) over the queries and the query heads of that head.
  * Results do not depend on timing: the same call gives the same bits.
- *   q, out  [batch][nQuery][headsQ][headDim], of one type
+ *   q, out  [batch][nQuery][headsQ][headDim], of one type.  out may be q itself
+ *           (the same data and strides) and overlaps it in no other way; but not
+ *           where accumulate needs the queries again after out is written: with
+ *           R = headsQ / heads * nQuery rows for a cache head, where R > 64, or
+ *           R > 16 and 4 * batch * heads * R * maxPages * pageSize > 2^25.
  *   lse     device float [batch][nQuery][headsQ], or NULL
  *   ws      device, ccb_kv8_attend_workspace_bytes(...) bytes, 128-B aligned,
  *           whatever it holds.  Calls that overlap in time need their own.
  * Errors: NULL_POINTER (also accumulate without weight), INVALID_VALUE (as
  * above; headsQ not a multiple of heads, nQuery or window < 0, more than 2^20 rows
- * (headsQ / heads * nQuery), a scale that is not finite, a workspace too small), UNSUPPORTED_DEVICE, HIP. */
+ * (headsQ / heads * nQuery), a scale that is not finite, out over q as above, a
+ * workspace too small), UNSUPPORTED_DEVICE, HIP. */
 CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
                                  const ccbKv8Rows* out, float* lse, int32_t headsQ, int32_t nQuery,
                                  float scale, int32_t window, int32_t accumulate, void* ws,

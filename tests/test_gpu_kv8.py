@@ -836,3 +836,26 @@ def test_evict_zero_codes_of_a_loud_block(kv8, fmt, P, D):
             for h in range(2):
                 want = oracle.dense(dst, which, b, h, np.arange(3)).astype(np.float32)
                 assert np.array_equal(got[b, :, h].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("queries,accumulate", [(1, True), (6, True), (33, False), (33, True)])
+def test_attend_in_place(kv8, queries, accumulate):
+    """out = q gives what a separate out does, or is refused (weights over more
+    rows than keep their scores) and changes nothing."""
+    from cross_core_barrier_amd import ccb
+    rng = np.random.default_rng(51)
+    c = _host(rng, "int8", [700, 0, 33], 2, 32, 64)
+    c["weight"] = np.zeros((3, 2, c["table"].shape[1] * 32), np.float32)
+    a, b = _device(kv8, c), _device(kv8, c)
+    q = torch.from_numpy(rng.normal(0, 1, (3, queries, 6, 64))).half().cuda()
+    want, lse = a.attend(q, accumulate=accumulate)
+    mine = q.clone()
+    _say(f"attend in place, {queries} queries, accumulate={accumulate}")
+    if accumulate and 3 * queries > 64:
+        with pytest.raises(ccb.CcbError):
+            b.attend(mine, accumulate=True, out=mine)
+        assert torch.equal(mine, q) and float(b.weight.abs().max()) == 0
+        return
+    got, got_lse = b.attend(mine, accumulate=accumulate, out=mine)
+    assert got is mine and torch.equal(got, want) and torch.equal(got_lse, lse)
+    assert torch.equal(a.weight, b.weight)

@@ -358,3 +358,21 @@ def test_eight_codes_round_once(again, fmt):
     got = again(fmt, v, np.array(s0), np.array(s1))
     want = [[oracle.nearest_code(_exact(x) * _exact(a) / _exact(b), fmt) for x in row] for row, a, b in zip(v, s0, s1)]
     assert np.array_equal(oracle.values(got, fmt), oracle.values(np.array(want, np.uint8), fmt))
+
+
+def test_attend_refuses_to_overwrite_queries_it_needs_again(ccb):
+    """Weights whose scores are not kept are computed from the queries after
+    the results are written."""
+    inv, big = ccb.CCB_ERR_INVALID_VALUE, 1 << 40
+
+    def attend(cache, out, n, acc):
+        q = _rows(ccb, strideBatch=1 << 20, strideToken=256)
+        return ccb.ccb_kv8_attend(cache, q, out, None, 4, n, 0.1, 0, acc, 9 << 20, big)
+    same = _rows(ccb, strideBatch=1 << 20, strideToken=256)
+    assert attend(_cache(ccb), same, 33, 1) == inv  # 66 rows
+    wide = dict(maxPages=1 << 13, tableStride=1 << 13, weightStride=1 << 17)
+    assert attend(_cache(ccb, **wide), same, 10, 1) == inv  # 20 rows, 63 MB of scores
+    # rows that begin alike and then part
+    for other in (dict(strideBatch=1 << 21, strideToken=256), dict(strideBatch=1 << 20, strideToken=512),
+                  dict(strideBatch=1 << 20, strideToken=256, strideHead=128)):
+        assert attend(_cache(ccb), _rows(ccb, **other), 2, 0) == inv, other
