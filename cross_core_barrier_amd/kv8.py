@@ -42,7 +42,8 @@ class Kv8Cache:
     k, v [pages, heads, page_size, head_dim] (int8 or float8_e4m3fn); k_scale,
     v_scale [pages, heads] float32; page_table [batch, max_pages] int32; lens
     [batch] int32; weight [batch, heads, at least max_pages * page_size]
-    float32 or None.  All contiguous, but for the page table's rows."""
+    float32 or None.  All contiguous, but for the page table's rows, and on one
+    GPU: a cache on the CPU can be made, but every call on it is refused."""
 
     def __init__(self, k, v, k_scale, v_scale, page_table, lens, weight=None):
         _need(k.dim() == 4 and k.dtype in _CODES, "k: [pages, heads, page_size, head_dim], int8 or float8_e4m3fn")
@@ -65,7 +66,7 @@ class Kv8Cache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.page_table, self.lens, self.weight = page_table, lens, weight
         self.heads, self.head_dim, self.batch, self.device = heads, head_dim, batch, k.device
-        self._index = k.get_device()
+        self._index = k.get_device()  # -1 on the CPU
         self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._c = ccb.ccbKv8Cache(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
@@ -86,6 +87,11 @@ class Kv8Cache:
         weight = torch.zeros((batch, heads, max_pages * page_size), dtype=torch.float32, device=device) \
             if weights else None
         return cls(k, v, ks, vs, table, lens, weight)
+
+    def _on_gpu(self) -> None:
+        """Before anything else in every call: what follows compares devices
+        with the cache's only, and the kernels get raw addresses."""
+        _need(self._index >= 0, "the cache's tensors are not on a GPU")
 
     def _rows(self, t: torch.Tensor, heads: int, what: str):
         kind = _ROWS.get(t.dtype)
@@ -131,6 +137,7 @@ class Kv8Cache:
                stream=None) -> None:
         """Write each sequence's counts[b] (None: all) new tokens as its last
         ones; lens counts them already.  k_new, v_new [batch, n, heads, head_dim]."""
+        self._on_gpu()
         k, v = self._rows(k_new, self.heads, "k_new"), self._rows(v_new, self.heads, "v_new")
         n = k_new.shape[1]
         _need(n == v_new.shape[1] and k.type == v.type, "v_new: shape and dtype of k_new")
@@ -141,6 +148,7 @@ class Kv8Cache:
 
     def attend_workspace(self, q_heads: int, queries: int = 1, accumulate: bool = False) -> torch.Tensor:
         """A workspace for attend() calls of these sizes that follow each other."""
+        self._on_gpu()
         n = ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
         _need(n > 0, "attend: sizes that ccb_kv8_attend refuses")
         return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -152,6 +160,7 @@ class Kv8Cache:
         last tokens; scale None is 1 / sqrt(head_dim).  Returns (out, lse).
         out may be q itself, but for weights accumulated over many rows (more
         than 64 a cache head, or 16 in a large cache; refused)."""
+        self._on_gpu()
         _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
         shape = q.shape
         queries, q_heads = shape[1], shape[2]
@@ -178,6 +187,7 @@ class Kv8Cache:
 
     def evict_workspace(self, budget: int) -> torch.Tensor:
         """A workspace for evict() calls with this budget that follow each other."""
+        self._on_gpu()
         n = ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
         _need(n > 0, "evict: sizes that ccb_kv8_evict refuses")
         return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -188,6 +198,7 @@ class Kv8Cache:
         """Copy the budget tokens of each sequence and head with the largest
         weight (and its first `sinks` and last `recent`) into the cache `to`.
         kept [batch, heads, budget] int32 gets their numbers; it is returned."""
+        self._on_gpu()
         _need(to._index == self._index, "to: on the cache's device")
         self._ints(kept, (self.batch, self.heads, budget), "kept")
         s = None if stream is None else _enter(stream, self.device)
@@ -200,6 +211,7 @@ class Kv8Cache:
     def read(self, count: int, first: Optional[torch.Tensor] = None, dtype=torch.float32, stream=None):
         """The values of `count` tokens of each sequence from first[b] (None: 0)
         as (k, v) [batch, count, heads, head_dim]; zeros where there is none."""
+        self._on_gpu()
         kind = _ROWS.get(dtype)
         _need(kind is not None, "dtype: float32, bfloat16 or float16")
         self._ints(first, (self.batch,), "first")

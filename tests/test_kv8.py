@@ -376,3 +376,34 @@ def test_attend_refuses_to_overwrite_queries_it_needs_again(ccb):
     for other in (dict(strideBatch=1 << 21, strideToken=256), dict(strideBatch=1 << 20, strideToken=512),
                   dict(strideBatch=1 << 20, strideToken=256, strideHead=128)):
         assert attend(_cache(ccb), _rows(ccb, **other), 2, 0) == inv, other
+
+
+@pytest.fixture
+def cpu_cache(monkeypatch):
+    """A whole cache on the CPU, and what reached the library of it: its entry
+    points record their names and enqueue nothing."""
+    torch = pytest.importorskip("torch")
+    from cross_core_barrier_amd import ccb, kv8
+    reached = []
+    for name in ("append", "attend", "evict", "read"):
+        monkeypatch.setattr(ccb, f"ccb_kv8_{name}", lambda *a, _n=name: reached.append(_n) or 0)
+    monkeypatch.setattr(kv8, "_current_stream", lambda index: 0)
+    make = lambda: kv8.Kv8Cache.allocate(8, 2, 16, 64, 3, 2, "int8", weights=True, device="cpu")  # noqa: E731
+    x = torch.zeros((3, 1, 2, 64), dtype=torch.bfloat16)
+    q = torch.zeros((3, 1, 4, 64), dtype=torch.bfloat16)
+    calls = {
+        "append": lambda c: c.append(x, x), "attend": lambda c: c.attend(q, accumulate=True),
+        "evict": lambda c: c.evict(make(), 8, recent=2), "read": lambda c: c.read(5),
+        "attend_workspace": lambda c: c.attend_workspace(4), "evict_workspace": lambda c: c.evict_workspace(8),
+    }
+    return make, calls, reached
+
+
+def test_no_call_on_cpu_tensors_reaches_a_kernel(cpu_cache):
+    """Well-shaped calls on a cache in host memory are refused before the
+    library gets its addresses."""
+    make, calls, reached = cpu_cache
+    for name, call in calls.items():
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call(make())
+        assert reached == [], name
