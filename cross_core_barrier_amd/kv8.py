@@ -10,9 +10,10 @@ only; every step runs in libccb.so's HIP kernels.
     out, lse = cache.attend(q, accumulate=True)  # q [batch, 1, q_heads, head_dim]
     kept = cache.evict(smaller, budget=1024, recent=128, sinks=4)
 
-Calls run on torch's current stream, or on `stream` (a torch.cuda.Stream or a
-raw hipStream_t) after the work already queued on the current stream, which
-is then ordered after them.  They copy nothing to the host.  Bad page numbers,
+Calls run on the cache's device, whichever is current: on torch's current
+stream there, or on `stream` (a torch.cuda.Stream or a raw hipStream_t of that
+device) after the work already queued on the current stream, which is then
+ordered after them.  They copy nothing to the host.  Bad page numbers,
 lengths and counts are met on the device: they set `cache.err`, which
 `cache.check()` reads (and waits for).
 """
@@ -29,6 +30,7 @@ from .workloads import _enter, _leave
 _CODES = {torch.int8: ccb.CCB_KV8_INT8, torch.float8_e4m3fn: ccb.CCB_KV8_E4M3}
 _FORMATS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 _current_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: a tenth of the object's cost
+_current_device = torch._C._cuda_getDevice
 _ROWS = {torch.bfloat16: ccb.CCB_KV8_BF16, torch.float16: ccb.CCB_KV8_FP16, torch.float32: ccb.CCB_KV8_FP32}
 
 
@@ -126,10 +128,25 @@ class Kv8Cache:
         _need(ws.is_contiguous() and ws.get_device() == self._index, "workspace: contiguous, on the cache's device")
         return ws, ws.nbytes
 
-    def _finish(self, status: int, what: str, s) -> None:
-        """Raise a call's error; order torch's stream after a call on `s`."""
+    def _enter(self, stream):
+        """The caller's stream, ordered after torch's; None for torch's own."""
+        if stream is None:
+            return None
+        _need(not isinstance(stream, torch.cuda.Stream) or stream.device_index == self._index,
+              "stream: one of the cache's device")
+        return _enter(stream, self.device)
+
+    def _call(self, fn, s, *args) -> None:
+        """An entry point with the cache's device current, on `s` or torch's
+        stream there; raises its error and orders torch's stream after `s`."""
+        stream = s or _current_stream(self._index)
+        if _current_device() == self._index:
+            status = fn(*args, stream)
+        else:
+            with torch.cuda.device(self._index):
+                status = fn(*args, stream)
         if status != ccb.CCB_OK:
-            raise ccb.CcbError(status, what)
+            raise ccb.CcbError(status, fn.__name__)
         if s is not None:
             _leave(s, self.device)
 
@@ -142,9 +159,8 @@ class Kv8Cache:
         n = k_new.shape[1]
         _need(n == v_new.shape[1] and k.type == v.type, "v_new: shape and dtype of k_new")
         self._ints(counts, (self.batch,), "counts")
-        s = None if stream is None else _enter(stream, self.device)
-        self._finish(ccb.ccb_kv8_append(self._c, k, v, n, counts, self.err, s or _current_stream(self._index)),
-                     "ccb_kv8_append", s)
+        s = self._enter(stream)
+        self._call(ccb.ccb_kv8_append, s, self._c, k, v, n, counts, self.err)
 
     def attend_workspace(self, q_heads: int, queries: int = 1, accumulate: bool = False) -> torch.Tensor:
         """A workspace for attend() calls of these sizes that follow each other."""
@@ -164,7 +180,7 @@ class Kv8Cache:
         _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
         shape = q.shape
         queries, q_heads = shape[1], shape[2]
-        s = None if stream is None else _enter(stream, self.device)
+        s = self._enter(stream)
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=q.device)
             if s is not None:
@@ -180,9 +196,8 @@ class Kv8Cache:
         need = 0 if workspace is not None else \
             ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
         ws, size = self._space(workspace, need, s)
-        self._finish(ccb.ccb_kv8_attend(self._c, qr, outr, lse, q_heads, queries,
-                                        self.head_dim ** -0.5 if scale is None else scale, window, int(accumulate), ws,
-                                        size, self.err, s or _current_stream(self._index)), "ccb_kv8_attend", s)
+        self._call(ccb.ccb_kv8_attend, s, self._c, qr, outr, lse, q_heads, queries,
+                   self.head_dim ** -0.5 if scale is None else scale, window, int(accumulate), ws, size, self.err)
         return out, lse
 
     def evict_workspace(self, budget: int) -> torch.Tensor:
@@ -201,11 +216,10 @@ class Kv8Cache:
         self._on_gpu()
         _need(to._index == self._index, "to: on the cache's device")
         self._ints(kept, (self.batch, self.heads, budget), "kept")
-        s = None if stream is None else _enter(stream, self.device)
+        s = self._enter(stream)
         need = 0 if workspace is not None else ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
         ws, size = self._space(workspace, need, s)
-        self._finish(ccb.ccb_kv8_evict(self._c, to._c, budget, recent, sinks, kept, ws, size, self.err,
-                                       s or _current_stream(self._index)), "ccb_kv8_evict", s)
+        self._call(ccb.ccb_kv8_evict, s, self._c, to._c, budget, recent, sinks, kept, ws, size, self.err)
         return kept
 
     def read(self, count: int, first: Optional[torch.Tensor] = None, dtype=torch.float32, stream=None):
@@ -215,15 +229,14 @@ class Kv8Cache:
         kind = _ROWS.get(dtype)
         _need(kind is not None, "dtype: float32, bfloat16 or float16")
         self._ints(first, (self.batch,), "first")
-        s = None if stream is None else _enter(stream, self.device)
+        s = self._enter(stream)
         both = torch.empty((2, self.batch, count, self.heads, self.head_dim), dtype=dtype, device=self.device)
         if s is not None:
             both.record_stream(s)
         k, v = both.unbind(0)
         row = self.heads * self.head_dim
-        self._finish(ccb.ccb_kv8_read(self._c, ccb.ccbKv8Rows(k.data_ptr(), count * row, row, self.head_dim, kind, 0),
-                                      ccb.ccbKv8Rows(v.data_ptr(), count * row, row, self.head_dim, kind, 0), count,
-                                      first, self.err, s or _current_stream(self._index)), "ccb_kv8_read", s)
+        self._call(ccb.ccb_kv8_read, s, self._c, ccb.ccbKv8Rows(k.data_ptr(), count * row, row, self.head_dim, kind, 0),
+                   ccb.ccbKv8Rows(v.data_ptr(), count * row, row, self.head_dim, kind, 0), count, first, self.err)
         return k, v
 
     def check(self) -> None:

@@ -407,3 +407,34 @@ def test_no_call_on_cpu_tensors_reaches_a_kernel(cpu_cache):
         with pytest.raises(ValueError, match="not on a GPU"):
             call(make())
         assert reached == [], name
+
+
+def test_calls_run_on_the_cache_s_device(cpu_cache, monkeypatch):
+    """The entry points act on the current device: the class makes the cache's
+    current for the call, and leaves it alone where it is already."""
+    import contextlib
+    from cross_core_barrier_amd import ccb, kv8
+    torch = pytest.importorskip("torch")
+    make, calls, reached = cpu_cache
+    current = [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+    where = []
+    for name in ("append", "attend", "evict", "read"):
+        def entry(*a):
+            where.append(current[0])
+            return 0
+        monkeypatch.setattr(ccb, f"ccb_kv8_{name}", entry)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(kv8, "_current_device", lambda: current[0], raising=False)
+    monkeypatch.setattr(kv8.Kv8Cache, "_on_gpu", lambda self: None)  # the CPU's index, -1, plays another GPU's
+    for other in (0, -1):
+        current[0] = other
+        for name in ("append", "attend", "evict", "read"):
+            del where[:]
+            calls[name](make())
+            assert where == [-1] and current[0] == other, name
