@@ -40,7 +40,8 @@ def _need(ok: bool, what: str) -> None:
 
 
 class Kv8Cache:
-    """A cache in the caller's tensors (they are kept, not copied):
+    """A cache in the caller's tensors (they are kept, not copied, and stay
+    the same tensors with the same storage for the cache's life):
     k, v [pages, heads, page_size, head_dim] (int8 or float8_e4m3fn); k_scale,
     v_scale [pages, heads] float32; page_table [batch, max_pages] int32; lens
     [batch] int32; weight [batch, heads, at least max_pages * page_size]
@@ -75,6 +76,14 @@ class Kv8Cache:
             lens.data_ptr(), 0 if weight is None else weight.data_ptr(),
             page_table.stride(0) if batch > 1 else max_pages, 0 if weight is None else weight.shape[2],
             _CODES[k.dtype], pages, heads, page_size, head_dim, batch, max_pages, 0)
+
+    def __setattr__(self, name: str, value) -> None:
+        """The kernels get the addresses that the constructor saw: a tensor's
+        contents may change (cache.lens += 1, cache.lens[...] = ...), the
+        tensor may not."""
+        if self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name}: change the tensor in place, or make another Kv8Cache")
+        object.__setattr__(self, name, value)
 
     @classmethod
     def allocate(cls, pages: int, heads: int, page_size: int, head_dim: int, batch: int, max_pages: int,

@@ -438,3 +438,21 @@ def test_calls_run_on_the_cache_s_device(cpu_cache, monkeypatch):
             del where[:]
             calls[name](make())
             assert where == [-1] and current[0] == other, name
+
+
+def test_tensors_of_a_cache_change_in_place_only(cpu_cache):
+    """The library holds their addresses: another tensor in their place would
+    leave it with freed memory."""
+    make, _, _ = cpu_cache
+    c = make()
+    for name in ("k", "v", "k_scale", "v_scale", "page_table", "lens", "weight", "err", "heads", "head_dim", "batch",
+                 "device", "_c", "_index"):
+        before = getattr(c, name)
+        with pytest.raises(AttributeError):
+            setattr(c, name, before + 1 if isinstance(before, int) else None)
+        assert getattr(c, name) is before, name
+    at = c.lens.data_ptr()
+    c.lens += 1
+    c.lens[0] = 7
+    assert c.lens.tolist() == [7, 1, 1] and c.lens.data_ptr() == at
+    assert c._c.lens == at
