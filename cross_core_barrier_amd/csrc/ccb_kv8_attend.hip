@@ -776,7 +776,12 @@ __global__ __launch_bounds__(kThreads) void kv8_k_join(Plan p, int32_t D)
             }
         }
         sum[tid] = o;
-        if (many) __syncthreads();
+        if (many) {
+            __syncthreads();
+        } else {  // a row's lanes are one wave's, whose LDS accesses keep the program's order
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
         if (me < V) {
             for (int32_t i = 1; i < groups; ++i) o += sum[(tid - me) + i * V + d4];
             write_row<T>(p, b, h, pair, row, d4, o, top, all);
