@@ -12,6 +12,7 @@ namespace {
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+constexpr size_t kLeastWorkspace = 128;
 constexpr int64_t kMaxTokens = 1 << 30;  // of one sequence
 
 ccbStatus check_cache(const ccbKv8Cache* c)
@@ -80,7 +81,7 @@ CCB_API ccbStatus ccb_kv8_append(const ccbKv8Cache* cache, const ccbKv8Rows* kNe
     if (cache->batch == 0 || nNew == 0) return CCB_OK;
     if ((st = check_rows(kNew, false)) != CCB_OK) return st;
     if ((st = check_rows(vNew, false)) != CCB_OK) return st;
-    if (kNew->type != vNew->type) return CCB_ERR_INVALID_VALUE;
+    if (kNew->type != vNew->type || !ccb::kv8_append_fits(*cache, nNew)) return CCB_ERR_INVALID_VALUE;
     if ((st = ccb::device_ready()) != CCB_OK) return st;
     return done(ccb::kv8_append(*cache, *kNew, *vNew, nNew, counts, err, (hipStream_t)stream));
 }
@@ -90,7 +91,7 @@ CCB_API size_t ccb_kv8_attend_workspace_bytes(const ccbKv8Cache* cache, int32_t 
 {
     if (check_cache(cache) != CCB_OK || !attend_sizes_ok(cache, headsQ, nQuery)) return 0;
     const size_t n = ccb::kv8_attend_bytes(*cache, headsQ, nQuery, accumulate);
-    return n < 128 ? 128 : n;
+    return n < kLeastWorkspace ? kLeastWorkspace : n;
 }
 
 CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
@@ -117,7 +118,8 @@ CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
             return CCB_ERR_INVALID_VALUE;
     }
     if (ws == nullptr) return CCB_ERR_NULL_POINTER;
-    if (wsBytes < ccb_kv8_attend_workspace_bytes(cache, headsQ, nQuery, accumulate))
+    if (wsBytes < kLeastWorkspace ||
+        !ccb::kv8_attend_fits(*cache, headsQ, nQuery, window, accumulate != 0, wsBytes))
         return CCB_ERR_INVALID_VALUE;
     if ((st = ccb::device_ready()) != CCB_OK) return st;
     ccb::Kv8AttendArgs a;
@@ -139,7 +141,7 @@ CCB_API size_t ccb_kv8_evict_workspace_bytes(const ccbKv8Cache* from, int32_t bu
 {
     if (check_cache(from) != CCB_OK || budget < 1 || budget > kMaxTokens) return 0;
     const size_t n = ccb::kv8_evict_bytes(*from, budget);
-    return n < 128 ? 128 : n;
+    return n < kLeastWorkspace ? kLeastWorkspace : n;
 }
 
 CCB_API ccbStatus ccb_kv8_evict(const ccbKv8Cache* from, const ccbKv8Cache* to, int32_t budget,
@@ -160,7 +162,8 @@ CCB_API ccbStatus ccb_kv8_evict(const ccbKv8Cache* from, const ccbKv8Cache* to, 
     if (from->weight == nullptr || ws == nullptr) return CCB_ERR_NULL_POINTER;
     if (to->lens == from->lens || to->weight == from->weight || to->pageTable == from->pageTable)
         return CCB_ERR_INVALID_VALUE;
-    if (wsBytes < ccb_kv8_evict_workspace_bytes(from, budget)) return CCB_ERR_INVALID_VALUE;
+    if (wsBytes < ccb_kv8_evict_workspace_bytes(from, budget) || !ccb::kv8_evict_fits(*from, budget))
+        return CCB_ERR_INVALID_VALUE;
     if ((st = ccb::device_ready()) != CCB_OK) return st;
     return done(ccb::kv8_evict(*from, *to, budget, recent, sinks, kept, ws, err, (hipStream_t)stream));
 }
@@ -178,6 +181,7 @@ CCB_API ccbStatus ccb_kv8_read(const ccbKv8Cache* cache, const ccbKv8Rows* kOut,
     if (kOut != nullptr && (st = check_rows(kOut, true)) != CCB_OK) return st;
     if (vOut != nullptr && (st = check_rows(vOut, true)) != CCB_OK) return st;
     if (kOut != nullptr && vOut != nullptr && kOut->type != vOut->type) return CCB_ERR_INVALID_VALUE;
+    if (!ccb::kv8_read_fits(*cache, count, kOut != nullptr && vOut != nullptr ? 2 : 1)) return CCB_ERR_INVALID_VALUE;
     if ((st = ccb::device_ready()) != CCB_OK) return st;
     return done(ccb::kv8_read(*cache, kOut, vOut, count, first, err, (hipStream_t)stream));
 }

@@ -969,6 +969,14 @@ size_t make_plan(Plan& p, const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, 
     return bytes;
 }
 
+// Workgroups that share a pair's tokens when the weights are computed again.
+int64_t weight_blocks(const Plan& p, int64_t pairs)
+{
+    const int64_t each = ((int64_t)p.tiles + kWaves - 1) / kWaves;
+    const int64_t most = pairs < 4096 ? 8192 / pairs : 2;
+    return each < most ? each : most;
+}
+
 template <int F, int T, int D>
 hipError_t launch(const Plan& p, int64_t blocks, hipStream_t s)
 {
@@ -977,14 +985,11 @@ hipError_t launch(const Plan& p, int64_t blocks, hipStream_t s)
         kv8_k_attend<F, T, D, 1><<<grid, dim3(kRunThreads), 0, s>>>(p);
     else if constexpr (D <= 96)
         kv8_k_attend<F, T, D, 2><<<grid, dim3(kRunThreads), 0, s>>>(p);
-    const int64_t pairs = (int64_t)p.a.c.batch * p.a.c.heads;
     if (!p.direct)
         kv8_k_join<T><<<dim3((unsigned)p.joinBlocks), block, 0, s>>>(p, D);
     if (p.lse2 != nullptr) {
-        int64_t each = ((int64_t)p.tiles + kWaves - 1) / kWaves;
-        const int64_t most = pairs < 4096 ? 8192 / pairs : 2;
-        each = each < most ? each : most;
-        kv8_k_weights<F, T, D><<<dim3((unsigned)(pairs * each)), block, 0, s>>>(p, (int32_t)each);
+        const int64_t each = weight_blocks(p, p.pairs);
+        kv8_k_weights<F, T, D><<<dim3((unsigned)(p.pairs * each)), block, 0, s>>>(p, (int32_t)each);
     }
     return hipGetLastError();
 }
@@ -1000,15 +1005,26 @@ size_t kv8_attend_bytes(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, in
     return make_plan(p, c, headsQ, nQuery, 0, accumulate, nullptr);
 }
 
+bool kv8_attend_fits(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, int32_t window, int32_t accumulate,
+                     size_t wsBytes)
+{
+    const int64_t pairs = (int64_t)c.batch * c.heads;
+    if (pairs > INT32_MAX) return false;
+    Plan p;
+    return make_plan(p, c, headsQ, nQuery, window, accumulate, nullptr) <= wsBytes &&
+           kv8_launch_fits(pairs * p.rowBlocks * p.splits, kRunThreads) && pairs * p.rows <= INT32_MAX &&
+           (p.direct || kv8_launch_fits(p.joinBlocks, kThreads)) &&
+           (!accumulate || kv8_attend_keeps_scores(c, headsQ, nQuery) ||
+            kv8_launch_fits(pairs * weight_blocks(p, pairs), kThreads));
+}
+
 hipError_t kv8_attend(const Kv8AttendArgs& a, hipStream_t s)
 {
     const ccbKv8Cache& c = a.c;
     Plan p;
     p.a = a;
     make_plan(p, c, a.headsQ, a.nQuery, a.window, a.accumulate, a.ws);
-    const int64_t pairs = (int64_t)c.batch * c.heads;
-    const int64_t blocks = pairs * p.rowBlocks * p.splits;
-    if (blocks > INT32_MAX || pairs * p.rows > INT32_MAX || p.joinBlocks > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t blocks = (int64_t)p.pairs * p.rowBlocks * p.splits;
 #define KV8_ATTEND_DIM(F, T) \
     switch (c.headDim) { \
     case 64: return launch<F, T, 64>(p, blocks, s); \

@@ -729,13 +729,29 @@ __global__ __launch_bounds__(kSelThreads) void kv8_k_select_long(SelectArgs a)
 
 namespace ccb {
 
+// Blocks of the pages that n tokens can touch, starting anywhere in a page
+// (one workgroup at most is rounded up: see team_groups); 0 for too many.
+static int64_t touched_blocks(const ccbKv8Cache& c, int32_t n, int32_t sides)
+{
+    const int64_t pairs = (int64_t)c.batch * c.heads;
+    const int64_t span = ((int64_t)n + c.pageSize - 2) / c.pageSize + 1;
+    const int64_t blocks = pairs > INT32_MAX ? 0 : pairs * span * sides;
+    return blocks <= INT32_MAX && kv8_launch_fits(team_groups(blocks, c.pageSize), kThreads) ? blocks : 0;
+}
+
+bool kv8_append_fits(const ccbKv8Cache& c, int32_t nNew) { return touched_blocks(c, nNew, 2) != 0; }
+
+bool kv8_read_fits(const ccbKv8Cache& c, int32_t count, int32_t sides)
+{
+    return touched_blocks(c, count, sides) != 0;
+}
+
 hipError_t kv8_append(const ccbKv8Cache& c, const ccbKv8Rows& k, const ccbKv8Rows& v, int32_t nNew,
                       const int32_t* counts, int32_t* err, hipStream_t s)
 {
     // pages that nNew tokens can touch, starting anywhere in a page
     const int32_t span = (nNew + c.pageSize - 2) / c.pageSize + 1;
-    const int64_t blocks = (int64_t)c.batch * span * c.heads * 2;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t blocks = touched_blocks(c, nNew, 2);
     const uint32_t units = (uint32_t)blocks;
     const dim3 grid(team_groups(blocks, c.pageSize));
 #define KV8_APPEND(F, T, D) \
@@ -754,8 +770,7 @@ hipError_t kv8_read(const ccbKv8Cache& c, const ccbKv8Rows* k, const ccbKv8Rows*
     const int32_t sides = (k != nullptr ? 1 : 0) | (v != nullptr ? 2 : 0);
     // pages that count tokens can touch, starting anywhere in a page
     const int32_t span = (int32_t)(((int64_t)count + c.pageSize - 2) / c.pageSize + 1);
-    const int64_t blocks = (int64_t)c.batch * span * c.heads * (sides == 3 ? 2 : 1);
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t blocks = touched_blocks(c, count, sides == 3 ? 2 : 1);
     const ccbKv8Rows kr = k != nullptr ? *k : *v, vr = v != nullptr ? *v : *k;
     const uint32_t units = (uint32_t)blocks;
     const dim3 grid(team_groups(blocks, c.pageSize));
@@ -804,6 +819,17 @@ size_t kv8_evict_bytes(const ccbKv8Cache& from, int32_t budget)
     return select_plan(a, from, budget, nullptr);
 }
 
+bool kv8_evict_fits(const ccbKv8Cache& from, int32_t budget)
+{
+    const int64_t rows = (int64_t)from.batch * from.heads;
+    if (rows > INT32_MAX) return false;
+    SelectArgs a;
+    select_plan(a, from, budget, nullptr);
+    const int64_t blocks = rows * ((budget + from.pageSize - 1) / from.pageSize) * 2;
+    return kv8_launch_fits(rows * (a.segments > 0 ? a.segments : 1), kSelThreads) && blocks <= INT32_MAX &&
+           kv8_launch_fits(team_groups(blocks, from.pageSize), kThreads);
+}
+
 hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t budget, int32_t recent,
                      int32_t sinks, int32_t* kept, void* ws, int32_t* err, hipStream_t s)
 {
@@ -816,7 +842,6 @@ hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t bud
     const int32_t nPages = (budget + from.pageSize - 1) / from.pageSize;
     const int64_t rows = (int64_t)from.batch * from.heads;
     const int64_t blocks = rows * nPages * 2;
-    if (blocks > INT32_MAX || rows * (a.segments + 1) > INT32_MAX) return hipErrorInvalidValue;
     const int32_t teams = kSelThreads / kThreads * (from.pageSize >= 64 ? 1 : 64 / from.pageSize);
     if (a.segments == 0 && 2 * nPages <= teams) {
 #define KV8_SELECT_MOVE(F, D) (kv8_k_select_move<F, D><<<dim3((unsigned)rows), dim3(kSelThreads), 0, s>>>(a, nPages), 0)

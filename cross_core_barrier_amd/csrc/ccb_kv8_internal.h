@@ -14,6 +14,19 @@ namespace ccb {
 // or CCB_ERR_HIP); in ccb_api.hip, beside the cached device properties.
 ccbStatus device_ready();
 
+// A launch holds fewer than 2^32 threads and numbers its work in 31 bits; what
+// needs more is refused before anything is enqueued.
+inline bool kv8_launch_fits(int64_t groups, int64_t threads)
+{
+    return groups <= INT32_MAX && groups * threads <= UINT32_MAX;
+}
+bool kv8_append_fits(const ccbKv8Cache& c, int32_t nNew);
+bool kv8_read_fits(const ccbKv8Cache& c, int32_t count, int32_t sides);
+bool kv8_evict_fits(const ccbKv8Cache& from, int32_t budget);
+// (and whether the workspace is large enough)
+bool kv8_attend_fits(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery, int32_t window,
+                     int32_t accumulate, size_t wsBytes);
+
 struct Kv8AttendArgs {
     ccbKv8Cache c;
     ccbKv8Rows q, out;

@@ -19,7 +19,9 @@
  * nothing and reads no device memory on the host, so all of them can be
  * captured into a HIP graph (kernel nodes only).  The conventions of ccb.h
  * hold: a ccbStatus is returned, arguments are checked before anything is
- * enqueued, and calls act on the calling thread's current device.
+ * enqueued, and calls act on the calling thread's current device.  A call whose
+ * work does not fit a launch (of the order of 2^24 blocks of a page's head, or
+ * 2^23 runs of tokens with 16 rows) gets CCB_ERR_INVALID_VALUE.
  *
  * Errors found on the device.  `err` (device, one int32, may be NULL) gets
  * CCB_ERR_INVALID_VALUE stored when a call meets a page number outside 0 ..

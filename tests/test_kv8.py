@@ -456,3 +456,23 @@ def test_tensors_of_a_cache_change_in_place_only(cpu_cache):
     c.lens[0] = 7
     assert c.lens.tolist() == [7, 1, 1] and c.lens.data_ptr() == at
     assert c._c.lens == at
+
+
+def test_refuses_more_than_a_launch_holds(ccb):
+    """2^32 threads and more: refused with nothing enqueued, not by the launch
+    of one of a call's kernels after others."""
+    inv, big = ccb.CCB_ERR_INVALID_VALUE, (1 << 63) - 1
+    wide = dict(heads=64, batch=4096, maxPages=1 << 16, tableStride=1 << 16, weightStride=1 << 23, pageSize=128)
+    c, r = _cache(ccb, **wide), _rows(ccb)
+    out = _rows(ccb, data=13 << 20)
+    assert ccb.ccb_kv8_append(c, r, r, 1 << 15) == inv  # 2^18 pairs of a sequence and a head, 2^8 pages, 2 sides
+    assert ccb.ccb_kv8_read(c, out, out, 1 << 15) == inv
+    assert ccb.ccb_kv8_read(c, out, None, 1 << 15) == inv
+    to = _cache(ccb, **{**wide, "pageTable": 10 << 20, "lens": 11 << 20, "weight": 12 << 20})
+    assert ccb.ccb_kv8_evict(c, to, 1 << 15, 4, 4, None, 9 << 20, big) == inv
+    for acc in (0, 1):  # 2^11 rows: 2^7 tiles of them
+        assert ccb.ccb_kv8_attend(c, r, out, None, 64, 1 << 11, 0.1, 0, acc, 9 << 20, big) == inv
+    # so many pairs that their number passes 31 bits
+    far = _cache(ccb, **{**wide, "heads": 65536, "batch": 1 << 30})
+    assert ccb.ccb_kv8_append(far, r, r, 1) == inv and ccb.ccb_kv8_read(far, out, out, 1) == inv
+    assert ccb.ccb_kv8_attend(far, r, out, None, 65536, 1, 0.1, 0, 0, 9 << 20, big) == inv
