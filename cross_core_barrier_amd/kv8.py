@@ -13,8 +13,9 @@ only; every step runs in libccb.so's HIP kernels.
 Calls run on the cache's device, whichever is current: on torch's current
 stream there, or on `stream` (a torch.cuda.Stream or a raw hipStream_t of that
 device) after the work already queued on the current stream, which is then
-ordered after them.  They copy nothing to the host.  Bad page numbers,
-lengths and counts are met on the device: they set `cache.err`, which
+ordered after them.  They copy nothing to the host and compute no gradients:
+rows that ask for one are refused, but under torch.no_grad().  Bad page
+numbers, lengths and counts are met on the device: they set `cache.err`, which
 `cache.check()` reads (and waits for).
 """
 
@@ -37,6 +38,12 @@ _ROWS = {torch.bfloat16: ccb.CCB_KV8_BF16, torch.float16: ccb.CCB_KV8_FP16, torc
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
+
+
+def _no_gradient(what: str, *tensors) -> None:
+    for t in tensors:
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{what}: no gradient is computed here; detach it, or call under torch.no_grad()")
 
 
 class Kv8Cache:
@@ -165,6 +172,7 @@ class Kv8Cache:
         ones; lens counts them already.  k_new, v_new [batch, n, heads, head_dim]."""
         self._on_gpu()
         k, v = self._rows(k_new, self.heads, "k_new"), self._rows(v_new, self.heads, "v_new")
+        _no_gradient("k_new, v_new", k_new, v_new)
         n = k_new.shape[1]
         _need(n == v_new.shape[1] and k.type == v.type, "v_new: shape and dtype of k_new")
         self._ints(counts, (self.batch,), "counts")
@@ -187,6 +195,7 @@ class Kv8Cache:
         than 64 a cache head, or 16 in a large cache; refused)."""
         self._on_gpu()
         _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
+        _no_gradient("q", q)
         shape = q.shape
         queries, q_heads = shape[1], shape[2]
         s = self._enter(stream)

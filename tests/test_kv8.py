@@ -476,3 +476,24 @@ def test_refuses_more_than_a_launch_holds(ccb):
     far = _cache(ccb, **{**wide, "heads": 65536, "batch": 1 << 30})
     assert ccb.ccb_kv8_append(far, r, r, 1) == inv and ccb.ccb_kv8_read(far, out, out, 1) == inv
     assert ccb.ccb_kv8_attend(far, r, out, None, 65536, 1, 0.1, 0, 0, 9 << 20, big) == inv
+
+
+def test_refuses_tensors_that_ask_for_a_gradient(cpu_cache, monkeypatch):
+    """None is computed: the results would silently have no history."""
+    torch = pytest.importorskip("torch")
+    from cross_core_barrier_amd import kv8
+    make, _, reached = cpu_cache
+    monkeypatch.setattr(kv8, "_current_device", lambda: -1)
+    monkeypatch.setattr(kv8.Kv8Cache, "_on_gpu", lambda self: None)  # no kernel runs
+    c = make()
+    x, q = torch.zeros((3, 1, 2, 64)).half(), torch.zeros((3, 1, 4, 64)).half()
+    asks_x, asks_q = x.clone().requires_grad_(), q.clone().requires_grad_()
+    for call in (lambda: c.append(asks_x, x), lambda: c.append(x, asks_x), lambda: c.attend(asks_q)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    assert reached == []
+    with torch.no_grad():
+        c.append(asks_x, asks_x)
+        c.attend(asks_q)
+    c.append(asks_x.detach(), x)
+    assert reached == ["append", "attend", "append"]
