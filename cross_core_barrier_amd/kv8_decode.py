@@ -40,6 +40,8 @@ class Pages:
 class Session:
     def __init__(self, batch=4, heads=8, q_heads=32, head_dim=128, page_size=64, limit=2048, budget=512, fmt="e4m3",
                  dtype=torch.bfloat16, seed=0):
+        if not 1 <= budget < limit:  # a cut has to leave room for the next token
+            raise ValueError(f"budget {budget}: at least 1, and less than the limit of {limit} tokens")
         dev = torch.device("cuda")
         self.batch, self.heads, self.q_heads, self.head_dim = batch, heads, q_heads, head_dim
         self.limit, self.budget = limit, budget
@@ -86,6 +88,8 @@ class Session:
     def prefill(self, prompts: list) -> None:
         """Write prompts [tokens, d], one for each sequence."""
         lens = [p.shape[0] for p in prompts]
+        if len(lens) != self.batch or not all(1 <= n <= self.limit for n in lens):
+            raise ValueError(f"prompts: {self.batch} of 1 to {self.limit} tokens each")
         self._reserve(lens)
         rows = torch.nn.utils.rnn.pad_sequence(prompts, batch_first=True)
         counts = torch.tensor(lens, dtype=torch.int32, device="cuda")

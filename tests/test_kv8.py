@@ -497,3 +497,18 @@ def test_refuses_tensors_that_ask_for_a_gradient(cpu_cache, monkeypatch):
         c.attend(asks_q)
     c.append(asks_x.detach(), x)
     assert reached == ["append", "attend", "append"]
+
+
+def test_session_refuses_what_does_not_fit():
+    """A cut that leaves no room for the next token, and prompts that pass the
+    limit or hold nothing, before any page is taken."""
+    torch = pytest.importorskip("torch")
+    from cross_core_barrier_amd.kv8_decode import Session
+    for budget in (96, 97, 0, -1):
+        with pytest.raises(ValueError):
+            Session(batch=2, limit=96, budget=budget)
+    s = Session.__new__(Session)  # the checks need no device
+    s.batch, s.limit = 2, 96
+    for lens in ([97, 5], [5, 0], [5], [5, 5, 5]):
+        with pytest.raises(ValueError):
+            s.prefill([torch.zeros((n, 64)) for n in lens])
