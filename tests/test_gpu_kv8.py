@@ -859,3 +859,48 @@ def test_attend_in_place(kv8, queries, accumulate):
     got, got_lse = b.attend(mine, accumulate=accumulate, out=mine)
     assert got is mine and torch.equal(got, want) and torch.equal(got_lse, lse)
     assert torch.equal(a.weight, b.weight)
+
+
+@pytest.mark.parametrize("fmt,dtype,D,P,heads,group", [("int8", "bf16", 128, 64, 4, 4), ("e4m3", "fp16", 192, 128, 1, 3),
+                                                       ("int8", "fp16", 96, 32, 2, 5), ("e4m3", "bf16", 256, 16, 1, 8),
+                                                       ("int8", "bf16", 64, 128, 1, 16)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_attend_joins_many_runs(kv8, fmt, dtype, D, P, heads, group, accumulate):
+    """More runs of one sequence than a wave joins: a workgroup for each row."""
+    _say(f"attend 17011 tokens, {heads} heads {fmt} {dtype} D={D} P={P} accumulate={accumulate}")
+    _attend_case(kv8, 60, fmt, dtype, [17011], heads, group, D, P, accumulate=accumulate)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "bf16"), ("e4m3", "fp16"), ("int8", "fp16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("D,P,window", [(96, 16, 0), (192, 64, 77), (256, 128, 0)])
+def test_attend_weights_computed_again(kv8, fmt, dtype, D, P, window):
+    """More rows than scores are kept for, in every head size."""
+    _say(f"attend 70 rows {fmt} {dtype} D={D} P={P} window={window}")
+    _attend_case(kv8, 61, fmt, dtype, [300, 0, 13, 700], 2, 5, D, P, 14, window)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("P,budget", [(128, 128), (128, 129), (128, 256), (128, 257), (64, 128), (64, 129), (32, 128),
+                                      (32, 97), (16, 128), (16, 129), (16, 113)])
+def test_evict_in_one_kernel_and_in_two(kv8, fmt, P, budget):
+    """Budgets at the largest that the selection's own workgroup moves, and one more."""
+    _say(f"evict {fmt} P={P} budget={budget}")
+    _evict_case(kv8, P, fmt, [600, 128, 256, 257, 0, 129], budget, 11, 3, 2, P, 96, ties=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_read_one_side(kv8, side, dtype):
+    """Keys alone or values alone, through the C entry point."""
+    from cross_core_barrier_amd import ccb
+    rng = np.random.default_rng(62)
+    c = _host(rng, "e4m3", [0, 5, 64, 130], 3, 32, 96)
+    cache = _device(kv8, c)
+    kind = {"bf16": ccb.CCB_KV8_BF16, "fp16": ccb.CCB_KV8_FP16, "fp32": ccb.CCB_KV8_FP32}[dtype]
+    t = {**TYPES, "fp32": torch.float32}[dtype]
+    out = torch.full((4, 150, 3, 96), 7, dtype=t, device="cuda")
+    rows = ccb.ccbKv8Rows(out.data_ptr(), *out.stride()[:3], kind, 0)
+    _say(f"read {side} alone as {dtype}")
+    assert ccb.ccb_kv8_read(cache._c, rows if side == "k" else None, rows if side == "v" else None, 150) == 0
+    want = torch.from_numpy(oracle.read(c, 150, [0] * 4)["kv".index(side)].astype(np.float32)).to(t)
+    assert torch.equal(out.cpu(), want)
