@@ -40,10 +40,9 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _no_gradient(what: str, *tensors) -> None:
-    for t in tensors:
-        if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{what}: no gradient is computed here; detach it, or call under torch.no_grad()")
+def _no_gradient(what: str) -> None:
+    if torch.is_grad_enabled():
+        raise ValueError(f"{what}: no gradient is computed here; detach it, or call under torch.no_grad()")
 
 
 class Kv8Cache:
@@ -107,8 +106,9 @@ class Kv8Cache:
         return cls(k, v, ks, vs, table, lens, weight)
 
     def _on_gpu(self) -> None:
-        """Before anything else in every call: what follows compares devices
-        with the cache's only, and the kernels get raw addresses."""
+        """Refuses a cache on the CPU, before anything else in every call: what
+        follows compares devices with the cache's only, and the kernels get raw
+        addresses."""
         _need(self._index >= 0, "the cache's tensors are not on a GPU")
 
     def _rows(self, t: torch.Tensor, heads: int, what: str):
@@ -145,9 +145,7 @@ class Kv8Cache:
         return ws, ws.nbytes
 
     def _enter(self, stream):
-        """The caller's stream, ordered after torch's; None for torch's own."""
-        if stream is None:
-            return None
+        """The caller's stream, ordered after torch's."""
         _need(not isinstance(stream, torch.cuda.Stream) or stream.device_index == self._index,
               "stream: one of the cache's device")
         return _enter(stream, self.device)
@@ -170,18 +168,21 @@ class Kv8Cache:
                stream=None) -> None:
         """Write each sequence's counts[b] (None: all) new tokens as its last
         ones; lens counts them already.  k_new, v_new [batch, n, heads, head_dim]."""
-        self._on_gpu()
+        if self._index < 0:
+            self._on_gpu()
         k, v = self._rows(k_new, self.heads, "k_new"), self._rows(v_new, self.heads, "v_new")
-        _no_gradient("k_new, v_new", k_new, v_new)
+        if k_new.requires_grad or v_new.requires_grad:
+            _no_gradient("k_new, v_new")
         n = k_new.shape[1]
         _need(n == v_new.shape[1] and k.type == v.type, "v_new: shape and dtype of k_new")
         self._ints(counts, (self.batch,), "counts")
-        s = self._enter(stream)
+        s = None if stream is None else self._enter(stream)
         self._call(ccb.ccb_kv8_append, s, self._c, k, v, n, counts, self.err)
 
     def attend_workspace(self, q_heads: int, queries: int = 1, accumulate: bool = False) -> torch.Tensor:
         """A workspace for attend() calls of these sizes that follow each other."""
-        self._on_gpu()
+        if self._index < 0:
+            self._on_gpu()
         n = ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
         _need(n > 0, "attend: sizes that ccb_kv8_attend refuses")
         return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -193,12 +194,14 @@ class Kv8Cache:
         last tokens; scale None is 1 / sqrt(head_dim).  Returns (out, lse).
         out may be q itself, but for weights accumulated over many rows (more
         than 64 a cache head, or 16 in a large cache; refused)."""
-        self._on_gpu()
+        if self._index < 0:
+            self._on_gpu()
         _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
-        _no_gradient("q", q)
+        if q.requires_grad:
+            _no_gradient("q")
         shape = q.shape
         queries, q_heads = shape[1], shape[2]
-        s = self._enter(stream)
+        s = None if stream is None else self._enter(stream)
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=q.device)
             if s is not None:
@@ -220,7 +223,8 @@ class Kv8Cache:
 
     def evict_workspace(self, budget: int) -> torch.Tensor:
         """A workspace for evict() calls with this budget that follow each other."""
-        self._on_gpu()
+        if self._index < 0:
+            self._on_gpu()
         n = ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
         _need(n > 0, "evict: sizes that ccb_kv8_evict refuses")
         return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -231,10 +235,11 @@ class Kv8Cache:
         """Copy the budget tokens of each sequence and head with the largest
         weight (and its first `sinks` and last `recent`) into the cache `to`.
         kept [batch, heads, budget] int32 gets their numbers; it is returned."""
-        self._on_gpu()
+        if self._index < 0:
+            self._on_gpu()
         _need(to._index == self._index, "to: on the cache's device")
         self._ints(kept, (self.batch, self.heads, budget), "kept")
-        s = self._enter(stream)
+        s = None if stream is None else self._enter(stream)
         need = 0 if workspace is not None else ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
         ws, size = self._space(workspace, need, s)
         self._call(ccb.ccb_kv8_evict, s, self._c, to._c, budget, recent, sinks, kept, ws, size, self.err)
@@ -243,11 +248,12 @@ class Kv8Cache:
     def read(self, count: int, first: Optional[torch.Tensor] = None, dtype=torch.float32, stream=None):
         """The values of `count` tokens of each sequence from first[b] (None: 0)
         as (k, v) [batch, count, heads, head_dim]; zeros where there is none."""
-        self._on_gpu()
+        if self._index < 0:
+            self._on_gpu()
         kind = _ROWS.get(dtype)
         _need(kind is not None, "dtype: float32, bfloat16 or float16")
         self._ints(first, (self.batch,), "first")
-        s = self._enter(stream)
+        s = None if stream is None else self._enter(stream)
         both = torch.empty((2, self.batch, count, self.heads, self.head_dim), dtype=dtype, device=self.device)
         if s is not None:
             both.record_stream(s)
