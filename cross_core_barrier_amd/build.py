@@ -45,11 +45,11 @@ def hipcc_command(out: str, extra=()) -> list:
     ]
 
 
-def device_assembly(out: str) -> str:
-    """Write the gfx950 assembly of the kernels, compiled exactly as in the
-    library, to `out` (for reading the code the library runs)."""
+def device_assembly(out: str, source: str = "ccb_kernels.hip") -> str:
+    """Write the gfx950 assembly of a file's kernels, compiled exactly as in
+    the library, to `out` (for reading the code the library runs)."""
     cmd = ["hipcc", *CODE_FLAGS, "-S", "--cuda-device-only", "-o", out,
-           os.path.join(CSRC, "ccb_kernels.hip")]
+           os.path.join(CSRC, source)]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("hipcc -S failed:\n" + res.stdout + res.stderr)
