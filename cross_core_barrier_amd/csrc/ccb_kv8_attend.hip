@@ -980,18 +980,17 @@ int64_t weight_blocks(const Plan& p, int64_t pairs)
 template <int F, int T, int D>
 hipError_t launch(const Plan& p, int64_t blocks, hipStream_t s)
 {
-    const dim3 grid((unsigned)blocks), block(kThreads);
+    hipError_t e = hipSuccess;
     if (p.tilesN == 1)
-        kv8_k_attend<F, T, D, 1><<<grid, dim3(kRunThreads), 0, s>>>(p);
+        e = enqueue(kv8_k_attend<F, T, D, 1>, blocks, kRunThreads, s, p);
     else if constexpr (D <= 96)
-        kv8_k_attend<F, T, D, 2><<<grid, dim3(kRunThreads), 0, s>>>(p);
-    if (!p.direct)
-        kv8_k_join<T><<<dim3((unsigned)p.joinBlocks), block, 0, s>>>(p, D);
-    if (p.lse2 != nullptr) {
+        e = enqueue(kv8_k_attend<F, T, D, 2>, blocks, kRunThreads, s, p);
+    if (e == hipSuccess && !p.direct) e = enqueue(kv8_k_join<T>, p.joinBlocks, kThreads, s, p, D);
+    if (e == hipSuccess && p.lse2 != nullptr) {
         const int64_t each = weight_blocks(p, p.pairs);
-        kv8_k_weights<F, T, D><<<dim3((unsigned)(p.pairs * each)), block, 0, s>>>(p, (int32_t)each);
+        e = enqueue(kv8_k_weights<F, T, D>, p.pairs * each, kThreads, s, p, (int32_t)each);
     }
-    return hipGetLastError();
+    return e;
 }
 
 }  // namespace

@@ -753,15 +753,14 @@ hipError_t kv8_append(const ccbKv8Cache& c, const ccbKv8Rows& k, const ccbKv8Row
     const int32_t span = (nNew + c.pageSize - 2) / c.pageSize + 1;
     const int64_t blocks = touched_blocks(c, nNew, 2);
     const uint32_t units = (uint32_t)blocks;
-    const dim3 grid(team_groups(blocks, c.pageSize));
+    const int64_t groups = team_groups(blocks, c.pageSize);
 #define KV8_APPEND(F, T, D) \
-    (kv8_k_append<F, T, D><<<grid, dim3(kThreads), 0, s>>>(c, k, v, nNew, counts, span, units, err), 0)
+    enqueue(kv8_k_append<F, T, D>, groups, kThreads, s, c, k, v, nNew, counts, span, units, err)
 #define KV8_APPEND_DIM(D) \
     (c.format == CCB_KV8_INT8 \
          ? (k.type == CCB_KV8_BF16 ? KV8_APPEND(kInt8, CCB_KV8_BF16, D) : KV8_APPEND(kInt8, CCB_KV8_FP16, D)) \
          : (k.type == CCB_KV8_BF16 ? KV8_APPEND(kE4m3, CCB_KV8_BF16, D) : KV8_APPEND(kE4m3, CCB_KV8_FP16, D)))
-    (void)KV8_BY_DIM(c.headDim, KV8_APPEND_DIM);
-    return hipGetLastError();
+    return KV8_BY_DIM(c.headDim, KV8_APPEND_DIM);
 }
 
 hipError_t kv8_read(const ccbKv8Cache& c, const ccbKv8Rows* k, const ccbKv8Rows* v, int32_t count,
@@ -773,16 +772,15 @@ hipError_t kv8_read(const ccbKv8Cache& c, const ccbKv8Rows* k, const ccbKv8Rows*
     const int64_t blocks = touched_blocks(c, count, sides == 3 ? 2 : 1);
     const ccbKv8Rows kr = k != nullptr ? *k : *v, vr = v != nullptr ? *v : *k;
     const uint32_t units = (uint32_t)blocks;
-    const dim3 grid(team_groups(blocks, c.pageSize));
+    const int64_t groups = team_groups(blocks, c.pageSize);
 #define KV8_READ(F, T, D) \
-    (kv8_k_read<F, T, D><<<grid, dim3(kThreads), 0, s>>>(c, kr, vr, count, first, span, sides, units, err), 0)
+    enqueue(kv8_k_read<F, T, D>, groups, kThreads, s, c, kr, vr, count, first, span, sides, units, err)
 #define KV8_READ_T(F, D) \
     (kr.type == CCB_KV8_BF16   ? KV8_READ(F, CCB_KV8_BF16, D) \
      : kr.type == CCB_KV8_FP16 ? KV8_READ(F, CCB_KV8_FP16, D) \
                                : KV8_READ(F, CCB_KV8_FP32, D))
 #define KV8_READ_DIM(D) (c.format == CCB_KV8_INT8 ? KV8_READ_T(kInt8, D) : KV8_READ_T(kE4m3, D))
-    (void)KV8_BY_DIM(c.headDim, KV8_READ_DIM);
-    return hipGetLastError();
+    return KV8_BY_DIM(c.headDim, KV8_READ_DIM);
 }
 
 // Segments of a row, 0 where one workgroup chooses by itself, and the
@@ -844,30 +842,24 @@ hipError_t kv8_evict(const ccbKv8Cache& from, const ccbKv8Cache& to, int32_t bud
     const int64_t blocks = rows * nPages * 2;
     const int32_t teams = kSelThreads / kThreads * (from.pageSize >= 64 ? 1 : 64 / from.pageSize);
     if (a.segments == 0 && 2 * nPages <= teams) {
-#define KV8_SELECT_MOVE(F, D) (kv8_k_select_move<F, D><<<dim3((unsigned)rows), dim3(kSelThreads), 0, s>>>(a, nPages), 0)
+#define KV8_SELECT_MOVE(F, D) enqueue(kv8_k_select_move<F, D>, rows, kSelThreads, s, a, nPages)
 #define KV8_SELECT_MOVE_DIM(D) \
     (from.format == CCB_KV8_INT8 ? KV8_SELECT_MOVE(kInt8, D) : KV8_SELECT_MOVE(kE4m3, D))
-        (void)KV8_BY_DIM(from.headDim, KV8_SELECT_MOVE_DIM);
-        return hipGetLastError();
+        return KV8_BY_DIM(from.headDim, KV8_SELECT_MOVE_DIM);
     }
+    hipError_t e = hipSuccess;
     if (a.segments == 0) {
-        kv8_k_select_short<<<dim3((unsigned)rows), dim3(kSelThreads), 0, s>>>(a);
+        e = enqueue(kv8_k_select_short, rows, kSelThreads, s, a);
     } else {
-        const dim3 segments((unsigned)(rows * a.segments));
-        kv8_k_select_long<0><<<segments, dim3(kSelThreads), 0, s>>>(a);
-        kv8_k_select_long<1><<<segments, dim3(kSelThreads), 0, s>>>(a);
-        kv8_k_select_long<2><<<segments, dim3(kSelThreads), 0, s>>>(a);
-        kv8_k_select_long<3><<<segments, dim3(kSelThreads), 0, s>>>(a);
+        for (auto stage : {kv8_k_select_long<0>, kv8_k_select_long<1>, kv8_k_select_long<2>, kv8_k_select_long<3>})
+            if (e == hipSuccess) e = enqueue(stage, rows * a.segments, kSelThreads, s, a);
     }
-    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const uint32_t units = (uint32_t)blocks;
-    const dim3 grid(team_groups(blocks, from.pageSize));
-#define KV8_MOVE(F, D) \
-    (kv8_k_move<F, D><<<grid, dim3(kThreads), 0, s>>>(from, to, budget, units, index, err), 0)
+    const int64_t groups = team_groups(blocks, from.pageSize);
+#define KV8_MOVE(F, D) enqueue(kv8_k_move<F, D>, groups, kThreads, s, from, to, budget, units, index, err)
 #define KV8_MOVE_DIM(D) (from.format == CCB_KV8_INT8 ? KV8_MOVE(kInt8, D) : KV8_MOVE(kE4m3, D))
-    (void)KV8_BY_DIM(from.headDim, KV8_MOVE_DIM);
-    return hipGetLastError();
+    return KV8_BY_DIM(from.headDim, KV8_MOVE_DIM);
 }
 
 }  // namespace ccb

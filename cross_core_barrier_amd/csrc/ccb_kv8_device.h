@@ -155,6 +155,19 @@ struct Team {
     }
 };
 
+// Enqueues a kernel and returns that launch's own status: the runtime's last
+// error may be of a call of the caller's that failed before.
+template <class T>
+struct Plain {
+    using type = T;
+};
+template <class... P>
+hipError_t enqueue(void (*kernel)(P...), int64_t groups, int threads, hipStream_t s, typename Plain<P>::type... p)
+{
+    void* args[] = {(void*)&p...};
+    return hipLaunchKernel((const void*)kernel, dim3((unsigned)groups), dim3((unsigned)threads), args, 0, s);
+}
+
 inline unsigned team_groups(int64_t units, int32_t pageSize)
 {
     const int32_t teams = pageSize >= 64 ? 1 : 64 / pageSize;

@@ -904,3 +904,40 @@ def test_read_one_side(kv8, side, dtype):
     assert ccb.ccb_kv8_read(cache._c, rows if side == "k" else None, rows if side == "v" else None, 150) == 0
     want = torch.from_numpy(oracle.read(c, 150, [0] * 4)["kv".index(side)].astype(np.float32)).to(t)
     assert torch.equal(out.cpu(), want)
+
+
+def test_an_error_left_by_another_call_is_not_reported(kv8):
+    """A HIP call that failed before, in the caller's own code, says nothing
+    of the cache's calls: they run and return OK, and leave that error be."""
+    import ctypes
+    from cross_core_barrier_amd import ccb
+    with open("/proc/self/maps") as f:  # the runtime that is loaded
+        hip = ctypes.CDLL(next(line.split()[-1] for line in f if "libamdhip64" in line))
+    rng = np.random.default_rng(63)
+    c = _host(rng, "int8", [60, 5], 2, 16, 64)
+    c["weight"] = np.zeros((2, 2, c["table"].shape[1] * 16), np.float32)
+    cache = _device(kv8, c)
+    x = torch.from_numpy(rng.normal(0, 1, (2, 1, 2, 64))).half().cuda()
+    q = torch.from_numpy(rng.normal(0, 1, (2, 1, 4, 64))).half().cuda()
+    out, lse, ws = torch.empty_like(q), torch.empty((2, 1, 4), device="cuda"), cache.attend_workspace(4, 1, True)
+    to = kv8.Kv8Cache.allocate(4, 2, 16, 64, 2, 2, "int8", weights=True)
+    to.page_table.copy_(torch.arange(4, dtype=torch.int32).view(2, 2))
+    kept, ews = torch.zeros((2, 2, 20), dtype=torch.int32, device="cuda"), cache.evict_workspace(20)
+    dense = torch.empty((2, 20, 2, 64), device="cuda")
+    rows = ccb.ccbKv8Rows(dense.data_ptr(), *dense.stride()[:3], ccb.CCB_KV8_FP32, 0)
+    calls = {"append": lambda: cache.append(x, x),
+             "attend": lambda: cache.attend(q, accumulate=True, out=out, lse=lse, workspace=ws),
+             "evict": lambda: cache.evict(to, 20, 4, 2, kept=kept, workspace=ews),
+             "read": lambda: ccb.check(ccb.ccb_kv8_read(cache._c, rows, None, 20))}
+    torch.cuda.synchronize()
+    for name, call in calls.items():
+        _say(f"{name} behind another call's error")
+        hip.hipGetLastError()
+        assert hip.hipSetDevice(1 << 20) != 0  # refused by the host: no such device
+        try:
+            call()
+        finally:
+            left = hip.hipGetLastError()
+        assert left != 0, name
+    torch.cuda.synchronize()
+    cache.check()
