@@ -37,10 +37,19 @@
 #include "ccb_kv8_internal.h"
 #include "ccb_kv8_device.h"
 
-// Scores are kept for the weights where that moves less than reading the
-// keys again (8 bytes a row and token against headDim a token), and for up
-// to 64 rows where all of them stay in the caches: there a launch less
-// counts for more.
+// Scores are kept for the weights of up to 16 rows: writing and reading them (8
+// bytes a row and token) costs less than a kernel more that reads, converts and
+// multiplies every key again.  In us, kept and again, 8 cache heads:
+//                               rows    D = 64      D = 128     D = 256
+//   16 sequences of 4096 tokens    4    23   39     33   61     65  109
+//                                 16    29   39     46   66     78  119
+//   64 of 8192 (D = 256: 32)       4   154  239    270  437    243  406
+//                                 16   263  242    373  448    287  431
+// Only D = 64 with 16 rows in a cache of 2^19 tokens goes the other way.  17 to
+// 64 rows keep theirs where all of them stay in the caches (8 sequences of 500 tokens, D = 128, 32 rows: 14.6 and 19.5).
+// Beyond that it depends on the head size (64 rows of 16 x 4096: 79 and 70 at
+// D = 64, 176 and 220 at 256), and the scores would take more memory than the
+// gain is worth (64 x 8192, 64 rows: 1.1 GB).
 bool ccb::kv8_attend_keeps_scores(const ccbKv8Cache& c, int32_t headsQ, int32_t nQuery)
 {
     const int64_t pairs = (int64_t)c.batch * c.heads, rows = (int64_t)nQuery * (headsQ / c.heads);

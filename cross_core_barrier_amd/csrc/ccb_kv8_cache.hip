@@ -31,7 +31,7 @@ typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 // gives the block's scale, then the new values are rounded and, where the
 // scale grew, the block's older codes are rounded again.  Blocks are
 // independent, so there is nothing to join.  Bound by the bytes of the new
-// values and codes (8 prompts of 8192 tokens: 402 MB in 79 to 105 us); one-token
+// values and codes (8 prompts of 8192 tokens: 402 MB in 75 to 87 us); one-token
 // steps by latency (5 us).
 // ---------------------------------------------------------------------------
 template <int F, int T, int D>
@@ -139,7 +139,8 @@ __global__ __launch_bounds__(kThreads) void kv8_k_append(ccbKv8Cache c, ccbKv8Ro
 // One team per page, head and side, so that page and scale are looked up
 // once; a thread's 4 codes become one store of 16 (8) bytes beside its
 // neighbours'.  Bound by the bytes written, which pass the caches by: 541 MB of
-// floats in 105 us (6.4 TB/s with the codes read), 115 through them.
+// floats in 105 us (6.4 TB/s with the codes read), 115 through them; 270 MB of
+// 16-bit values in 60 us (6.8 TB/s).
 // ---------------------------------------------------------------------------
 template <int F, int T, int D>
 __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows kOut,
@@ -218,8 +219,10 @@ __global__ __launch_bounds__(kThreads) void kv8_k_read(ccbKv8Cache c, ccbKv8Rows
 //
 // One team per new page, head and side: looks its tokens' places up once,
 // gathers their codes into registers, finds the new scale, rounds the codes
-// again and writes them.  Half bound by instructions (about 20 a code, 8 of
-// them for rounding), half by the chain token -> page -> codes: 66 MB in 27 us.
+// again and writes them.  Bound by instructions first: about 20 a code, 8 of
+// them for rounding, fill the vector units for 2/3 of the time (16 x 1024 tokens of 8 heads, 66 MB in 26 us);
+// of the waves' time 38% waits for their turn and 38% for memory, the chain
+// token -> page -> codes.
 // ---------------------------------------------------------------------------
 struct MoveLds {
     int64_t place[128];  // where a token's codes start

@@ -8,7 +8,7 @@ only; every step runs in libccb.so's HIP kernels.
     cache.lens += 1                            # one token more for every sequence
     cache.append(k_new, v_new)                 # [batch, 1, heads, head_dim]
     out, lse = cache.attend(q, accumulate=True)  # q [batch, 1, q_heads, head_dim]
-    kept = cache.evict(smaller, budget=1024, recent=128, sinks=4)
+    cache.evict(smaller, budget=1024, recent=128, sinks=4, kept=kept)  # kept: which tokens, or None
 
 Calls run on the cache's device, whichever is current: on torch's current
 stream there, or on `stream` (a torch.cuda.Stream or a raw hipStream_t of that
@@ -180,7 +180,9 @@ class Kv8Cache:
         self._call(ccb.ccb_kv8_append, s, self._c, k, v, n, counts, self.err)
 
     def attend_workspace(self, q_heads: int, queries: int = 1, accumulate: bool = False) -> torch.Tensor:
-        """A workspace for attend() calls of these sizes that follow each other."""
+        """A workspace for attend() calls of these sizes that follow each other.
+        With weights it grows with the capacity: 4 bytes for each of the rows
+        of a cache head and each token there is room for."""
         if self._index < 0:
             self._on_gpu()
         n = ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
@@ -234,7 +236,9 @@ class Kv8Cache:
               stream=None) -> Optional[torch.Tensor]:
         """Copy the budget tokens of each sequence and head with the largest
         weight (and its first `sinks` and last `recent`) into the cache `to`.
-        kept [batch, heads, budget] int32 gets their numbers; it is returned."""
+        kept [batch, heads, budget] int32, where given, gets their numbers; it
+        is returned.  Bad pages of either cache are reported by this one's
+        check()."""
         if self._index < 0:
             self._on_gpu()
         _need(to._index == self._index, "to: on the cache's device")

@@ -29,7 +29,8 @@
  * 0 .. min(nNew, lens[b]); it is never cleared.  Nothing is read or written
  * out of range then: a sequence with a bad length or count counts as empty
  * (for ccb_kv8_append: is left alone), the tokens of a bad page count as
- * unseen (attention), as zeros (read, evict) or are dropped (append).
+ * unseen (attention), as zeros (read, evict) or are dropped (append).  A bad
+ * page of evict's `to` is left out, and `lens` counts its tokens all the same.
  *
  * Contents past lens[b], and pages that no sequence uses, may hold any bytes
  * (NaN codes and NaN scales among them) and reach no result.  Within a
@@ -135,7 +136,11 @@ CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
                                  size_t wsBytes, int32_t* err, ccbStream stream);
 
 /* Bytes of ccb_kv8_attend's workspace, whatever the window (0 for arguments it
- * refuses). */
+ * refuses).  It goes by the capacity, not by the lengths: with R as above,
+ * headDim + 2 floats for R rows of each run of tokens, of which there are at most
+ * max(4096, batch * heads), and with accumulate 4 * batch * heads * R * maxPages *
+ * pageSize bytes for R <= 16 (and R <= 64 while that is at most 2^25): 1.1 GB for
+ * 64 sequences of 131072 tokens with 8 heads and 4 rows each. */
 CCB_API size_t ccb_kv8_attend_workspace_bytes(const ccbKv8Cache* cache, int32_t headsQ,
                                               int32_t nQuery, int32_t accumulate);
 
