@@ -95,6 +95,25 @@ class ccbKv8Rows(ctypes.Structure):
                 ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+CCB_PAGES_MAX_BATCH = 8192
+
+
+class ccbPagePool(ctypes.Structure):
+    _fields_ = [("free", ctypes.c_void_p), ("count", ctypes.c_void_p), ("state", ctypes.c_void_p),
+                ("numPages", ctypes.c_int32), ("pageSize", ctypes.c_int32)]
+
+
+class ccbPageTable(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("batch", ctypes.c_int32), ("maxPages", ctypes.c_int32)]
+
+
+class ccbSlotMaps(ctypes.Structure):
+    _fields_ = [("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("sequences", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("granted", ctypes.c_void_p), ("tokens", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class ccbCntRecordInfo(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("value", ctypes.c_uint32)]
 
@@ -118,6 +137,8 @@ def check(status: int, what: str = "ccb call") -> None:
 _V = ctypes.c_void_p
 _SZ, _F32 = ctypes.c_size_t, ctypes.c_float
 _KC, _KR = ctypes.POINTER(ccbKv8Cache), ctypes.POINTER(ccbKv8Rows)
+_PP = ctypes.POINTER(ccbPagePool)
+_PT, _SM = ctypes.POINTER(ccbPageTable), ctypes.POINTER(ccbSlotMaps)
 _I32, _U32, _I64, _U64 = ctypes.c_int32, ctypes.c_uint32, ctypes.c_int64, ctypes.c_uint64
 
 
@@ -178,6 +199,8 @@ _f = {
     "ccb_kv8_evict": _sig("ccb_kv8_evict", _I32, _KC, _KC, _I32, _I32, _I32, _V, _V, _SZ, _V, _V),
     "ccb_kv8_evict_workspace_bytes": _sig("ccb_kv8_evict_workspace_bytes", _SZ, _KC, _I32),
     "ccb_kv8_read": _sig("ccb_kv8_read", _I32, _KC, _KR, _KR, _I32, _V, _V, _V),
+    "ccb_pages_trim": _sig("ccb_pages_trim", _I32, _PP, _PT, _V, _V, _V),
+    "ccb_pages_grow": _sig("ccb_pages_grow", _I32, _PP, _PT, _V, _SM, _V, _V),
 }
 
 EXPORTED = sorted(_f)
@@ -405,3 +428,14 @@ def ccb_kv8_evict_workspace_bytes(src, budget: int) -> int:
 
 def ccb_kv8_read(cache, k_out, v_out, count, first=None, err=None, stream=None) -> int:
     return _f["ccb_kv8_read"](cache, k_out, v_out, count, _p(first), _p(err), _s(stream))
+
+
+# --- pages of a paged cache -------------------------------------------------------------
+# pool, table and maps arguments are ccbPagePool, ccbPageTable and ccbSlotMaps structures
+
+def ccb_pages_trim(pool, table, keep, err=None, stream=None) -> int:
+    return _f["ccb_pages_trim"](pool, table, _p(keep), _p(err), _s(stream))
+
+
+def ccb_pages_grow(pool, table, counts, maps, err=None, stream=None) -> int:
+    return _f["ccb_pages_grow"](pool, table, _p(counts), maps, _p(err), _s(stream))

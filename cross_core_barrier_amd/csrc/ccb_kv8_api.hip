@@ -10,7 +10,7 @@
 
 namespace {
 
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using ccb::aligned;
 
 constexpr size_t kLeastWorkspace = 128;
 constexpr int64_t kMaxTokens = 1 << 30;  // of one sequence
@@ -53,13 +53,6 @@ ccbStatus check_rows(const ccbKv8Rows* r, bool allow32)
     return CCB_OK;
 }
 
-ccbStatus done(hipError_t e)
-{
-    if (e == hipSuccess) return CCB_OK;
-    (void)hipGetLastError();  // reported through the status only
-    return e == hipErrorInvalidValue ? CCB_ERR_INVALID_VALUE : CCB_ERR_HIP;
-}
-
 bool attend_sizes_ok(const ccbKv8Cache* c, int32_t headsQ, int32_t nQuery)
 {
     return headsQ >= 1 && headsQ % c->heads == 0 && nQuery >= 0 &&
@@ -83,7 +76,7 @@ CCB_API ccbStatus ccb_kv8_append(const ccbKv8Cache* cache, const ccbKv8Rows* kNe
     if ((st = check_rows(vNew, false)) != CCB_OK) return st;
     if (kNew->type != vNew->type || !ccb::kv8_append_fits(*cache, nNew)) return CCB_ERR_INVALID_VALUE;
     if ((st = ccb::device_ready()) != CCB_OK) return st;
-    return done(ccb::kv8_append(*cache, *kNew, *vNew, nNew, counts, err, (hipStream_t)stream));
+    return ccb::launch_status(ccb::kv8_append(*cache, *kNew, *vNew, nNew, counts, err, (hipStream_t)stream));
 }
 
 CCB_API size_t ccb_kv8_attend_workspace_bytes(const ccbKv8Cache* cache, int32_t headsQ,
@@ -134,7 +127,7 @@ CCB_API ccbStatus ccb_kv8_attend(const ccbKv8Cache* cache, const ccbKv8Rows* q,
     a.scale = scale;
     a.ws = ws;
     a.err = err;
-    return done(ccb::kv8_attend(a, (hipStream_t)stream));
+    return ccb::launch_status(ccb::kv8_attend(a, (hipStream_t)stream));
 }
 
 CCB_API size_t ccb_kv8_evict_workspace_bytes(const ccbKv8Cache* from, int32_t budget)
@@ -165,7 +158,7 @@ CCB_API ccbStatus ccb_kv8_evict(const ccbKv8Cache* from, const ccbKv8Cache* to, 
     if (wsBytes < ccb_kv8_evict_workspace_bytes(from, budget) || !ccb::kv8_evict_fits(*from, budget))
         return CCB_ERR_INVALID_VALUE;
     if ((st = ccb::device_ready()) != CCB_OK) return st;
-    return done(ccb::kv8_evict(*from, *to, budget, recent, sinks, kept, ws, err, (hipStream_t)stream));
+    return ccb::launch_status(ccb::kv8_evict(*from, *to, budget, recent, sinks, kept, ws, err, (hipStream_t)stream));
 }
 
 CCB_API ccbStatus ccb_kv8_read(const ccbKv8Cache* cache, const ccbKv8Rows* kOut,
@@ -183,7 +176,7 @@ CCB_API ccbStatus ccb_kv8_read(const ccbKv8Cache* cache, const ccbKv8Rows* kOut,
     if (kOut != nullptr && vOut != nullptr && kOut->type != vOut->type) return CCB_ERR_INVALID_VALUE;
     if (!ccb::kv8_read_fits(*cache, count, kOut != nullptr && vOut != nullptr ? 2 : 1)) return CCB_ERR_INVALID_VALUE;
     if ((st = ccb::device_ready()) != CCB_OK) return st;
-    return done(ccb::kv8_read(*cache, kOut, vOut, count, first, err, (hipStream_t)stream));
+    return ccb::launch_status(ccb::kv8_read(*cache, kOut, vOut, count, first, err, (hipStream_t)stream));
 }
 
 }  // extern "C"

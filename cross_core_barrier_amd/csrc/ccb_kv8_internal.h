@@ -14,6 +14,16 @@ namespace ccb {
 // or CCB_ERR_HIP); in ccb_api.hip, beside the cached device properties.
 ccbStatus device_ready();
 
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// A launch's own error as a status; nothing of it stays behind.
+inline ccbStatus launch_status(hipError_t e)
+{
+    if (e == hipSuccess) return CCB_OK;
+    (void)hipGetLastError();  // reported through the status only
+    return e == hipErrorInvalidValue ? CCB_ERR_INVALID_VALUE : CCB_ERR_HIP;
+}
+
 // A launch holds fewer than 2^32 threads and numbers its work in 31 bits; what
 // needs more is refused before anything is enqueued.
 inline bool kv8_launch_fits(int64_t groups, int64_t threads)

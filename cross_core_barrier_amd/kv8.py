@@ -45,71 +45,26 @@ def _no_gradient(what: str) -> None:
         raise ValueError(f"{what}: no gradient is computed here; detach it, or call under torch.no_grad()")
 
 
-class Kv8Cache:
-    """A cache in the caller's tensors (they are kept, not copied, and stay
-    the same tensors with the same storage for the cache's life):
-    k, v [pages, heads, page_size, head_dim] (int8 or float8_e4m3fn); k_scale,
-    v_scale [pages, heads] float32; page_table [batch, max_pages] int32; lens
-    [batch] int32; weight [batch, heads, at least max_pages * page_size]
-    float32 or None.  All contiguous, but for the page table's rows, and on one
-    GPU: a cache on the CPU can be made, but every call on it is refused."""
+class OnDevice:
+    """What the classes around the paged caches' calls share: tensors of one
+    GPU whose addresses the kernels get (device, _index, err; a cache's batch
+    and head_dim too), and calls that run there."""
 
-    def __init__(self, k, v, k_scale, v_scale, page_table, lens, weight=None):
-        _need(k.dim() == 4 and k.dtype in _CODES, "k: [pages, heads, page_size, head_dim], int8 or float8_e4m3fn")
-        pages, heads, page_size, head_dim = k.shape
-        _need(v.shape == k.shape and v.dtype == k.dtype, "v: shape and dtype of k")
-        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-            _need(tuple(s.shape) == (pages, heads) and s.dtype == torch.float32, f"{name}: [pages, heads] float32")
-        _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and page_table.shape[1] >= 1 and
-              page_table.stride(1) == 1, "page_table: [batch, max_pages] int32")
-        batch, max_pages = page_table.shape
-        _need(tuple(lens.shape) == (batch,) and lens.dtype == torch.int32, "lens: [batch] int32")
-        if weight is not None:
-            _need(weight.dim() == 3 and tuple(weight.shape[:2]) == (batch, heads) and weight.dtype == torch.float32
-                  and weight.shape[2] >= max_pages * page_size,
-                  "weight: [batch, heads, max_pages * page_size or more] float32")
-        for t in (k, v, k_scale, v_scale, lens) + (() if weight is None else (weight,)):
-            _need(t.is_contiguous(), "cache tensors are contiguous")
-        for t in (v, k_scale, v_scale, page_table, lens) + (() if weight is None else (weight,)):
-            _need(t.device == k.device, "cache tensors share a device")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.page_table, self.lens, self.weight = page_table, lens, weight
-        self.heads, self.head_dim, self.batch, self.device = heads, head_dim, batch, k.device
-        self._index = k.get_device()  # -1 on the CPU
-        self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self._c = ccb.ccbKv8Cache(
-            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
-            lens.data_ptr(), 0 if weight is None else weight.data_ptr(),
-            page_table.stride(0) if batch > 1 else max_pages, 0 if weight is None else weight.shape[2],
-            _CODES[k.dtype], pages, heads, page_size, head_dim, batch, max_pages, 0)
+    _what = "paged cache"
 
     def __setattr__(self, name: str, value) -> None:
         """The kernels get the addresses that the constructor saw: a tensor's
         contents may change (cache.lens += 1, cache.lens[...] = ...), the
         tensor may not."""
         if self.__dict__.get(name, value) is not value:
-            raise AttributeError(f"{name}: change the tensor in place, or make another Kv8Cache")
+            raise AttributeError(f"{name}: change the tensor in place, or make another {type(self).__name__}")
         object.__setattr__(self, name, value)
 
-    @classmethod
-    def allocate(cls, pages: int, heads: int, page_size: int, head_dim: int, batch: int, max_pages: int,
-                 fmt: str = "e4m3", weights: bool = False, device="cuda") -> "Kv8Cache":
-        """Zeroed tensors: no sequence holds a token, every page number is 0."""
-        _need(fmt in _FORMATS, "fmt: int8 or e4m3")
-        shape = (pages, heads, page_size, head_dim)
-        k, v = (torch.zeros(shape, dtype=torch.int8, device=device).view(_FORMATS[fmt]) for _ in range(2))
-        ks, vs = (torch.zeros((pages, heads), dtype=torch.float32, device=device) for _ in range(2))
-        table = torch.zeros((batch, max_pages), dtype=torch.int32, device=device)
-        lens = torch.zeros(batch, dtype=torch.int32, device=device)
-        weight = torch.zeros((batch, heads, max_pages * page_size), dtype=torch.float32, device=device) \
-            if weights else None
-        return cls(k, v, ks, vs, table, lens, weight)
-
     def _on_gpu(self) -> None:
-        """Refuses a cache on the CPU, before anything else in every call: what
-        follows compares devices with the cache's only, and the kernels get raw
-        addresses."""
-        _need(self._index >= 0, "the cache's tensors are not on a GPU")
+        """Refuses tensors on the CPU, before anything else in every call: what
+        follows compares devices with these tensors' only, and the kernels get
+        raw addresses."""
+        _need(self._index >= 0, f"the {self._what}'s tensors are not on a GPU")
 
     def _rows(self, t: torch.Tensor, heads: int, what: str):
         kind = _ROWS.get(t.dtype)
@@ -141,17 +96,17 @@ class Kv8Cache:
             if s is not None:
                 s.wait_stream(torch.cuda.current_stream(self.device))
                 ws.record_stream(s)
-        _need(ws.is_contiguous() and ws.get_device() == self._index, "workspace: contiguous, on the cache's device")
+        _need(ws.is_contiguous() and ws.get_device() == self._index, f"workspace: contiguous, on the {self._what}'s device")
         return ws, ws.nbytes
 
     def _enter(self, stream):
         """The caller's stream, ordered after torch's."""
         _need(not isinstance(stream, torch.cuda.Stream) or stream.device_index == self._index,
-              "stream: one of the cache's device")
+              f"stream: one of the {self._what}'s device")
         return _enter(stream, self.device)
 
     def _call(self, fn, s, *args) -> None:
-        """An entry point with the cache's device current, on `s` or torch's
+        """An entry point with the tensors' device current, on `s` or torch's
         stream there; raises its error and orders torch's stream after `s`."""
         stream = s or _current_stream(self._index)
         if _current_device() == self._index:
@@ -163,6 +118,68 @@ class Kv8Cache:
             raise ccb.CcbError(status, fn.__name__)
         if s is not None:
             _leave(s, self.device)
+
+    def check(self) -> None:
+        """Raise if one of this object's calls met bad numbers (pages, lengths,
+        counts) since the last check.  Waits for the device."""
+        status = int(self.err.item())
+        self.err.zero_()
+        ccb.check(status, self._what)
+
+
+class Kv8Cache(OnDevice):
+    """A cache in the caller's tensors (they are kept, not copied, and stay
+    the same tensors with the same storage for the cache's life):
+    k, v [pages, heads, page_size, head_dim] (int8 or float8_e4m3fn); k_scale,
+    v_scale [pages, heads] float32; page_table [batch, max_pages] int32; lens
+    [batch] int32; weight [batch, heads, at least max_pages * page_size]
+    float32 or None.  All contiguous, but for the page table's rows, and on one
+    GPU: a cache on the CPU can be made, but every call on it is refused."""
+
+    _what = "8-bit cache"
+
+    def __init__(self, k, v, k_scale, v_scale, page_table, lens, weight=None):
+        _need(k.dim() == 4 and k.dtype in _CODES, "k: [pages, heads, page_size, head_dim], int8 or float8_e4m3fn")
+        pages, heads, page_size, head_dim = k.shape
+        _need(v.shape == k.shape and v.dtype == k.dtype, "v: shape and dtype of k")
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _need(tuple(s.shape) == (pages, heads) and s.dtype == torch.float32, f"{name}: [pages, heads] float32")
+        _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and page_table.shape[1] >= 1 and
+              page_table.stride(1) == 1, "page_table: [batch, max_pages] int32")
+        batch, max_pages = page_table.shape
+        _need(tuple(lens.shape) == (batch,) and lens.dtype == torch.int32, "lens: [batch] int32")
+        if weight is not None:
+            _need(weight.dim() == 3 and tuple(weight.shape[:2]) == (batch, heads) and weight.dtype == torch.float32
+                  and weight.shape[2] >= max_pages * page_size,
+                  "weight: [batch, heads, max_pages * page_size or more] float32")
+        for t in (k, v, k_scale, v_scale, lens) + (() if weight is None else (weight,)):
+            _need(t.is_contiguous(), "cache tensors are contiguous")
+        for t in (v, k_scale, v_scale, page_table, lens) + (() if weight is None else (weight,)):
+            _need(t.device == k.device, "cache tensors share a device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table, self.lens, self.weight = page_table, lens, weight
+        self.heads, self.head_dim, self.batch, self.device = heads, head_dim, batch, k.device
+        self._index = k.get_device()  # -1 on the CPU
+        self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._c = ccb.ccbKv8Cache(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+            lens.data_ptr(), 0 if weight is None else weight.data_ptr(),
+            page_table.stride(0) if batch > 1 else max_pages, 0 if weight is None else weight.shape[2],
+            _CODES[k.dtype], pages, heads, page_size, head_dim, batch, max_pages, 0)
+
+    @classmethod
+    def allocate(cls, pages: int, heads: int, page_size: int, head_dim: int, batch: int, max_pages: int,
+                 fmt: str = "e4m3", weights: bool = False, device="cuda") -> "Kv8Cache":
+        """Zeroed tensors: no sequence holds a token, every page number is 0."""
+        _need(fmt in _FORMATS, "fmt: int8 or e4m3")
+        shape = (pages, heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.int8, device=device).view(_FORMATS[fmt]) for _ in range(2))
+        ks, vs = (torch.zeros((pages, heads), dtype=torch.float32, device=device) for _ in range(2))
+        table = torch.zeros((batch, max_pages), dtype=torch.int32, device=device)
+        lens = torch.zeros(batch, dtype=torch.int32, device=device)
+        weight = torch.zeros((batch, heads, max_pages * page_size), dtype=torch.float32, device=device) \
+            if weights else None
+        return cls(k, v, ks, vs, table, lens, weight)
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts: Optional[torch.Tensor] = None,
                stream=None) -> None:
@@ -266,10 +283,3 @@ class Kv8Cache:
         self._call(ccb.ccb_kv8_read, s, self._c, ccb.ccbKv8Rows(k.data_ptr(), count * row, row, self.head_dim, kind, 0),
                    ccb.ccbKv8Rows(v.data_ptr(), count * row, row, self.head_dim, kind, 0), count, first, self.err)
         return k, v
-
-    def check(self) -> None:
-        """Raise if a call on this cache met a bad page number, length or
-        count since the last check.  Waits for the device."""
-        status = int(self.err.item())
-        self.err.zero_()
-        ccb.check(status, "8-bit cache")
