@@ -17,10 +17,11 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libccb.so")
 SOURCES = ["ccb_kernels.hip", "ccb_api.hip", "ccb_kv8_cache.hip", "ccb_kv8_attend.hip",
-           "ccb_kv8_api.hip", "ccb_pages.hip"]
-HEADERS = [os.path.join(ROOT, "include", h) for h in ("ccb.h", "ccb_device.h", "ccb_kv8.h", "ccb_pages.h")] + \
+           "ccb_kv8_api.hip", "ccb_kv4_cache.hip", "ccb_kv4_attend.hip", "ccb_kv4_api.hip", "ccb_pages.hip"]
+HEADERS = [os.path.join(ROOT, "include", h) for h in ("ccb.h", "ccb_device.h", "ccb_kv8.h", "ccb_kv4.h",
+                                                     "ccb_pages.h")] + \
           [os.path.join(CSRC, h) for h in ("ccb_internal.h", "ccb_kv8_internal.h", "ccb_kv8_math.h",
-                                           "ccb_kv8_device.h")]
+                                           "ccb_kv8_device.h", "ccb_kv4_internal.h")]
 
 
 # flags shared by every compile of the kernels (the library and its review)

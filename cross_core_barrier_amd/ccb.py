@@ -95,6 +95,14 @@ class ccbKv8Rows(ctypes.Structure):
                 ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class ccbKv4Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kScale", ctypes.c_void_p),
+                ("vScale", ctypes.c_void_p), ("pageTable", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("tableStride", ctypes.c_int64), ("numPages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("pageSize", ctypes.c_int32), ("headDim", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("maxPages", ctypes.c_int32)]
+
+
 CCB_PAGES_MAX_BATCH = 8192
 
 
@@ -137,7 +145,7 @@ def check(status: int, what: str = "ccb call") -> None:
 _V = ctypes.c_void_p
 _SZ, _F32 = ctypes.c_size_t, ctypes.c_float
 _KC, _KR = ctypes.POINTER(ccbKv8Cache), ctypes.POINTER(ccbKv8Rows)
-_PP = ctypes.POINTER(ccbPagePool)
+_K4, _PP = ctypes.POINTER(ccbKv4Cache), ctypes.POINTER(ccbPagePool)
 _PT, _SM = ctypes.POINTER(ccbPageTable), ctypes.POINTER(ccbSlotMaps)
 _I32, _U32, _I64, _U64 = ctypes.c_int32, ctypes.c_uint32, ctypes.c_int64, ctypes.c_uint64
 
@@ -199,6 +207,10 @@ _f = {
     "ccb_kv8_evict": _sig("ccb_kv8_evict", _I32, _KC, _KC, _I32, _I32, _I32, _V, _V, _SZ, _V, _V),
     "ccb_kv8_evict_workspace_bytes": _sig("ccb_kv8_evict_workspace_bytes", _SZ, _KC, _I32),
     "ccb_kv8_read": _sig("ccb_kv8_read", _I32, _KC, _KR, _KR, _I32, _V, _V, _V),
+    "ccb_kv4_append": _sig("ccb_kv4_append", _I32, _K4, _KR, _KR, _I32, _V, _V, _V),
+    "ccb_kv4_attend": _sig("ccb_kv4_attend", _I32, _K4, _KR, _KR, _V, _I32, _I32, _F32, _I32, _V, _SZ, _V, _V),
+    "ccb_kv4_attend_workspace_bytes": _sig("ccb_kv4_attend_workspace_bytes", _SZ, _K4, _I32, _I32),
+    "ccb_kv4_read": _sig("ccb_kv4_read", _I32, _K4, _KR, _KR, _I32, _V, _V, _V),
     "ccb_pages_trim": _sig("ccb_pages_trim", _I32, _PP, _PT, _V, _V, _V),
     "ccb_pages_grow": _sig("ccb_pages_grow", _I32, _PP, _PT, _V, _SM, _V, _V),
 }
@@ -428,6 +440,27 @@ def ccb_kv8_evict_workspace_bytes(src, budget: int) -> int:
 
 def ccb_kv8_read(cache, k_out, v_out, count, first=None, err=None, stream=None) -> int:
     return _f["ccb_kv8_read"](cache, k_out, v_out, count, _p(first), _p(err), _s(stream))
+
+
+# --- 4-bit key/value cache ------------------------------------------------------------
+# cache arguments are ccbKv4Cache structures, rows ccbKv8Rows structures (or None)
+
+def ccb_kv4_append(cache, k_new, v_new, n_new, slots, err=None, stream=None) -> int:
+    return _f["ccb_kv4_append"](cache, k_new, v_new, n_new, _p(slots), _p(err), _s(stream))
+
+
+def ccb_kv4_attend(cache, q, out, lse, heads_q, n_query, scale, window, ws, ws_bytes, err=None,
+                   stream=None) -> int:
+    return _f["ccb_kv4_attend"](cache, q, out, _p(lse), heads_q, n_query, scale, window, _p(ws), ws_bytes,
+                                _p(err), _s(stream))
+
+
+def ccb_kv4_attend_workspace_bytes(cache, heads_q: int, n_query: int) -> int:
+    return int(_f["ccb_kv4_attend_workspace_bytes"](cache, heads_q, n_query))
+
+
+def ccb_kv4_read(cache, k_out, v_out, count, first=None, err=None, stream=None) -> int:
+    return _f["ccb_kv4_read"](cache, k_out, v_out, count, _p(first), _p(err), _s(stream))
 
 
 # --- pages of a paged cache -------------------------------------------------------------
