@@ -24,7 +24,8 @@ ccbStatus check_cache(const ccbKv4Cache* c)
         c->headDim != 256)
         return CCB_ERR_INVALID_VALUE;
     if (c->numPages < 1 || c->heads < 1 || c->heads > 65536 || c->batch < 0 || c->maxPages < 1 ||
-        (int64_t)c->maxPages * c->pageSize > kMaxTokens || c->tableStride < c->maxPages)
+        (int64_t)c->maxPages * c->pageSize > kMaxTokens || c->tableStride < c->maxPages ||
+        (int64_t)c->numPages > (int64_t)UINT32_MAX / ((int64_t)c->heads * c->pageSize))
         return CCB_ERR_INVALID_VALUE;
     if (c->batch == 0) return CCB_OK;
     if (c->k == nullptr || c->v == nullptr || c->kScale == nullptr || c->vScale == nullptr ||

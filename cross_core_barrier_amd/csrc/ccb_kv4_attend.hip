@@ -1,8 +1,45 @@
 // ccb_kv4_attend.hip -- attention of a decoding step over the 4-bit key/value
 // cache, in one pass over the codes on the matrix cores, split over tokens.
+//
+// The rows of one cache head (its queries and query heads) share every key and
+// value, so one workgroup takes a (sequence, cache head, run of tokens) and up
+// to 16 rows.  Its eight waves take 32-token tiles in turn and never wait for
+// one another in the loop; each keeps its own running maximum, sum and weighted
+// values.
+//
+// S^T = K Q^T and O^T = V^T P^T on 16x16x32 tiles.  In that order a row of
+// scores lies on one lane index (lane % 16), so the softmax needs no
+// transposition: a lane's 4 + 4 scores of a tile are the 8 places of the next
+// product's operand that it has to supply.  Which dimension or token stands at
+// which place of a contraction is free as long as both operands agree: lane (n,
+// g) takes a quarter of token n's dimensions, side by side in memory and under
+// one scale (two at most), and the queries are laid out to match.  So keys go
+// from memory into registers and through the conversion, which applies the
+// scale, into the product; nothing of them passes LDS.  Values are converted the
+// same way, written to the wave's own part of LDS as bf16, and read transposed.
+//
+// A code times its power of two is exact in bf16, and so is an fp16 query in two
+// bf16 pieces: q k is exact up to its 32-bit sums.  The weights go into the
+// second product as two bf16 pieces, together within 2^-18.  (One fp16 number,
+// 2^-12, with values held relative to the largest scale, takes 8 products and 20
+// instructions less a tile and was 2% faster: 24.3 us against 24.9 for 32
+// sequences of 100 to 4096 tokens, too little for what it loses.)
+//
+// What bounds it.  A tile of 32 tokens (D = 128) costs a wave about 260
+// instructions for 4352 bytes, which a workgroup of 8 waves gets through in 1.1
+// us: large even calls are bound by memory (64 sequences of 16384 tokens: 1.13 GB
+// in 198 us, 5.7 TB/s), a long sequence on its own workgroup by the issue of
+// instructions (30 GB/s a CU), and short calls by the start (about 6 us: launch,
+// length -> page -> codes, the join of the waves).  Taking two tiles ahead, 16
+// waves a workgroup, the next tile's scores beside this one's weights, or all
+// transposed reads at once changed little or cost (24.5 us against 26.2, 23.5,
+// 26.6 and 25.0; 16 waves take 19.6 us against 14.6 for 200 short sequences).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
+#include <chrono>
 
 #include "ccb_kv4_internal.h"
 #include "ccb_kv8_device.h"
@@ -11,14 +48,16 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kThreads = 512;  // of a workgroup that takes a run of tokens
+constexpr int kThreads = 512;                  // of a workgroup that takes a run of tokens
 constexpr int kWaves = kThreads / 64;
 constexpr int kJoinThreads = 256;
 constexpr int kTile = 32;                     // tokens of a wave's step
 constexpr int kRunUnit = kWaves * kTile;
-constexpr int kSegment = 32 * kWaves * kTile;  // tokens whose pages fit a wave's lanes
+constexpr int kSegment = 32 * kRunUnit;  // tokens whose pages fit a wave's lanes
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr uint32_t kNone = 0xffffffffu;
+constexpr int kJoinHere = 64;    // runs that the last of them may join, at most
 constexpr int kJoinRuns = 32;   // more of them are joined by a workgroup, not a wave
 constexpr float kSlack = 8.0f;  // how far (in powers of two) scores may pass the running maximum
 
@@ -31,13 +70,17 @@ typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
 struct Plan {
     ccb::Kv4AttendArgs a;
-    int32_t pairs;      // (sequence, cache head)
     int32_t rows;       // of a cache head
-    int32_t tilesN;     // NT
     int32_t rowBlocks;  // workgroups that share a run of tokens
-    int32_t splits;     // runs of a sequence, see range_of
-    float* partO;       // [pair][split][row][D], unused for one run
-    float2* partML;     // [pair][split][row]: maximum (base 2) and sum
+    int32_t runs;       // of a head, over all sequences, at most: see chunk_of
+    int32_t whole;      // units of a sequence that is one run
+    float least;        // units of a run, at least
+    float lowBy, highBy;  // about 1 / runs and 1 / (runs - sequences): see place_of
+    bool joinHere;      // the run that ends last joins a sequence's, else another kernel
+    float* partO;       // [head][run][row][D], of sequences with several runs
+    float2* partML;     // [head][run][row]: maximum (base 2) and sum
+    uint64_t* tags;     // [head][rowBlock][run]: see join_here
+    uint64_t tag;
 };
 
 __device__ __forceinline__ f4 mfma(const u4& a, const u4& b, const f4& c)
@@ -67,37 +110,135 @@ __device__ __forceinline__ void pieces(float a, float b, uint32_t& hi, uint32_t&
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// What a sequence's queries may see, and its runs.  Every sequence has
-// p.splits of them, as long as its own length asks: the capacity, which is all
-// that the host knows, may be many times what a sequence holds.
-struct Range {
+// Memory that workgroups on several XCDs share within the kernel: accesses that
+// no cache of one XCD's answers.
+__device__ __forceinline__ void store_shared(float* p, float a, float b)
+{
+    const f2 x = {a, b};
+    __hip_atomic_store((uint64_t*)p, __builtin_bit_cast(uint64_t, x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ f2 load_shared(const float* p)
+{
+    return __builtin_bit_cast(f2, __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+
+// What a sequence's queries may see.
+struct Seen {
     int32_t len;    // 0 where the length is bad
     int32_t first;  // first token any query sees
     int32_t base;   // first, at a tile's border: where the runs start
-    int32_t chunk;  // tokens of a run, a multiple of kRunUnit
-    int32_t runs;   // that hold tokens
 };
 
-__device__ __forceinline__ Range range_of(const Plan& p, int32_t b)
+__device__ __forceinline__ Seen seen_of(const ccb::Kv4AttendArgs& a, int32_t len)
 {
-    const ccb::Kv4AttendArgs& a = p.a;
-    Range r;
-    r.len = checked_len(a.c.lens[b], a.c.maxPages * a.c.pageSize);
+    Seen r;
+    r.len = checked_len(len, a.c.maxPages * a.c.pageSize);
     if (r.len < 0) {
-        if (threadIdx.x == 0) report(a.err);
+        report(a.err);
         r.len = 0;
     }
     const int64_t f = a.window > 0 ? (int64_t)r.len - a.nQuery + 1 - a.window : 0;
     r.first = f > 0 ? (int32_t)f : 0;
     r.base = r.first & ~(kTile - 1);
-    const uint32_t held = (uint32_t)(r.len - r.base), splits = (uint32_t)p.splits;
-    r.chunk = (int32_t)(((held + splits * kRunUnit - 1) / (splits * kRunUnit)) * kRunUnit);
-    r.runs = r.chunk > 0 ? (int32_t)((held + (uint32_t)r.chunk - 1) / (uint32_t)r.chunk) : 0;
     return r;
 }
 
+// Its length in units of kRunUnit tokens, at most 2^22.
+__device__ __forceinline__ int32_t units_of(const Seen& r) { return (r.len - r.base + kRunUnit - 1) / kRunUnit; }
+
+// A sequence's units as they count where runs are made: a short one is one run,
+// and so is an empty one, whose results somebody has to write.
+__device__ __forceinline__ float counted(int32_t units, int32_t whole) { return units <= whole ? 1.0f : (float)units; }
+
+// Runs of `chunk` units in that many, whole numbers below 2^23: their quotient
+// rounded up.  It comes out of the estimate at most one too small, and then the
+// remainder shows it.
+__device__ __forceinline__ float runs_in(float units, float chunk, float inverse)
+{
+    float q = floorf(units * inverse);
+    const float r = fmaf(-q, chunk, units);
+    q += r > 0.0f ? 1.0f : 0.0f;
+    return q + (r > chunk ? 1.0f : 0.0f);
+}
+
+// x summed over the lanes up to this one (no exchange through LDS, whose latency
+// six times over is a third of a microsecond).
+__device__ __forceinline__ int32_t scan(int32_t x)
+{
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);  // 1, 2, 4, 8 lanes before, in rows of 16
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // the last of a row, to the next one
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // the last of two rows, to the next two
+    return x;
+}
+
+// A sequence and its runs among those of its head.
+struct Place {
+    int32_t b, first, n;  // n = 0: there is no such run
+    int32_t chunk;        // a run's length in units
+    int32_t len;          // as it stands in lens
+};
+
+// The sequence that run u belongs to, or (u < 0) sequence b itself.  A run's
+// length, for all sequences, is the least with which there are no more than
+// p.runs runs (of up to 64 sequences; of more, one that is enough for that), so
+// that a long sequence has many workgroups and a short one few.  The host knows
+// only the capacity, which may be many times what a sequence holds.
+__device__ __forceinline__ Place place_of(const Plan& p, int32_t u, int32_t b)
+{
+    const int lane = threadIdx.x & 63;
+    const int32_t batch = p.a.c.batch;
+    int32_t len = 0, sum = 0;
+    float units = 0.0f;
+    for (int32_t b0 = 0; b0 < batch; b0 += 64) {
+        int32_t held = 0;
+        if (b0 + lane < batch) {
+            len = p.a.c.lens[b0 + lane];
+            held = units_of(seen_of(p.a, len));
+        }
+        units = counted(held, p.whole);
+        sum += __builtin_amdgcn_readlane(scan(held), 63);  // (less than 2^31: see make_plan)
+    }
+    // (a few parts in 2^20 above and below the quotients)
+    const float high = fmaxf(ceilf((float)sum * p.highBy), p.least);
+    float chunk = high;
+    if (batch <= 64) {  // every lane tries another length between the bounds
+        const float low = fminf(high, fmaxf(floorf((float)sum * p.lowBy), p.least));
+        const float mine = lane == 63 ? high : low + floorf((high - low) * (float)lane * (1.0f / 63.0f));
+        const float inverse = __builtin_amdgcn_rcpf(mine);
+        float runs = 0.0f;
+#pragma unroll 4
+        for (int32_t i = 0; i < batch; ++i)
+            runs += runs_in(of_bits(__builtin_amdgcn_readlane(bits(units), i)), mine, inverse);
+        const uint64_t enough = __ballot(runs <= (float)p.runs || lane == 63);
+        chunk = of_bits(__builtin_amdgcn_readlane(bits(mine), __builtin_ctzll(enough)));
+    }
+    const float inverse = __builtin_amdgcn_rcpf(chunk);
+    int32_t before = 0;
+    for (int32_t b0 = 0; b0 < batch; b0 += 64) {
+        if (batch > 64 && b0 + lane < batch) {
+            len = p.a.c.lens[b0 + lane];
+            units = counted(units_of(seen_of(p.a, len)), p.whole);
+        }
+        const int32_t mine = b0 + lane < batch ? (int32_t)runs_in(units, chunk, inverse) : 0;
+        const int32_t upto = scan(mine);
+        const uint64_t here = __ballot(u >= 0 ? before + upto > u : b0 + lane == b);
+        if (here != 0) {
+            const int at = __builtin_ctzll(here);
+            const int32_t n = __builtin_amdgcn_readlane(mine, at);
+            return Place{b0 + at, before + __builtin_amdgcn_readlane(upto, at) - n, n, (int32_t)chunk,
+                         __builtin_amdgcn_readlane(len, at)};
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return Place{0, 0, 0, 1, 0};
+}
+
 // What query i sees, as [begin, end); empty for a row that is not there.
-__device__ __forceinline__ void seen_by(const ccb::Kv4AttendArgs& a, const Range& r, int32_t row, int32_t rows,
+__device__ __forceinline__ void seen_by(const ccb::Kv4AttendArgs& a, const Seen& r, int32_t row, int32_t rows,
                                         int32_t group, int32_t& begin, int32_t& end)
 {
     begin = 0, end = 0;
@@ -111,14 +252,6 @@ __device__ __forceinline__ void seen_by(const ccb::Kv4AttendArgs& a, const Range
 __device__ __forceinline__ int64_t row_at(const ccbKv8Rows& r, int32_t b, int32_t h, int32_t row, int32_t group)
 {
     return b * r.strideBatch + (row / group) * r.strideToken + (int64_t)(h * group + row % group) * r.strideHead;
-}
-
-// How the chunks of 16 dimensions (32 bytes) of a token's values are swapped in
-// LDS, so that the 8 tokens that half a wave reads at one chunk fall on all the banks.
-template <int D>
-__device__ __forceinline__ int swap_of(int t)
-{
-    return D == 64 || D == 192 ? (t >> 1) & 3 : D == 96 ? (t >> 2) & 1 : t & 7;
 }
 
 // Writes a row's results from the sum of its weighted values: 4 of its
@@ -140,9 +273,111 @@ __device__ __forceinline__ void write_row(const Plan& p, int32_t b, int32_t h, i
             all != 0.0f ? (top + log2f(all)) * kLn2 : -INFINITY;
 }
 
+// A maximum and sum joined with another (a sum of 0 has no maximum; a NaN stays).
+__device__ __forceinline__ void merge(float& top, float& all, float top2, float all2)
+{
+    const float t = fmaxf(top, top2);
+    const float x = all == 0.0f ? 0.0f : all * exp2_(top - t);
+    const float y = all2 == 0.0f ? 0.0f : all2 * exp2_(top2 - t);
+    top = t;
+    all = x + y;
+}
+
+// Joins a sequence's runs where there are a few: the workgroup that finds all of
+// them done does it.  A run's workgroup stores its parts, waits until they are in
+// memory, stores its tag, waits again, and reads the tags of all runs.  The last
+// one to store its tag so finds all of them set, and so may others, which then
+// write the same results; but for those that find tags cleared again, by one that
+// joins already.  The tag is this call's own number, so that it does not matter
+// what the workspace held, and the tags are cleared, so that a replayed call may
+// use its number again.
+template <int T, int D, int R>
+__device__ __forceinline__ void join_here(const Plan& p, const Place& runs, int32_t run, int32_t h, int32_t row0,
+                                          uint8_t* lds)
+{
+    const int32_t n = runs.n;
+    __shared__ int32_t all;
+    const int tid = threadIdx.x;
+    uint64_t* tags = p.tags + ((int64_t)h * p.rowBlocks + row0 / R) * p.runs + runs.first;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid < 64) {
+        if (tid == 0) {
+            __hip_atomic_store(tags + run, p.tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        bool set = true;
+        for (int32_t s = tid; s < n; s += 64)
+            set &= __hip_atomic_load(tags + s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.tag;
+        set = __all(set);
+        if (tid == 0) all = set;
+    }
+    __syncthreads();
+    if (all == 0) return;
+    for (int32_t s = tid; s < n; s += kThreads)
+        __hip_atomic_store(tags + s, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+
+    constexpr int V = D / 4, kWide = 8;  // vectors of a row; loads in flight
+    f4* const sums = (f4*)lds;                   // [thread]
+    float* const factor = (float*)(sums + kThreads);  // [run][R]
+    float* const top = factor + kJoinHere * R;   // [R]
+    float* const total = top + R;                // [R]
+    const int32_t rows = p.rows - row0 < R ? p.rows - row0 : R, items = V * rows;
+    const int32_t side = kThreads / items;  // runs side by side, where a pass has threads for them
+    const int32_t sg = side > 1 ? tid / items : 0, by = side > 1 ? side : 1;
+    const int64_t first = ((int64_t)h * p.runs + runs.first) * p.rows + row0;
+    auto part_at = [&](int32_t s, int32_t item) {
+        const float* src = p.partO + (first + (int64_t)s * p.rows + item / V) * D + item % V * 4;
+        const f2 x = load_shared(src), y = load_shared(src + 2);
+        return f4{x.x, x.y, y.x, y.y};
+    };
+    for (int32_t base = 0; base < items; base += kThreads) {
+        const int32_t item = side > 1 ? tid % items : base + tid;
+        const bool mine = item < items && sg < by;
+        f4 v[kWide];
+#pragma unroll
+        for (int k = 0; k < kWide; ++k)
+            if (mine && sg + k * by < n) v[k] = part_at(sg + k * by, item);
+        if (base == 0) {  // a wave for every eighth row, a lane for each run
+            const int lane = tid & 63;
+            for (int32_t i = tid >> 6; i < rows; i += kWaves) {
+                f2 x = {-INFINITY, 0.0f};
+                if (lane < n) x = load_shared((const float*)(p.partML + first + (int64_t)lane * p.rows + i));
+                float m = x.x;
+#pragma unroll
+                for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+                const float f = x.y == 0.0f ? 0.0f : exp2_(x.x - m);
+                float l = x.y * f;
+#pragma unroll
+                for (int d = 32; d >= 1; d >>= 1) l += __shfl_xor(l, d, 64);
+                if (lane < n) factor[lane * R + i] = f;
+                if (lane == 0) top[i] = m, total[i] = l;
+            }
+            __syncthreads();
+        }
+        f4 o = {0, 0, 0, 0};
+        if (mine) {
+            const float* f = factor + item / V;
+#pragma unroll
+            for (int k = 0; k < kWide; ++k)
+                if (sg + k * by < n) o += v[k] * f[(sg + k * by) * R];
+            for (int32_t s = sg + kWide * by; s < n; s += by) o += part_at(s, item) * f[s * R];
+        }
+        if (side > 1) {
+            sums[tid] = o;
+            __syncthreads();
+            if (sg == 0)
+                for (int32_t i = 1; i < side; ++i) o += sums[i * items + item];
+        }
+        if (mine && sg == 0) write_row<T>(p, runs.b, h, row0 + item / V, item % V, o, top[item / V], total[item / V]);
+    }
+}
+
 // One half (16 tokens) of a wave's tile, keys or values: a lane's D / 4
 // dimensions of token n, and the scales of the first and the last of them (no
 // lane has more than two).
+typedef const __attribute__((address_space(1))) uint8_t* global;
+
 template <int D>
 struct Half {
     uint32_t w[D / 32];
@@ -151,28 +386,41 @@ struct Half {
     // dimensions g * D/4 + 8 j .. + 7 lie under the scale (g * D/4 + 8 j) / 32
     static __device__ __forceinline__ int group_at(int g, int j) { return (g * (D / 32) + j) >> 2; }
 
-    // from the codes and scales of the half's 16 rows
-    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int n, int g)
+    // where a lane's codes and scales are within 16 rows
+    static __device__ __forceinline__ uint32_t codes_at(int n, int g) { return (uint32_t)(n * (D / 2) + g * (D / 8)); }
+    static __device__ __forceinline__ uint32_t scale_at(int n, int g, int j)
     {
-        const uint8_t* src = codes + (n * (D / 2) + g * (D / 8));
+        return (uint32_t)(n * (D / 32) + group_at(g, j));
+    }
+
+    // From the codes and scales of the half's 16 rows, the first of them `row` of
+    // the cache's: scalar addresses and 32-bit offsets.
+    __device__ __forceinline__ void load(const uint8_t* allCodes, const uint8_t* allScales, uint32_t row,
+                                         uint32_t codesAt, uint32_t scaleAt0, uint32_t scaleAt1)
+    {
+        typedef const __attribute__((address_space(1))) u4* global4;
+        typedef const __attribute__((address_space(1))) u2* global2;
+        typedef const __attribute__((address_space(1))) uint32_t* global1;
+        uint64_t at = (uint64_t)allCodes + (uint64_t)row * (D / 2), scaleAt = (uint64_t)allScales + (uint64_t)row * (D / 32);
+        asm("" : "+s"(at), "+s"(scaleAt));  // (not added to the offsets in vector registers)
+        const global src = (global)at + codesAt, scales = (global)scaleAt;
         if constexpr (D == 64) {
-            const u2 x = *(const u2*)src;
+            const u2 x = *(global2)src;
             w[0] = x.x, w[1] = x.y;
         } else if constexpr (D == 96) {
-            const uint32_t* x = (const uint32_t*)src;
+            const global1 x = (global1)src;
             w[0] = x[0], w[1] = x[1], w[2] = x[2];
         } else if constexpr (D == 192) {
-            const u2* x = (const u2*)src;
+            const global2 x = (global2)src;
 #pragma unroll
             for (int i = 0; i < 3; ++i) w[2 * i] = x[i].x, w[2 * i + 1] = x[i].y;
         } else {
-            const u4* x = (const u4*)src;
+            const global4 x = (global4)src;
 #pragma unroll
             for (int i = 0; i < D / 128; ++i) w[4 * i] = x[i].x, w[4 * i + 1] = x[i].y, w[4 * i + 2] = x[i].z, w[4 * i + 3] = x[i].w;
         }
-        const uint8_t* s = scales + n * (D / 32);
-        s0 = s[group_at(g, 0)];
-        s1 = D <= 128 && D != 96 ? s0 : s[group_at(g, D / 32 - 1)];
+        s0 = scales[scaleAt0];
+        s1 = D == 64 || D == 128 ? s0 : scales[scaleAt1];
     }
 
     // words 8 j .. 8 j + 7 as bf16
@@ -183,43 +431,55 @@ struct Half {
     }
 };
 
-template <int D>
-struct Tile {
-    Half<D> k[2], v[2];
-};
-
 template <int T, int D, int NT>
 __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
 {
     constexpr int NB = D / 16;                          // blocks of 16 dimensions
     constexpr int NJ = D / 32;                          // steps of the first product
     constexpr int NQ = T == CCB_KV8_BF16 ? 1 : 2;       // bf16 pieces of a query: exact
-    __shared__ __attribute__((aligned(16))) uint8_t vBuf[kWaves][kTile * D * 2];
+    // A token's values in LDS, and 32 bytes more: the 8 tokens that half a wave
+    // reads 16 dimensions of fall on all the banks, and so do 8 writes of 16 bytes.
+    constexpr int S = 2 * D + 32;
+    __shared__ __attribute__((aligned(16))) uint8_t vBuf[kWaves][kTile * S];
     __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT];
 
     const ccb::Kv4AttendArgs& a = p.a;
     const ccbKv4Cache& c = a.c;
     // Neighbouring workgroups, which go to different XCDs, take neighbouring
-    // heads of one run: runs past short sequences' ends cost every XCD alike.
+    // heads of one run: runs past the last cost every XCD alike.
     uint32_t rest = blockIdx.x;
-    const int32_t pair = rest % (uint32_t)p.pairs;
-    rest /= (uint32_t)p.pairs;
+    const int32_t h = rest % (uint32_t)c.heads;
+    rest /= (uint32_t)c.heads;
     const int32_t row0 = (int32_t)(rest % (uint32_t)p.rowBlocks) * (16 * NT);
-    const int32_t split = rest / (uint32_t)p.rowBlocks;
-    const int32_t h = pair % c.heads, b = pair / c.heads;
+    const int32_t number = rest / (uint32_t)p.rowBlocks;
     const int32_t P = c.pageSize, group = a.headsQ / c.heads;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
+
+    Place runs = {number, number, 1, 1, 0};  // as many runs as sequences: one each
+    if (p.runs > c.batch) {
+        runs = place_of(p, number, 0);
+        if (runs.n == 0) return;
+    }
+    const int32_t b = runs.b, run = number - runs.first;
 
     // lane i's place in a segment: the wave's i-th half tile
     const int32_t shift = __builtin_ctz(P);
     const int32_t laneAt = ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
     const int32_t* table = c.pageTable + b * c.tableStride;
+    // without a window a single run's place does not depend on the length: the
+    // first page numbers are fetched beside it (they may be of pages past the end)
+    int32_t entry = -1;
+    const bool early = a.window == 0 && run == 0;
+    if (early && laneAt < c.maxPages * P) entry = table[laneAt >> shift];
 
-    const Range r = range_of(p, b);
-    if (split > 0 && split >= r.runs) return;  // the join knows
-    const int32_t lo = r.base + split * r.chunk;
-    const int32_t hi = r.len - lo < r.chunk ? r.len : lo + r.chunk;
+    Seen r = seen_of(a, p.runs > c.batch ? runs.len : c.lens[b]);
+    // (alike in all lanes: what follows from it stays in scalar registers)
+    r.len = __builtin_amdgcn_readfirstlane(r.len);
+    r.first = __builtin_amdgcn_readfirstlane(r.first);
+    r.base = __builtin_amdgcn_readfirstlane(r.base);
+    const int32_t tokens = runs.chunk * kRunUnit, lo = r.base + (runs.n > 1 ? run * tokens : 0);
+    const int32_t hi = runs.n > 1 && r.len - lo > tokens ? lo + tokens : r.len;
 
     // Queries, 8 values of a row per lane and step (a row that is not there
     // computes row0's again, for nothing).  Scores are scaled by |scale|, a
@@ -267,85 +527,112 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
         for (int d = 0; d < NB; ++d) o[nt][d] = f4{0, 0, 0, 0};
     }
 
+    const uint32_t laneCodes = Half<D>::codes_at(n, g);
+    const uint32_t laneScale0 = Half<D>::scale_at(n, g, 0), laneScale1 = Half<D>::scale_at(n, g, D / 32 - 1);
     // where this lane reads values: 4 lanes for a token's 16 dimensions
     const int vTok = 4 * g + (n >> 2);
     uint8_t* const buf = vBuf[wave];
-    const uint8_t* const vFrom[2] = {buf + vTok * (2 * D) + (n & 3) * 8, buf + (16 + vTok) * (2 * D) + (n & 3) * 8};
-    const int vSwap = swap_of<D>(vTok), wSwap = swap_of<D>(n);  // alike for token 16 + x
+    const uint8_t* const vFrom = buf + vTok * S + (n & 3) * 8;
+    uint8_t* const vTo = buf + n * S + g * (D / 2);
 
     for (int32_t seg = lo; seg < hi; seg += kSegment) {
         const int32_t segEnd = hi - seg < kSegment ? hi : seg + kSegment;
-        // lane i holds the page of the wave's i-th half tile
-        int32_t page = -1;
+        // lane i holds the first row of the wave's i-th half tile, among all of the
+        // cache's (less than 2^32 - 1), or kNone
+        uint32_t rows = kNone;
         {
             const int32_t t = seg + laneAt;
             if (t < segEnd && t + 16 > r.first) {
-                page = checked_page(table[t >> shift], c.numPages);
+                const int32_t page = checked_page(early && seg == lo ? entry : table[t >> shift], c.numPages);
                 if (page < 0) report(a.err);
+                else rows = ((((uint32_t)page * (uint32_t)c.heads) + (uint32_t)h) << shift) + ((uint32_t)t & (uint32_t)(P - 1));
             }
         }
         const int32_t nTiles = ((segEnd - seg + kTile - 1) / kTile - wave + kWaves - 1) / kWaves;
 
-        auto load = [&](int32_t i, Tile<D>& x) {
-            const int32_t t = seg + (i * kWaves + wave) * kTile;
+        auto load = [&](int32_t i, const uint8_t* codes, const uint8_t* scales, Half<D>(&x)[2]) {
+            // (the compiler has to see here that these are 32 bits)
+            uint32_t codesAt = laneCodes, scaleAt0 = laneScale0, scaleAt1 = laneScale1;
+            asm("" : "+v"(codesAt), "+v"(scaleAt0), "+v"(scaleAt1));
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                int32_t pg = __builtin_amdgcn_readlane(page, 2 * i + half);
-                pg = pg < 0 ? 0 : pg;  // an unseen page's place: page 0 is loaded and not used
-                const int64_t row = ((int64_t)pg * c.heads + h) * P + ((t + 16 * half) & (P - 1));
-                x.k[half].load(c.k + row * (D / 2), c.kScale + row * (D / 32), n, g);
-                x.v[half].load(c.v + row * (D / 2), c.vScale + row * (D / 32), n, g);
+                uint32_t row = (uint32_t)__builtin_amdgcn_readlane((int32_t)rows, 2 * i + half);
+                row = row == kNone ? 0 : row;  // an unseen page's place: page 0 is loaded and not used
+                x[half].load(codes, scales, row, codesAt, scaleAt0, scaleAt1);
             }
         };
 
-        auto step = [&](int32_t i, Tile<D>& x) {
+        Half<D> key[2], val[2];
+        auto step = [&](int32_t i) {
             const int32_t t0 = seg + (i * kWaves + wave) * kTile;
-            const int32_t pg0 = __builtin_amdgcn_readlane(page, 2 * i);
-            const int32_t pg1 = __builtin_amdgcn_readlane(page, 2 * i + 1);
-            const bool whole = t0 >= allBegin && t0 + kTile <= allEnd && (pg0 | pg1) >= 0;
+            const bool there0 = (uint32_t)__builtin_amdgcn_readlane((int32_t)rows, 2 * i) != kNone;
+            const bool there1 = (uint32_t)__builtin_amdgcn_readlane((int32_t)rows, 2 * i + 1) != kNone;
+            const bool whole = t0 >= allBegin && t0 + kTile <= allEnd && there0 && there1;
             // scores
             f4 s[NT][2];
+            {
+                float f[2][2];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float f0 = of_bits(x.k[half].s0 << 23), f1 = of_bits(x.k[half].s1 << 23);
+                for (int half = 0; half < 2; ++half) {
+                    f[half][0] = of_bits(key[half].s0 << 23), f[half][1] = of_bits(key[half].s1 << 23);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) s[nt][half] = f4{0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const u4 key = x.k[half].values(j, g, f0, f1);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int k = 0; k < NQ; ++k) s[nt][half] = mfma(key, q[nt][j][k], s[nt][half]);
+                    for (int nt = 0; nt < NT; ++nt) s[nt][half] = f4{0, 0, 0, 0};
                 }
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const u4 k8 = key[half].values(j, g, f[half][0], f[half][1]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int k = 0; k < NQ; ++k) s[nt][half] = mfma(k8, q[nt][j][k], s[nt][half]);
+                    }
             }
+            // the next tile's keys (behind the last one's: the same again, so that the
+            // number of loads in flight is the same in every step)
+            const int32_t next = i + 1 < nTiles ? i + 1 : i;
+            load(next, c.k, c.kScale, key);
             float by = scale2;
             bool grows = false;
             if (!whole) {
+                asm volatile("");  // a branch: its instructions would be a third of the step's
                 by = 1.0f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int32_t t = t0 + 4 * g + e;
-                        s[nt][0][e] = t >= begin[nt] && t < end[nt] && pg0 >= 0 ? s[nt][0][e] * scale2 : -INFINITY;
-                        s[nt][1][e] = t + 16 >= begin[nt] && t + 16 < end[nt] && pg1 >= 0 ? s[nt][1][e] * scale2 : -INFINITY;
+                        s[nt][0][e] = t >= begin[nt] && t < end[nt] && there0 ? s[nt][0][e] * scale2 : -INFINITY;
+                        s[nt][1][e] = t + 16 >= begin[nt] && t + 16 < end[nt] && there1 ? s[nt][1][e] * scale2 : -INFINITY;
                     }
                 // values that are not there: any scale, but a number
-                if (!(pg0 >= 0 && t0 + n < r.len)) x.v[0].s0 = x.v[0].s1 = 127;
-                if (!(pg1 >= 0 && t0 + 16 + n < r.len)) x.v[1].s0 = x.v[1].s1 = 127;
+                if (!(there0 && t0 + n < r.len)) val[0].s0 = val[0].s1 = 127;
+                if (!(there1 && t0 + 16 + n < r.len)) val[1].s0 = val[1].s1 = 127;
             }
             // values into LDS, as bf16
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float f0 = of_bits(x.v[half].s0 << 23), f1 = of_bits(x.v[half].s1 << 23);
-                uint8_t* dst = buf + (16 * half + n) * (2 * D);
+                const float f0 = of_bits(val[half].s0 << 23), f1 = of_bits(val[half].s1 << 23);
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const int at = g * NJ + j;  // of 8 dimensions
-                    *(u4*)(dst + ((((at >> 1) ^ wSwap) << 5) | ((at & 1) << 4))) = x.v[half].values(j, g, f0, f1);
-                }
+                for (int j = 0; j < NJ; ++j) *(u4*)(vTo + 16 * half * S + 16 * j) = val[half].values(j, g, f0, f1);
             }
+            load(next, c.v, c.vScale, val);
+            // Transposed, the first blocks of 16 dimensions are asked for before the
+            // weights are computed.  (A wave's LDS accesses keep the program's order.)
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            constexpr int NR = NB % 4 == 0 ? 4 : 3;
+            u4 value[NR];
+            auto transposed = [&](int d) {
+                typedef __attribute__((address_space(3))) s4 lds4;
+                const u2 y0 = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vFrom + 32 * d)));
+                const u2 y1 = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vFrom + 16 * S + 32 * d)));
+                return u4{y0.x, y0.y, y1.x, y1.y};
+            };
+#pragma unroll
+            for (int d = 0; d < NR; ++d) value[d] = transposed(d);
+            __builtin_amdgcn_sched_barrier(0);
             float mx[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -382,38 +669,29 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
                     pl[nt][2 * half] = l0, pl[nt][2 * half + 1] = l1;
                 }
             }
-            // a wave's LDS accesses keep the program's order
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int d = 0; d < NB; ++d) {
-                typedef __attribute__((address_space(3))) s4 lds4;
-                const s4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vFrom[0] + ((d ^ vSwap) << 5)));
-                const s4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(vFrom[1] + ((d ^ vSwap) << 5)));
-                const u2 y0 = __builtin_bit_cast(u2, v0), y1 = __builtin_bit_cast(u2, v1);
-                const u4 y = {y0.x, y0.y, y1.x, y1.y};
+            for (int d0 = 0; d0 < NB; d0 += NR) {
+                if (d0 > 0) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    o[nt][d] = mfma(y, ph[nt], o[nt][d]);
-                    o[nt][d] = mfma(y, pl[nt], o[nt][d]);
+                    for (int d = 0; d < NR; ++d) value[d] = transposed(d0 + d);
                 }
+#pragma unroll
+                for (int d = 0; d < NR; ++d)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) o[nt][d0 + d] = mfma(value[d], ph[nt], o[nt][d0 + d]);
+#pragma unroll
+                for (int d = 0; d < NR; ++d)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) o[nt][d0 + d] = mfma(value[d], pl[nt], o[nt][d0 + d]);
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         };
 
-        // One tile ahead; the last is asked for again, so that the number of
-        // loads in flight is the same in every step.
         if (nTiles > 0) {
-            Tile<D> x, y;
-            load(0, x);
-            for (int32_t i = 0; i < nTiles; i += 2) {
-                load(i + 1 < nTiles ? i + 1 : i, y);
-                step(i, x);
-                if (i + 1 >= nTiles) break;
-                load(i + 2 < nTiles ? i + 2 : i + 1, x);
-                step(i + 1, y);
-            }
+            load(0, c.k, c.kScale, key);
+            load(0, c.v, c.vScale, val);
+            for (int32_t i = 0; i < nTiles; ++i) step(i);
         }
     }
 
@@ -425,7 +703,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
         if (g == 0) sm[wave][nt * 16 + n] = m[nt], sl[wave][nt * 16 + n] = l[nt];
     }
     __syncthreads();
-    const int64_t part = ((int64_t)pair * p.splits + split) * p.rows;
+    const int64_t part = ((int64_t)h * p.runs + number) * p.rows;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         float top = -INFINITY;
@@ -450,8 +728,13 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
                 ll += sl[w][nt * 16 + i] == 0.0f ? 0.0f : sl[w][nt * 16 + i] * exp2_(sm[w][nt * 16 + i] - mm);
-            if (p.splits == 1) {
+            if (runs.n == 1) {
                 write_row<T>(p, b, h, row, d4, sum, mm, ll);
+            } else if (p.joinHere) {
+                float* dst = p.partO + (part + row) * D + d4 * 4;
+                store_shared(dst, sum.x, sum.y);
+                store_shared(dst + 2, sum.z, sum.w);
+                if (d4 == 0) store_shared((float*)(p.partML + part + row), mm, ll);
             } else {
                 *(f4*)(p.partO + (part + row) * D + d4 * 4) = sum;
                 if (d4 == 0) p.partML[part + row] = make_float2(mm, ll);
@@ -459,16 +742,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
         }
         __syncthreads();
     }
-}
-
-// A maximum and sum joined with another (a sum of 0 has no maximum; a NaN stays).
-__device__ __forceinline__ void merge(float& top, float& all, float top2, float all2)
-{
-    const float t = fmaxf(top, top2);
-    const float x = all == 0.0f ? 0.0f : all * exp2_(top - t);
-    const float y = all2 == 0.0f ? 0.0f : all2 * exp2_(top2 - t);
-    top = t;
-    all = x + y;
+    if (runs.n > 1 && p.joinHere) join_here<T, D, 16 * NT>(p, runs, run, h, row0, vBuf[0]);
 }
 
 // Joins the runs of a row: four rows to a workgroup, or one where there are
@@ -481,13 +755,16 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_k_join(Plan p, int32_t D)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int32_t V = D / 4;  // vectors of a row
     const int64_t step = (int64_t)p.rows * D;
-    const bool many = p.splits > kJoinRuns;
+    const bool many = p.runs - p.a.c.batch >= kJoinRuns;
     const int64_t at = many ? blockIdx.x : (int64_t)blockIdx.x * kJoinWaves + wave;
     const int32_t pair = (int32_t)(at / p.rows), row = (int32_t)(at % p.rows);
-    if (pair >= p.pairs) return;  // (not where the workgroup works together)
+    if (pair >= p.a.c.batch * p.a.c.heads) return;  // (not where the workgroup works together)
     const int32_t h = pair % p.a.c.heads, b = pair / p.a.c.heads;
-    const int32_t n = range_of(p, b).runs;
-    const float2* ml = p.partML + (int64_t)pair * p.splits * p.rows + row;
+    const Place runs = place_of(p, -1, b);
+    const int32_t n = runs.n;
+    if (n <= 1) return;  // written by the run itself (the same in a workgroup that works together)
+    const int64_t first = ((int64_t)h * p.runs + runs.first) * p.rows + row;
+    const float2* ml = p.partML + first;
     float top = -INFINITY, all = 0.0f;
     for (int32_t s = lane; s < n; s += 64) {
         const float2 x = ml[(int64_t)s * p.rows];
@@ -498,7 +775,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_k_join(Plan p, int32_t D)
     // threads of a row: V for the vectors, and runs side by side
     const int32_t me = many ? tid : lane, groups = (many ? kJoinThreads : 64) / V;
     const int32_t d4 = me % V, sg = me / V;
-    const float* src = p.partO + ((int64_t)pair * p.splits * p.rows + row) * D + d4 * 4;
+    const float* src = p.partO + first * D + d4 * 4;
     f4 o = {0, 0, 0, 0};
     if (sg < groups) {
         int32_t s = sg;
@@ -535,52 +812,89 @@ __global__ __launch_bounds__(kJoinThreads) void kv4_k_join(Plan p, int32_t D)
 // which do not depend on the window.  There is a sequence and a query.
 size_t make_plan(Plan& p, const ccbKv4Cache& c, int32_t headsQ, int32_t nQuery, int32_t window, void* ws)
 {
-    const int64_t pairs = (int64_t)c.batch * c.heads;
-    const int64_t rows = (int64_t)nQuery * (headsQ / c.heads);
-    p.pairs = (int32_t)pairs;
+    const int64_t rows = (int64_t)nQuery * (headsQ / c.heads), batch = c.batch;
+    auto up = [](int64_t x, int64_t by) { return (x + by - 1) / by; };
     p.rows = (int32_t)rows;
+    p.rowBlocks = (int32_t)up(rows, 16);
+    const int64_t groups = (int64_t)c.heads * p.rowBlocks;  // workgroups that take a run
     // tokens that a sequence's queries may see, from a tile's border
     const int64_t room = (int64_t)c.maxPages * c.pageSize;
     int64_t span = room;
     if (window > 0 && (int64_t)window + nQuery - 1 + kTile < span)
         span = (int64_t)window + nQuery - 1 + kTile;
+    // One workgroup of 8 waves for each CU: the second one that it has room for
+    // brings no bandwidth, pays its start once more and makes more to join (16
+    // sequences of 4096 tokens 20.4 us, with 384 or 512 workgroups 23.7 and 21.5;
+    // 8 of 1500 to 16384, D = 256, 26.3 and 41).  More where a run could pass 2 MB
+    // of codes: many short sequences do not wait for a long one's end.
     constexpr int64_t target = 256, limit = 16 * target;
-    auto up = [](int64_t x, int64_t by) { return (x + by - 1) / by; };
-    auto runs = [&](int64_t tokens, int64_t groups) {
-        const int64_t byLength = up(tokens, (1 << 21) / c.headDim), mostHere = limit / groups;
-        int64_t n = byLength < mostHere ? byLength : mostHere;
-        n = n > target / groups ? n : target / groups;
-        n = n < up(tokens, kRunUnit) ? n : up(tokens, kRunUnit);
-        return n > 1 && tokens > 256 ? n : 1;
+    const int64_t longest = (1 << 21) / c.headDim;
+    // A sequence of so many units stays whole: a join costs 3 us, a unit 1.1 at D =
+    // 128 and 2.2 at 256 (6 sequences with a window of 1000: 9.8 us, cut 12.2).
+    p.whole = c.headDim <= 128 ? 5 : 2;
+    // runs of a head for sequences of up to `tokens`, and their least length
+    auto runs = [&](int64_t tokens, float& least) {
+        int64_t n = target / groups;
+        least = 1.0f;
+        if (tokens <= p.whole * kRunUnit || batch * up(tokens, kRunUnit) > INT32_MAX) return batch;
+        if (n <= batch) {  // enough workgroups, unless a sequence is long
+            if (tokens <= longest) return batch;
+            least = (float)up(longest, kRunUnit);
+            const int64_t more = up(batch * tokens, longest);
+            n = batch + (more < limit / groups ? more : limit / groups);
+        }
+        const int64_t most = batch * up(tokens, kRunUnit);
+        return n < most ? n : most;
     };
-    p.tilesN = 1;
-    p.rowBlocks = (int32_t)up(rows, 16 * p.tilesN);
-    p.splits = (int32_t)runs(span, pairs * p.rowBlocks);
-    const int64_t mostSplits = runs(room, pairs);  // over every window
+    float unused;
+    const int64_t roomy = runs(room, unused);  // over every window: the workspace holds so many
+    const int64_t asked = runs(span, p.least);
+    p.runs = (int32_t)(asked < roomy ? asked : roomy);
+    p.lowBy = (1.0f - 0x1p-20f) / (float)p.runs;
+    p.highBy = p.runs > batch ? (1.0f + 0x1p-20f) / (float)(p.runs - batch) : 0.0f;
+    const int64_t most = roomy > batch ? roomy : 0;
     size_t bytes = 0;
     auto take = [&](int64_t n, size_t each) {
         char* here = (char*)ws + bytes;
         bytes += ((size_t)n * each + 127) / 128 * 128;
         return here;
     };
-    const int64_t parts = mostSplits > 1 || rows > 16 ? pairs * mostSplits * rows : 0;
-    p.partO = (float*)take(parts * c.headDim, sizeof(float));
-    p.partML = (float2*)take(parts, sizeof(float2));
+    p.partO = (float*)take(c.heads * most * rows * c.headDim, sizeof(float));
+    p.partML = (float2*)take(c.heads * most * rows, sizeof(float2));
+    p.tags = (uint64_t*)take(groups * most, sizeof(uint64_t));
+    // Runs that one sequence may have, and may be taken to have.  The last of them
+    // joins a few (8 sequences of 1500 to 16384 tokens: 26.4 us, with a kernel of its
+    // own 28.5); where a head's parts pass 64 KB one workgroup is too slow for them
+    // (32 runs of 8 rows, D = 128: 60.4 us against 59.5).
+    const int64_t extra = p.runs - batch + 1, byLength = up(up(span, kRunUnit), (int64_t)p.least);
+    const int64_t here = extra < byLength ? extra : byLength, few = up(2 * p.runs, batch);
+    p.joinHere = here <= kJoinHere &&
+                 (here < few ? here : few) * (rows < 16 ? rows : 16) * c.headDim * 4 <= (64 << 10);
     return bytes;
+}
+
+// A number that no other call of this process has, nor one of another whose
+// memory this one may have got (up to 2^-64); not 0.
+uint64_t new_tag()
+{
+    static std::atomic<uint64_t> next{
+        (uint64_t)std::chrono::system_clock::now().time_since_epoch().count() * 0x9E3779B97F4A7C15u ^ (uint64_t)&next};
+    const uint64_t n = next.fetch_add(1, std::memory_order_relaxed);
+    return n != 0 ? n : next.fetch_add(1, std::memory_order_relaxed);
 }
 
 int64_t join_groups(const Plan& p)
 {
-    const int64_t rows = (int64_t)p.pairs * p.rows;
-    return p.splits > kJoinRuns ? rows : (rows + 3) / 4;
+    const int64_t rows = (int64_t)p.rows * p.a.c.batch * p.a.c.heads;
+    return p.runs - p.a.c.batch >= kJoinRuns ? rows : (rows + 3) / 4;
 }
 
 template <int T, int D>
 hipError_t launch(const Plan& p, hipStream_t s)
 {
-    const int64_t groups = (int64_t)p.pairs * p.rowBlocks * p.splits;
+    const int64_t groups = (int64_t)p.a.c.heads * p.rowBlocks * p.runs;
     hipError_t e = enqueue(kv4_k_attend<T, D, 1>, groups, kThreads, s, p);
-    if (e == hipSuccess && p.splits > 1) e = enqueue(kv4_k_join<T>, join_groups(p), kJoinThreads, s, p, D);
+    if (e == hipSuccess && p.runs > p.a.c.batch && !p.joinHere) e = enqueue(kv4_k_join<T>, join_groups(p), kJoinThreads, s, p, D);
     return e;
 }
 
@@ -597,11 +911,13 @@ size_t kv4_attend_bytes(const ccbKv4Cache& c, int32_t headsQ, int32_t nQuery)
 
 bool kv4_attend_fits(const ccbKv4Cache& c, int32_t headsQ, int32_t nQuery, int32_t window, size_t wsBytes)
 {
-    const int64_t pairs = (int64_t)c.batch * c.heads;
-    if (pairs > INT32_MAX) return false;
+    const int64_t pairs = (int64_t)c.batch * c.heads, rows = (int64_t)nQuery * (headsQ / c.heads);
+    if (pairs > INT32_MAX || pairs * rows > INT32_MAX) return false;
     Plan p;
-    return make_plan(p, c, headsQ, nQuery, window, nullptr) <= wsBytes && pairs * p.rows <= INT32_MAX &&
-           kv8_launch_fits(pairs * p.rowBlocks * p.splits, kThreads) && kv8_launch_fits(join_groups(p), kJoinThreads);
+    p.a.c = c;
+    return make_plan(p, c, headsQ, nQuery, window, nullptr) <= wsBytes &&
+           kv8_launch_fits((int64_t)c.heads * p.rowBlocks * p.runs, kThreads) &&
+           kv8_launch_fits(join_groups(p), kJoinThreads);
 }
 
 hipError_t kv4_attend(const Kv4AttendArgs& a, hipStream_t s)
@@ -609,6 +925,7 @@ hipError_t kv4_attend(const Kv4AttendArgs& a, hipStream_t s)
     Plan p;
     p.a = a;
     make_plan(p, a.c, a.headsQ, a.nQuery, a.window, a.ws);
+    p.tag = new_tag();
 #define KV4_ATTEND_DIM(T) \
     switch (a.c.headDim) { \
     case 64: return launch<T, 64>(p, s); \

@@ -47,7 +47,7 @@ typedef struct ccbKv4Cache {
     const int32_t* pageTable; /* [batch][tableStride], the first maxPages of each row in use */
     const int32_t* lens;      /* [batch] */
     int64_t tableStride;      /* >= maxPages */
-    int32_t numPages;
+    int32_t numPages;         /* numPages * heads * pageSize < 2^32 (more than the card's memory holds) */
     int32_t heads;            /* heads of the cache, 1 .. 65536 */
     int32_t pageSize;         /* 16, 32, 64 or 128 */
     int32_t headDim;          /* 64, 96, 128, 192 or 256 */
@@ -100,7 +100,7 @@ CCB_API ccbStatus ccb_kv4_attend(const ccbKv4Cache* cache, const ccbKv8Rows* q,
 /* Bytes of ccb_kv4_attend's workspace, whatever the window (0 for arguments it
  * refuses).  It goes by the capacity, not by the lengths: headDim + 2 floats for
  * each of headsQ / heads * nQuery rows of each run of tokens, of which there are
- * at most max(4096, batch * heads). */
+ * at most batch * heads + 4096, and 8 bytes for every 16 of its rows. */
 CCB_API size_t ccb_kv4_attend_workspace_bytes(const ccbKv4Cache* cache, int32_t headsQ,
                                               int32_t nQuery);
 

@@ -167,6 +167,60 @@ def test_attend_many_sequences(kv4):
     _attend_case(kv4, 7, "bf16", lens, 2, 2, 64, 16)
 
 
+@pytest.mark.parametrize("dtype,heads,group,D,P,lens", [
+    ("bf16", 2, 4, 128, 64, [4000, 100, 0, 2600, 1, 1281, 1280, 900]),          # joined by the last run
+    ("fp16", 4, 4, 256, 64, [5000, 700, 0, 513, 512]),
+    ("bf16", 1, 16, 64, 32, [3000, 3000, 2999]),                                # by a kernel, of rows in waves
+    ("fp16", 1, 20, 96, 16, [20000, 5]),                                        # by a kernel, of rows in workgroups
+    ("fp16", 1, 5, 192, 128, [600 * (i % 7) + i for i in range(64)]),           # as many sequences as a wave has lanes
+    ("bf16", 1, 2, 64, 16, [(977 * i) % 2500 for i in range(65)]),              # one more
+    ("fp16", 1, 1, 128, 64, [3000] + [(13 * i) % 90 for i in range(200)]),      # many, one of them long
+    ("bf16", 2, 3, 256, 128, [9000, 17000] + [3] * 150),                        # more workgroups than CUs
+    ("bf16", 3, 2, 128, 64, [2048] * 16),                                       # all alike
+    ("fp16", 1, 2, 64, 16, [0] * 70 + [1500] + [0] * 5),                        # nearly all empty
+])
+def test_attend_cut_sequences(kv4, dtype, heads, group, D, P, lens):
+    """Sequences cut into runs by all their lengths: every way to find them, and
+    every way to join them."""
+    _say(f"attend cut {dtype} heads={heads} group={group} D={D} batch={len(lens)}")
+    _attend_case(kv4, D + len(lens), dtype, lens, heads, group, D, P)
+
+
+@pytest.mark.parametrize("window,queries", [(1500, 1), (3000, 5), (1400, 30)])
+def test_attend_cut_windows(kv4, window, queries):
+    _say(f"attend cut windows window={window} queries={queries}")
+    _attend_case(kv4, window, "fp16", [4000, 1700, 1, 0, 2999], 1, 2, 128, 32, queries, window)
+
+
+def test_attend_cut_sequences_replayed(kv4):
+    """The joins within the kernel in a captured call: replayed with other
+    lengths, eagerly called on the same workspace between."""
+    rng = np.random.default_rng(25)
+    c = _host(rng, [6000, 6000, 6000], 2, 64, 64)
+    cache = _device(kv4, c)
+    q = torch.from_numpy(rng.normal(0, 1, (3, 1, 8, 64))).half().cuda()
+    out, lse = torch.empty_like(q), torch.empty((3, 1, 8), device="cuda")
+    ws = cache.attend_workspace(8)
+    cache.attend(q, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.attend(q, out=out, lse=lse, workspace=ws)
+    for rep, lens in enumerate(([6000, 6000, 6000], [1, 6000, 0], [5000, 3, 2000], [0, 0, 0], [6000, 5999, 1300])):
+        _say(f"attend cut, replay {rep}")
+        c["lens"][:] = lens
+        cache.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        q.copy_(torch.from_numpy(rng.normal(0, 1, q.shape)).half())
+        torch.cuda.synchronize()
+        for _ in range(3):
+            out.fill_(7)
+            g.replay()
+        torch.cuda.synchronize()
+        _compare(64, "fp16", lens, *oracle.attend(c, q.double().cpu().numpy(), 0.125, 0), out, lse)
+        again = cache.attend(q, workspace=ws)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 @pytest.mark.parametrize("q_size,scale", [(30.0, None), (1.0, 0.0), (1e-3, -2.0), (1.0, -0.3), (1.0, 1e-30),
                                           (300.0, 1e-3)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
