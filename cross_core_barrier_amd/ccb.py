@@ -104,6 +104,7 @@ class ccbKv4Cache(ctypes.Structure):
 
 
 CCB_PAGES_MAX_BATCH = 8192
+CCB_PAGES_STATE_BYTES = 2176
 
 
 class ccbPagePool(ctypes.Structure):

@@ -7,8 +7,15 @@
 // share of the tokens or pages, and finds their sequences by bisection in LDS.
 // What the call changes of its own inputs (lens, count) is written by the
 // workgroup that ends last, when all others have read them: it is the one that
-// finds state at the number of the others, and leaves it at 0.  Small calls are
-// one workgroup.
+// finds the counters of `state` full, and leaves them at 0.  Small calls are one
+// workgroup.
+//
+// What bounds it: latency.  A step of 64 sequences takes 3.6 us (trim) and 6.4
+// (grow), of which 2.5 is the start and the rest a chain of loads: lengths, two
+// sums, a token's sequence, its page.  A million tokens of 1000 sequences take
+// 13.7 us for 17 MB written (3.3 at a copy's rate), 256 prompts of 243,000 tokens
+// 8.7; so many tokens a workgroup that its sums are worth their while, 2048: with
+// 1024 (256 threads) the million took 16.3, with 4096 (1024 threads) 16.6.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -23,9 +30,25 @@ using kv8::report;
 
 constexpr uint32_t kMost = 1u << 30;  // sums stop here: above every size there is
 constexpr int32_t kShortBatch = 1024;
+constexpr int32_t kTeam = 32, kMostGroups = 512;  // workgroups to a counter, and in all
+constexpr int32_t kLineWords = CCB_LINE_BYTES / 4;
+static_assert((1 + kMostGroups / kTeam) * CCB_LINE_BYTES == CCB_PAGES_STATE_BYTES, "a line for each counter");
 
 // a + b for sums that stop at kMost.
 __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return min(a + b, kMost); }
+
+// x summed over the lanes up to this one (without exchanges through LDS, whose
+// latency six times over is a third of a microsecond).
+__device__ __forceinline__ uint32_t scan(uint32_t x)
+{
+    x = add(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xf, 0xf, true));  // 1, 2, 4, 8 lanes before,
+    x = add(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xf, 0xf, true));  // in rows of 16
+    x = add(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xf, 0xf, true));
+    x = add(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xf, 0xf, true));
+    x = add(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xa, 0xf, false));  // the last of a row, to the
+    x = add(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xc, 0xf, false));  // next; of two, to two
+    return x;
+}
 
 // x's sum over the threads before this one, and over all.
 template <int THREADS>
@@ -33,16 +56,10 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t x, uint32_t* scratch, ui
 {
     constexpr int W = THREADS / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t sum = x;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t y = __shfl_up(sum, d, 64);
-        if (lane >= d) sum = add(sum, y);
-    }
+    const uint32_t sum = scan(x);
     __syncthreads();  // the scratch of the sum before
     if (lane == 63) scratch[wave] = sum;
-    uint32_t own = __shfl_up(sum, 1, 64);
-    if (lane == 0) own = 0;
+    uint32_t own = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sum, 0x138, 0xf, 0xf, true);  // the lane before's
     __syncthreads();
     uint32_t before = 0;
     all = 0;
@@ -65,15 +82,22 @@ __device__ __forceinline__ int32_t find(const uint32_t* at, int32_t batch, uint3
     return lo;
 }
 
-// Whether this workgroup is the last to come here; all of its reads are done.
+// Whether this workgroup is the last to come here; all of its reads are done.  In
+// two steps, 32 workgroups to a counter: one address takes 11 ns an arrival, so
+// that 512 at one would take 6 us.
 __device__ __forceinline__ bool last_of_all(int32_t* state, int32_t* flag)
 {
-    if (gridDim.x == 1) return true;
+    const int32_t grid = (int32_t)gridDim.x, me = (int32_t)blockIdx.x;
+    if (grid == 1) return true;
     __syncthreads();
     if (threadIdx.x == 0) {
-        const int32_t before = __hip_atomic_fetch_add(state, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        *flag = before == (int32_t)gridDim.x - 1;
-        if (*flag) __hip_atomic_store(state, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        auto last = [](int32_t* word, int32_t of) {
+            if (__hip_atomic_fetch_add(word, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != of - 1) return false;
+            __hip_atomic_store(word, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            return true;
+        };
+        const int32_t teams = (grid + kTeam - 1) / kTeam, team = me % teams;
+        *flag = last(state + (1 + team) * kLineWords, (grid - team + teams - 1) / teams) && last(state, teams);
     }
     __syncthreads();
     return *flag != 0;
@@ -307,7 +331,7 @@ ccbStatus check(const ccbPagePool* p, const ccbPageTable* t, const int32_t* numb
         return CCB_ERR_INVALID_VALUE;
     if (p->free == nullptr || p->count == nullptr || p->state == nullptr) return CCB_ERR_NULL_POINTER;
     if (t->batch > 0 && (t->pages == nullptr || t->lens == nullptr || numbers == nullptr)) return CCB_ERR_NULL_POINTER;
-    if (!aligned(p->free, 4) || !aligned(p->count, 4) || !aligned(p->state, 4) || !aligned(t->pages, 4) ||
+    if (!aligned(p->free, 4) || !aligned(p->count, 4) || !aligned(p->state, CCB_LINE_BYTES) || !aligned(t->pages, 4) ||
         !aligned(t->lens, 4) || !aligned(numbers, 4) || !aligned(err, 4))
         return CCB_ERR_INVALID_VALUE;
     return CCB_OK;
@@ -342,9 +366,9 @@ CCB_API ccbStatus ccb_pages_trim(const ccbPagePool* pool, const ccbPageTable* ta
     const Pool a = pool_of(pool, table, err);
     const int64_t pages = (int64_t)table->batch * table->maxPages;
     if (table->batch <= kShortBatch)
-        return ccb::launch_status(kv8::enqueue(pages_k_trim<kShortBatch, 256>, groups_for(pages, 8192, 256), 256,
+        return ccb::launch_status(kv8::enqueue(pages_k_trim<kShortBatch, 256>, groups_for(pages, 2048, kMostGroups), 256,
                                                (hipStream_t)stream, a, keep));
-    return ccb::launch_status(kv8::enqueue(pages_k_trim<CCB_PAGES_MAX_BATCH, 1024>, groups_for(pages, 32768, 128),
+    return ccb::launch_status(kv8::enqueue(pages_k_trim<CCB_PAGES_MAX_BATCH, 1024>, groups_for(pages, 16384, kMostGroups),
                                            1024, (hipStream_t)stream, a, keep));
 }
 
@@ -363,10 +387,10 @@ CCB_API ccbStatus ccb_pages_grow(const ccbPagePool* pool, const ccbPageTable* ta
     if ((st = ccb::device_ready()) != CCB_OK) return st;
     const Pool a = pool_of(pool, table, err);
     if (table->batch <= kShortBatch)
-        return ccb::launch_status(kv8::enqueue(pages_k_grow<kShortBatch, 256>, groups_for(maps->tokens, 4096, 512), 256,
+        return ccb::launch_status(kv8::enqueue(pages_k_grow<kShortBatch, 512>, groups_for(maps->tokens, 2048, kMostGroups), 512,
                                                (hipStream_t)stream, a, counts, *maps));
     return ccb::launch_status(kv8::enqueue(pages_k_grow<CCB_PAGES_MAX_BATCH, 1024>,
-                                           groups_for(maps->tokens, 16384, 128), 1024, (hipStream_t)stream, a, counts,
+                                           groups_for(maps->tokens, 4096, kMostGroups), 1024, (hipStream_t)stream, a, counts,
                                            *maps));
 }
 

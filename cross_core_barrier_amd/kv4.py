@@ -28,6 +28,7 @@ from . import ccb
 from .kv8 import _ROWS, OnDevice, _need, _no_gradient
 
 GROUP = 32  # dimensions that share a scale
+_PACKED = {t: kind for t, kind in _ROWS.items() if kind != ccb.CCB_KV8_FP32}
 
 
 class Kv4Cache(OnDevice):
@@ -62,6 +63,7 @@ class Kv4Cache(OnDevice):
         self.heads, self.head_dim, self.batch, self.device = heads, 2 * half, batch, k.device
         self._index = k.get_device()  # -1 on the CPU
         self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._err = self.err.data_ptr()
         self._c = ccb.ccbKv4Cache(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
             lens.data_ptr(), page_table.stride(0) if batch > 1 else max_pages, pages, heads, page_size, 2 * half,
@@ -80,20 +82,15 @@ class Kv4Cache(OnDevice):
         return cls(k, v, ks, vs, table, torch.zeros(batch, dtype=torch.int32, device=device))
 
     def _packed(self, t: torch.Tensor, what: str):
-        kind = _ROWS.get(t.dtype)
-        shape = t.shape
-        if kind is None or kind == ccb.CCB_KV8_FP32 or len(shape) != 3 or shape[1] != self.heads or shape[2] != self.head_dim \
-                or t.get_device() != self._index:
-            kind = None
-        else:
+        kind = _PACKED.get(t.dtype)
+        if kind is not None and t.dim() == 3 and t.get_device() == self._index:
+            n, heads, dim = t.shape
             st, sh, sd = t.stride()
-            if sd != 1 and t.numel() != 0:
-                kind = None
-        if kind is None:
-            raise ValueError(f"{what}: [tokens, heads {self.heads}, head_dim {self.head_dim}] on {self.device}, "
-                             "bfloat16 or float16, the last dimension contiguous")
-        # the stride of a dimension with one place is never used
-        return ccb.ccbKv8Rows(t.data_ptr(), 0, st if shape[0] > 1 else 0, sh if self.heads > 1 else 0, kind, 0)
+            if heads == self.heads and dim == self.head_dim and (sd == 1 or t.numel() == 0):
+                # the stride of a dimension with one place is never used
+                return ccb.ccbKv8Rows(t.data_ptr(), 0, st if n > 1 else 0, sh if heads > 1 else 0, kind, 0)
+        raise ValueError(f"{what}: [tokens, heads {self.heads}, head_dim {self.head_dim}] on {self.device}, "
+                         "bfloat16 or float16, the last dimension contiguous")
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
         """Write tokens k_new, v_new [tokens, heads, head_dim], each to its
@@ -106,11 +103,13 @@ class Kv4Cache(OnDevice):
         if k_new.requires_grad or v_new.requires_grad:
             _no_gradient("k_new, v_new")
         n = k_new.shape[0]
-        _need(n == v_new.shape[0] and k.type == v.type, "v_new: shape and dtype of k_new")
-        _need(slots.shape == (n,) and slots.dtype == torch.int64 and slots.is_contiguous()
-              and slots.get_device() == self._index, f"slots: [{n}] int64, contiguous")
+        if n != v_new.shape[0] or k.type != v.type:
+            raise ValueError("v_new: shape and dtype of k_new")
+        if slots.dtype is not torch.int64 or slots.dim() != 1 or slots.shape[0] != n \
+                or slots.get_device() != self._index or not slots.is_contiguous():
+            raise ValueError(f"slots: [{n}] int64, contiguous, on {self.device}")
         s = None if stream is None else self._enter(stream)
-        self._call(ccb.ccb_kv4_append, s, self._c, k, v, n, slots, self.err)
+        self._call(ccb.ccb_kv4_append, s, self._c, k, v, n, slots, self._err)
 
     def attend_workspace(self, q_heads: int, queries: int = 1) -> torch.Tensor:
         """A workspace for attend() calls of these sizes that follow each other."""
@@ -128,7 +127,8 @@ class Kv4Cache(OnDevice):
         out may be q itself."""
         if self._index < 0:
             self._on_gpu()
-        _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
+        if q.dim() != 4:
+            raise ValueError("q: [batch, queries, q_heads, head_dim]")
         if q.requires_grad:
             _no_gradient("q")
         shape = q.shape
@@ -143,13 +143,15 @@ class Kv4Cache(OnDevice):
             if s is not None:
                 lse.record_stream(s)
         qr, outr = self._rows(q, q_heads, "q"), self._rows(out, q_heads, "out")
-        _need(out.shape[1] == queries and outr.type == qr.type, "out: shape and dtype of q")
-        _need(lse.shape == shape[:3] and lse.dtype == torch.float32 and lse.is_contiguous()
-              and lse.get_device() == self._index, "lse: [batch, queries, q_heads] float32, contiguous")
+        if out.shape[1] != queries or outr.type != qr.type:
+            raise ValueError("out: shape and dtype of q")
+        if lse.shape != shape[:3] or lse.dtype is not torch.float32 or lse.get_device() != self._index \
+                or not lse.is_contiguous():
+            raise ValueError("lse: [batch, queries, q_heads] float32, contiguous")
         need = 0 if workspace is not None else ccb.ccb_kv4_attend_workspace_bytes(self._c, q_heads, queries)
         ws, size = self._space(workspace, need, s)
         self._call(ccb.ccb_kv4_attend, s, self._c, qr, outr, lse, q_heads, queries,
-                   self.head_dim ** -0.5 if scale is None else scale, window, ws, size, self.err)
+                   self.head_dim ** -0.5 if scale is None else scale, window, ws, size, self._err)
         return out, lse
 
     def read(self, count: int, first: Optional[torch.Tensor] = None, dtype=torch.float32, stream=None):
@@ -158,14 +160,16 @@ class Kv4Cache(OnDevice):
         if self._index < 0:
             self._on_gpu()
         kind = _ROWS.get(dtype)
-        _need(kind is not None, "dtype: float32, bfloat16 or float16")
-        self._ints(first, (self.batch,), "first")
+        if kind is None:
+            raise ValueError("dtype: float32, bfloat16 or float16")
+        if first is not None:
+            self._ints(first, (self.batch,), "first")
         s = None if stream is None else self._enter(stream)
         both = torch.empty((2, self.batch, count, self.heads, self.head_dim), dtype=dtype, device=self.device)
         if s is not None:
             both.record_stream(s)
         k, v = both.unbind(0)
-        row = self.heads * self.head_dim
-        self._call(ccb.ccb_kv4_read, s, self._c, ccb.ccbKv8Rows(k.data_ptr(), count * row, row, self.head_dim, kind, 0),
-                   ccb.ccbKv8Rows(v.data_ptr(), count * row, row, self.head_dim, kind, 0), count, first, self.err)
+        row, dim = self.heads * self.head_dim, self.head_dim
+        self._call(ccb.ccb_kv4_read, s, self._c, ccb.ccbKv8Rows(k.data_ptr(), count * row, row, dim, kind, 0),
+                   ccb.ccbKv8Rows(v.data_ptr(), count * row, row, dim, kind, 0), count, first, self._err)
         return k, v

@@ -68,20 +68,15 @@ class OnDevice:
 
     def _rows(self, t: torch.Tensor, heads: int, what: str):
         kind = _ROWS.get(t.dtype)
-        shape = t.shape
-        if kind is None or len(shape) != 4 or shape[0] != self.batch or shape[2] != heads \
-                or shape[3] != self.head_dim or t.get_device() != self._index:
-            kind = None
-        else:
+        if kind is not None and t.dim() == 4 and t.get_device() == self._index:
+            batch, tokens, h, dim = t.shape
             sb, st, sh, sd = t.stride()
-            if sd != 1 and t.numel() != 0:
-                kind = None
-        if kind is None:
-            raise ValueError(f"{what}: [batch {self.batch}, tokens, heads {heads}, head_dim {self.head_dim}] on "
-                             f"{self.device}, bfloat16 or float16, the last dimension contiguous")
-        # the stride of a dimension with one place is never used
-        return ccb.ccbKv8Rows(t.data_ptr(), sb if self.batch > 1 else 0, st if shape[1] > 1 else 0,
-                              sh if heads > 1 else 0, kind, 0)
+            if batch == self.batch and h == heads and dim == self.head_dim and (sd == 1 or t.numel() == 0):
+                # the stride of a dimension with one place is never used
+                return ccb.ccbKv8Rows(t.data_ptr(), sb if batch > 1 else 0, st if tokens > 1 else 0,
+                                      sh if h > 1 else 0, kind, 0)
+        raise ValueError(f"{what}: [batch {self.batch}, tokens, heads {heads}, head_dim {self.head_dim}] on "
+                         f"{self.device}, bfloat16 or float16, the last dimension contiguous")
 
     def _ints(self, t: Optional[torch.Tensor], shape: tuple, what: str):
         if t is not None:

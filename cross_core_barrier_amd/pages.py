@@ -24,6 +24,8 @@ import torch
 from . import ccb
 from .kv8 import OnDevice, _need
 
+_INT = torch.int32
+
 
 class SlotMaps:
     """Where a step's new tokens go, packed sequence after sequence (of the
@@ -68,7 +70,8 @@ class PagePool(OnDevice):
         self.page_size, self.free, self.count, self.device = page_size, free, count, free.device
         self._index = free.get_device()  # -1 on the CPU
         self.err = torch.zeros(1, dtype=torch.int32, device=free.device)
-        self._state = torch.zeros(1, dtype=torch.int32, device=free.device)
+        self._state = torch.zeros(ccb.CCB_PAGES_STATE_BYTES // 4, dtype=torch.int32, device=free.device)
+        self._err = self.err.data_ptr()
         self._c = ccb.ccbPagePool(free.data_ptr(), count.data_ptr(), self._state.data_ptr(), free.shape[0], page_size)
 
     @classmethod
@@ -83,24 +86,28 @@ class PagePool(OnDevice):
               f"maps: up to {ccb.CCB_PAGES_MAX_BATCH} sequences, less than 2^30 tokens")
         return SlotMaps(batch, tokens, self.device)
 
-    def _table(self, page_table: torch.Tensor, lens: torch.Tensor):
-        shape = page_table.shape
-        if len(shape) != 2 or page_table.dtype != torch.int32 or shape[1] < 1 or page_table.stride(1) != 1 \
-                or page_table.get_device() != self._index:
+    def _table(self, page_table: torch.Tensor, lens: torch.Tensor, numbers: torch.Tensor, what: str):
+        """The table as the library takes it.  The checks are few steps on
+        purpose: a call's time on the host is most of a decoding step's."""
+        index = self._index
+        batch, width = page_table.shape if page_table.dim() == 2 else (-1, 0)
+        stride, last = page_table.stride() if batch >= 0 else (0, 0)
+        if batch < 0 or width < 1 or last != 1 or page_table.dtype is not _INT or page_table.get_device() != index:
             raise ValueError(f"page_table: [batch, max_pages] int32 on {self.device}, rows contiguous")
-        self._ints(lens, (shape[0],), "lens")
-        stride = page_table.stride(0) if shape[0] > 1 else shape[1]
-        return ccb.ccbPageTable(page_table.data_ptr(), lens.data_ptr(), stride, shape[0], shape[1])
+        for t in (lens, numbers):
+            if t.dtype is not _INT or t.get_device() != index or t.dim() != 1 or t.shape[0] != batch \
+                    or not t.is_contiguous():
+                raise ValueError(f"{'lens' if t is lens else what}: [{batch}] int32, contiguous, on {self.device}")
+        return ccb.ccbPageTable(page_table.data_ptr(), lens.data_ptr(), stride if batch > 1 else width, batch, width)
 
     def trim(self, page_table: torch.Tensor, lens: torch.Tensor, keep: torch.Tensor, stream=None) -> None:
         """Cut sequence b to its first keep[b] tokens (int32; negative: all stay)
         and take back the pages behind them."""
         if self._index < 0:
             self._on_gpu()
-        table = self._table(page_table, lens)
-        self._ints(keep, lens.shape, "keep")
+        table = self._table(page_table, lens, keep, "keep")
         s = None if stream is None else self._enter(stream)
-        self._call(ccb.ccb_pages_trim, s, self._c, table, keep, self.err)
+        self._call(ccb.ccb_pages_trim, s, self._c, table, keep, self._err)
 
     def grow(self, page_table: torch.Tensor, lens: torch.Tensor, counts: torch.Tensor, maps: SlotMaps,
              stream=None) -> None:
@@ -108,9 +115,8 @@ class PagePool(OnDevice):
         the table, lens, and where each token goes into maps."""
         if self._index < 0:
             self._on_gpu()
-        table = self._table(page_table, lens)
-        self._ints(counts, lens.shape, "counts")
-        _need(maps._batch == lens.shape[0] and maps._index == self._index,
-              "maps: for as many sequences, on the pool's device")
+        table = self._table(page_table, lens, counts, "counts")
+        if maps._batch != table.batch or maps._index != self._index:
+            raise ValueError("maps: for as many sequences, on the pool's device")
         s = None if stream is None else self._enter(stream)
-        self._call(ccb.ccb_pages_grow, s, self._c, table, counts, maps._c, self.err)
+        self._call(ccb.ccb_pages_grow, s, self._c, table, counts, maps._c, self._err)

@@ -38,10 +38,14 @@ extern "C" {
 /* Sequences that a call takes (larger tables go in several calls). */
 #define CCB_PAGES_MAX_BATCH 8192
 
+/* Bytes of a pool's state. */
+#define CCB_PAGES_STATE_BYTES 2176
+
 typedef struct ccbPagePool {
     int32_t* free;    /* [numPages], the first *count of them in use */
     int32_t* count;   /* one: free pages */
-    int32_t* state;   /* one: 0 before the pool's first call, and after each */
+    int32_t* state;   /* CCB_PAGES_STATE_BYTES, 128-B aligned: zeros before the pool's first
+                       * call, and after each */
     int32_t numPages; /* 1 .. 2^30 - 1 */
     int32_t pageSize; /* a power of two, 1 .. 32768 */
 } ccbPagePool;

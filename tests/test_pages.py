@@ -63,7 +63,7 @@ def _maps(ccb, **change):
 
 
 @pytest.mark.parametrize("change", [dict(numPages=0), dict(numPages=1 << 30), dict(pageSize=0), dict(pageSize=24),
-                                    dict(pageSize=65536), dict(free=2), dict(count=2), dict(state=2)], ids=str)
+                                    dict(pageSize=65536), dict(free=2), dict(count=2), dict(state=64)], ids=str)
 def test_refuses_a_bad_pool(ccb, change):
     p, t, numbers = _pool(ccb, **change), _table(ccb), 11 << 20
     assert ccb.ccb_pages_trim(p, t, numbers) == ccb.CCB_ERR_INVALID_VALUE
