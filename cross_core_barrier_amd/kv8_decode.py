@@ -1,6 +1,7 @@
-"""A decoding session on the 8-bit key/value cache, one attention layer deep:
+"""Decoding sessions on the paged key/value caches, one attention layer deep:
 
     python -m cross_core_barrier_amd.kv8_decode --batch 16 --steps 500
+    python -m cross_core_barrier_amd.kv8_decode --batch 16 --steps 500 --format mxfp4
 
 Prompts are written on a stream of their own; a CntNotify counter tells the
 decoding stream when all of them are there.  A step then appends one token for
@@ -9,6 +10,12 @@ into a HIP graph once and replayed.  When a sequence is about to pass its limit
 the cache is cut to the tokens that drew the most weight, into fresh pages, and
 the old pages go back to the pool.  The layer's weights are random; PyTorch does
 the projections.
+
+With the 4-bit cache (mxfp4) requests come and go: one that has reached its limit
+leaves its seat to the next prompt.  Pages are handed out and taken back on the
+GPU, so that the captured step holds the whole of it: pages and slots of the
+step's tokens, append, attention.  A request that finds the pool empty waits with
+its token until another one leaves.
 """
 
 from __future__ import annotations
@@ -19,7 +26,9 @@ import time
 import torch
 
 from . import ccb
+from .kv4 import Kv4Cache
 from .kv8 import Kv8Cache
+from .pages import PagePool
 
 
 class Pages:
@@ -35,6 +44,29 @@ class Pages:
 
     def give(self, pages: list) -> None:
         self.free += pages
+
+
+class Layer:
+    """The weights, and what they make of hidden states."""
+
+    def __init__(self, heads, q_heads, head_dim, dtype, seed):
+        dev = torch.device("cuda")
+        gen = torch.Generator(device=dev).manual_seed(seed)
+        d = q_heads * head_dim
+        n = (q_heads + 2 * heads) * head_dim
+        self.heads, self.q_heads, self.head_dim = heads, q_heads, head_dim
+        self.w_qkv = (torch.randn((d, n), generator=gen, device=dev) / d ** 0.5).to(dtype)
+        self.w_out = (torch.randn((d, d), generator=gen, device=dev) / d ** 0.5).to(dtype)
+
+    def project(self, x: torch.Tensor):
+        """x [..., d] as queries, keys and values [..., heads, head_dim]."""
+        qkv = (x @ self.w_qkv).unflatten(-1, (-1, self.head_dim))
+        return qkv.split([self.q_heads, self.heads, self.heads], dim=-2)
+
+    def output(self, out: torch.Tensor) -> torch.Tensor:
+        """Attention's results [batch, 1, q_heads, head_dim] as the next hidden states."""
+        y = out.flatten(1) @ self.w_out
+        return y / (y.float().square().mean(-1, keepdim=True) + 1e-6).sqrt().to(y.dtype)
 
 
 class Session:
@@ -58,12 +90,9 @@ class Session:
                             torch.zeros((batch, heads, self.out_width * page_size), device=dev))
         self.held = [[] for _ in range(batch)]  # pages of each sequence, on the host
         self.lens = [0] * batch
-        gen = torch.Generator(device=dev).manual_seed(seed)
-        d = q_heads * head_dim
-        n = (q_heads + 2 * heads) * head_dim
-        self.w_qkv = (torch.randn((d, n), generator=gen, device=dev) / d ** 0.5).to(dtype)
-        self.w_out = (torch.randn((d, d), generator=gen, device=dev) / d ** 0.5).to(dtype)
-        self.x = torch.zeros((batch, d), dtype=dtype, device=dev)  # a step's input and output
+        self.layer = Layer(heads, q_heads, head_dim, dtype, seed)
+        self.project, self.w_qkv, self.w_out = self.layer.project, self.layer.w_qkv, self.layer.w_out
+        self.x = torch.zeros((batch, q_heads * head_dim), dtype=dtype, device=dev)  # a step's input and output
         self.attend_ws = self.cache.attend_workspace(q_heads, 1, accumulate=True)
         self.evict_ws = self.cache.evict_workspace(budget)
         self.graph = None
@@ -79,11 +108,6 @@ class Session:
                 self.held[b] += self.pages.take(more)
                 self.cache.page_table[b, first:first + more] = torch.tensor(self.held[b][first:], dtype=torch.int32)
         self.lens = list(lens)
-
-    def project(self, x: torch.Tensor):
-        """x [batch, tokens, d] as queries, keys and values [batch, tokens, heads, head_dim]."""
-        qkv = (x @ self.w_qkv).unflatten(-1, (-1, self.head_dim))
-        return qkv.split([self.q_heads, self.heads, self.heads], dim=2)
 
     def prefill(self, prompts: list) -> None:
         """Write prompts [tokens, d], one for each sequence."""
@@ -115,8 +139,7 @@ class Session:
         self.cache.lens.add_(1)
         self.cache.append(k, v)
         out, _ = self.cache.attend(q, accumulate=True, workspace=self.attend_ws)
-        y = out.flatten(1) @ self.w_out
-        self.x.copy_(y / (y.float().square().mean(-1, keepdim=True) + 1e-6).sqrt().to(y.dtype))
+        self.x.copy_(self.layer.output(out))
 
     def _evict(self) -> None:
         """Cut every sequence to the budget, into pages of its own."""
@@ -170,6 +193,134 @@ class Session:
         self.cache.lens.copy_(lens)
 
 
+class PooledSession:
+    """Seats for requests on a 4-bit cache, whose pages the GPU hands out."""
+
+    def __init__(self, batch=4, heads=8, q_heads=32, head_dim=128, page_size=64, limit=2048, pages=None,
+                 dtype=torch.bfloat16, seed=0):
+        dev = torch.device("cuda")
+        width = -(-limit // page_size)
+        pages = batch * width if pages is None else pages
+        if pages < width:
+            raise ValueError(f"pages {pages}: one request may need {width}")
+        self.batch, self.limit = batch, limit
+        self.layer = Layer(heads, q_heads, head_dim, dtype, seed)
+        self.cache = Kv4Cache.allocate(pages, heads, page_size, head_dim, batch, width)
+        self.pool = PagePool.allocate(pages, page_size)
+        self.maps = self.pool.maps(batch, batch)  # of a step
+        self.workspace = self.cache.attend_workspace(q_heads)
+        self.x = torch.zeros((batch, q_heads * head_dim), dtype=dtype, device=dev)  # a step's input and output
+        self.asks = torch.zeros(batch, dtype=torch.int32, device=dev)  # tokens that a step adds: 1 where somebody sits
+        self.graph = None
+
+    def _numbers(self, seats, fill: int, value) -> torch.Tensor:
+        x = [fill] * self.batch
+        for i, seat in enumerate(seats):
+            x[seat] = value[i] if isinstance(value, list) else value
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def leave(self, seats: list) -> None:
+        """Requests that end: their pages go back."""
+        self.pool.trim(self.cache.page_table, self.cache.lens, self._numbers(seats, -1, 0))
+        self.asks[seats] = 0
+
+    def sit(self, seats: list, prompts: list) -> list:
+        """Prompts [tokens, d] for free seats.  Returns the seats that got pages;
+        the others stay free.  Waits for the device."""
+        lens = [p.shape[0] for p in prompts]
+        if len(lens) != len(seats) or len(set(seats)) != len(seats) or not all(1 <= n <= self.limit for n in lens):
+            raise ValueError(f"prompts: one for each seat, of 1 to {self.limit} tokens")
+        order = sorted(range(len(seats)), key=lambda i: seats[i])  # as the new tokens are numbered
+        rows = torch.cat([prompts[i] for i in order])
+        maps = self.pool.maps(self.batch, rows.shape[0])
+        self.pool.grow(self.cache.page_table, self.cache.lens, self._numbers(seats, 0, lens), maps)
+        _, k, v = self.layer.project(rows)
+        self.cache.append(k, v, maps.slots)
+        granted = maps.granted.tolist()
+        sat = [i for i in order if granted[seats[i]] > 0]
+        for i in sat:
+            self.x[seats[i]] = prompts[i][-1]
+            self.asks[seats[i]] = 1
+        return [seats[i] for i in sat]
+
+    def _step(self) -> None:
+        q, k, v = self.layer.project(self.x[:, None])
+        self.pool.grow(self.cache.page_table, self.cache.lens, self.asks, self.maps)
+        # the step's tokens stand one behind the other: seats that ask for none are left out
+        of = self.maps.sequences.clamp(min=0).long()
+        self.cache.append(k[of, 0], v[of, 0], self.maps.slots)
+        out, _ = self.cache.attend(q, workspace=self.workspace)
+        # (a token that got no page comes again)
+        self.x.copy_(torch.where(self.maps.granted.unsqueeze(1) > 0, self.layer.output(out), self.x))
+
+    def step(self, graph: bool = True) -> torch.Tensor:
+        """One token more for every request; returns the layer's output."""
+        if not graph:
+            self._step()
+        else:
+            if self.graph is None:
+                self._capture()
+            self.graph.replay()
+        return self.x
+
+    def _capture(self) -> None:
+        """Capture the step.  The run outside the capture that this needs is
+        made with nobody asking for a token, which changes nothing."""
+        x, asks = self.x.clone(), self.asks.clone()
+        self.asks.zero_()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            self._step()
+        torch.cuda.current_stream().wait_stream(side)
+        self.graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(self.graph):
+            self._step()
+        self.x.copy_(x)
+        self.asks.copy_(asks)
+
+
+def serve(a) -> None:
+    """Requests on the 4-bit cache: prompts of unlike lengths, each decoded to the limit."""
+    s = PooledSession(batch=a.batch, limit=a.limit)
+    d = s.x.shape[1]
+    waiting = [torch.randn((max(1, a.prompt - 37 * (b % a.batch)), d), device="cuda", dtype=s.x.dtype)
+               for b in range(2 * a.batch)]
+    left = [0] * a.batch  # tokens until a seat's request is at its limit; 0: nobody sits there
+    served = tokens = 0
+
+    def fill() -> None:
+        free = [b for b in range(a.batch) if left[b] == 0][:len(waiting)]
+        if free:
+            prompts = [waiting.pop(0) for _ in free]
+            for b in s.sit(free, prompts):  # (the pool has pages for every seat)
+                left[b] = a.limit - prompts[free.index(b)].shape[0]
+
+    def step() -> tuple:
+        s.step(not a.eager)
+        ended = [b for b in range(a.batch) if left[b] == 1]
+        busy = sum(n > 0 for n in left)
+        left[:] = [max(0, n - 1) for n in left]
+        if ended:
+            s.leave(ended)
+            fill()
+        return busy, len(ended)
+    fill()
+    step()
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    for _ in range(a.steps - 1):
+        busy, ended = step()
+        tokens, served = tokens + busy, served + ended
+    torch.cuda.synchronize()
+    t = time.perf_counter() - t
+    s.cache.check()
+    s.pool.check()
+    print(f"{a.batch} seats, {a.steps} steps, {served} requests ended: {t / max(1, a.steps - 1) * 1e6:.1f} us a step, "
+          f"{tokens / t:.0f} tokens/s; lengths now {min(s.cache.lens.tolist())} to {max(s.cache.lens.tolist())}")
+
+
 def main(argv=None) -> None:
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--batch", type=int, default=16)
@@ -177,9 +328,12 @@ def main(argv=None) -> None:
     ap.add_argument("--prompt", type=int, default=1800)
     ap.add_argument("--limit", type=int, default=2048)
     ap.add_argument("--budget", type=int, default=512)
-    ap.add_argument("--format", choices=["int8", "e4m3"], default="e4m3")
+    ap.add_argument("--format", choices=["int8", "e4m3", "mxfp4"], default="e4m3")
     ap.add_argument("--eager", action="store_true", help="no HIP graph")
     a = ap.parse_args(argv)
+    if a.format == "mxfp4":
+        serve(a)
+        return
     s = Session(batch=a.batch, limit=a.limit, budget=a.budget, fmt=a.format)
     d = s.x.shape[1]
     # prompts of unlike lengths

@@ -603,3 +603,79 @@ def test_an_error_left_by_another_call_is_not_reported(kv4):
     assert ccb.ccb_bench_copy(q, q, -1) != 0
     out, _ = cache.attend(q)
     assert torch.isfinite(out).all()
+
+
+def _session(graph, pages=None, limit=40):
+    """A session driven through arrivals, ends and shortages; what it ends in."""
+    from cross_core_barrier_amd.kv8_decode import PooledSession
+    s = PooledSession(batch=4, heads=2, q_heads=6, head_dim=64, page_size=16, limit=limit, pages=pages, seed=3)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    prompt = lambda n: torch.randn((n, s.x.shape[1]), generator=gen, device="cuda").to(s.x.dtype)  # noqa: E731
+    log = [s.sit([2, 0, 3], [prompt(20), prompt(1), prompt(33)])]
+    for i in range(12):
+        s.step(graph)
+        if i == 4:
+            s.leave([3])
+            log.append(s.sit([1, 3], [prompt(30), prompt(17)]))
+        if i == 8:
+            s.leave([0])
+    torch.cuda.synchronize()
+    s.cache.check()
+    s.pool.check()
+    # every page is in the pool, or held once
+    held = [p for b, n in enumerate(s.cache.lens.tolist()) for p in s.cache.page_table[b, :-(-n // 16)].tolist()]
+    free = s.pool.free[:s.pool.count.item()].tolist()
+    assert sorted(held + free) == list(range(s.cache.k.shape[0]))
+    return s, log, gen
+
+
+@pytest.mark.parametrize("pages", [None, 6])
+def test_pooled_session(kv4, pages):
+    """Requests that come and go, with pages for everybody and with too few:
+    replayed from a graph and made eagerly the session ends in the same bits, and
+    its attention is the oracle's over what the cache holds."""
+    ends = []
+    for graph in (True, False):
+        _say(f"pooled session pages={pages} graph={graph}")
+        s, log, gen = _session(graph, pages)
+        ends.append((s.x.clone(), s.cache.lens.clone(), s.pool.free.clone(), *s.cache.read(48)))
+        if pages is None:
+            assert log == [[0, 2, 3], [1, 3]] and s.cache.lens.tolist() == [0, 37, 32, 24]
+        else:  # 1 + 2 + 3 pages, and then 3 of them for the two that come: the second has to wait
+            assert log[0] == [0, 2, 3] and log[1] == [1]
+    assert all(torch.equal(a, b) for a, b in zip(*ends))
+    q = torch.randn((4, 1, 6, 64), generator=gen, device="cuda").half()
+    c = dict(lens=s.cache.lens.cpu().numpy(), table=s.cache.page_table.cpu().numpy(), k=s.cache.k.cpu().numpy(),
+             v=s.cache.v.cpu().numpy(), ks=s.cache.k_scale.cpu().numpy(), vs=s.cache.v_scale.cpu().numpy())
+    want = oracle.attend(c, q.double().cpu().numpy(), 0.125, 0)
+    _compare(64, "fp16", c["lens"].tolist(), *want, *s.cache.attend(q))
+
+
+def test_pooled_session_waits_for_pages(kv4):
+    """A request whose next page is not there stays at its token until another
+    one leaves."""
+    from cross_core_barrier_amd.kv8_decode import PooledSession
+    _say("pooled session: a token that waits")
+    s = PooledSession(batch=2, heads=1, q_heads=2, head_dim=64, page_size=16, limit=64, pages=4, seed=4)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    rows = torch.randn((64, 128), generator=gen, device="cuda").to(s.x.dtype)
+    assert s.sit([0, 1], [rows[:31], rows[:30]]) == [0, 1]
+    s.step()
+    s.step()  # both at the end of their second page, the second in its last place
+    assert s.cache.lens.tolist() == [32, 32]
+    x = s.x.clone()
+    s.step()
+    assert s.cache.lens.tolist() == [32, 32] and torch.equal(s.x, x)
+    s.leave([1])
+    s.step()
+    assert s.cache.lens.tolist() == [33, 0] and not torch.equal(s.x[0], x[0])
+    s.pool.check()
+
+
+def test_decode_command_serves_requests(kv4, capsys):
+    from cross_core_barrier_amd import kv8_decode
+    _say("kv8_decode --format mxfp4")
+    kv8_decode.main(["--batch", "3", "--steps", "30", "--prompt", "90", "--limit", "100", "--format", "mxfp4"])
+    # prompts of 90, 53, 16, 90, 53, 16 tokens, to 100 each: the first seat's ends after 10 steps, and after 20
+    out = capsys.readouterr().out
+    assert "3 seats, 30 steps, 2 requests ended" in out and "lengths now 46 to 83" in out

@@ -260,3 +260,15 @@ def test_class_checks_its_rows(cpu_cache, monkeypatch):
     c.append(x[:0], x[:0], slots[:0])
     c.read(5)
     assert reached == ["append", "attend", "append", "append", "read"]
+
+
+def test_session_refuses_what_does_not_fit():
+    """Before any page is taken."""
+    from cross_core_barrier_amd.kv8_decode import PooledSession
+    with pytest.raises(ValueError):
+        PooledSession(batch=2, limit=100, page_size=16, pages=6)  # 7 for one request
+    s = PooledSession.__new__(PooledSession)  # the checks need no device
+    s.batch, s.limit = 3, 96
+    for seats, lens in (([0], [97]), ([0], [0]), ([0, 1], [5]), ([1, 1], [5, 5])):
+        with pytest.raises(ValueError):
+            s.sit(seats, [torch.zeros((n, 64)) for n in lens])
