@@ -527,6 +527,9 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
         for (int d = 0; d < NB; ++d) o[nt][d] = f4{0, 0, 0, 0};
     }
 
+    // Whether a maximum has passed 2^20: what the product's rounding adds to the
+    // maximum, 2^-24 of it, would no longer be small as an exponent.
+    bool loud = false;
     const uint32_t laneCodes = Half<D>::codes_at(n, g);
     const uint32_t laneScale0 = Half<D>::scale_at(n, g, 0), laneScale1 = Half<D>::scale_at(n, g, D / 32 - 1);
     // where this lane reads values: 4 lanes for a token's 16 dimensions
@@ -593,9 +596,11 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
             // number of loads in flight is the same in every step)
             const int32_t next = i + 1 < nTiles ? i + 1 : i;
             load(next, c.k, c.kScale, key);
+            // Scores are multiplied by `by` where the maximum is subtracted, in one
+            // rounding; or before.
             float by = scale2;
             bool grows = false;
-            if (!whole) {
+            if (!whole || loud) {
                 asm volatile("");  // a branch: its instructions would be a third of the step's
                 by = 1.0f;
 #pragma unroll
@@ -651,6 +656,12 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
                     l[nt] *= f;
 #pragma unroll
                     for (int d = 0; d < NB; ++d) o[nt][d] *= f;
+                    loud |= __any(fabsf(ref[nt]) > 0x1p20f) != 0;
+                }
+                if (loud) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) s[nt][0] *= by, s[nt][1] *= by;
+                    by = 1.0f;
                 }
             }
             u4 ph[NT], pl[NT];

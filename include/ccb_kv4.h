@@ -57,7 +57,7 @@ typedef struct ccbKv4Cache {
 
 /* Write new tokens: row i of kNew and vNew becomes the token at slots[i] (page
  * slots[i] / pageSize, slot slots[i] % pageSize); a row with slot -1 is left
- * out.  For each head and each 32 dimensions of a row, with a the largest
+ * out (and every row, where the cache's batch is 0).  For each head and each 32 dimensions of a row, with a the largest
  * finite |x| among them: e is the least whole number with a <= 7 * 2^e, at
  * least -64 and at most 125; the scale is e + 127; a code is x / 2^e rounded
  * once to e2m1 (half to even), saturated at +-6 (with this e nothing that is

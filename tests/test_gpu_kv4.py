@@ -229,6 +229,14 @@ def test_attend_score_ranges(kv4, dtype, q_size, scale):
     _attend_case(kv4, 8, dtype, [300, 40, 1], 2, 3, 128, 32, 2, q_size=q_size, scale=scale)
 
 
+@pytest.mark.parametrize("q_size", [1e-30, 1e8, 1e12, 1e30])
+@pytest.mark.parametrize("lens", [[300, 2], [2600, 700, 33]])
+def test_attend_bf16_range(kv4, q_size, lens):
+    """Scores far beyond what a weight's exponent holds, and far below."""
+    _say(f"attend q_size={q_size} lens={lens}")
+    _attend_case(kv4, 26, "bf16", lens, 1, 2, 64, 16, q_size=q_size)
+
+
 @pytest.mark.parametrize("low,high", [(63, 64), (64, 190), (127, 160)])
 def test_attend_scale_ranges(kv4, low, high):
     """Scales of unlike size side by side: loud and silent groups."""
