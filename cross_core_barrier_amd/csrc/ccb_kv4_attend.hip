@@ -35,6 +35,7 @@
 // transposed reads at once changed little or cost (24.5 us against 26.2, 23.5,
 // 26.6 and 25.0; 16 waves take 19.6 us against 14.6 for 200 short sequences).
 
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -56,7 +57,6 @@ constexpr int kRunUnit = kWaves * kTile;
 constexpr int kSegment = 32 * kRunUnit;  // tokens whose pages fit a wave's lanes
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr uint32_t kNone = 0xffffffffu;
 constexpr int kJoinHere = 64;    // runs that the last of them may join, at most
 constexpr int kJoinRuns = 32;   // more of them are joined by a workgroup, not a wave
 constexpr float kSlack = 8.0f;  // how far (in powers of two) scores may pass the running maximum
@@ -104,6 +104,7 @@ __device__ __forceinline__ void pieces(float a, float b, uint32_t& hi, uint32_t&
 {
     const bf2 h = {(__bf16)a, (__bf16)b};
     hi = __builtin_bit_cast(uint32_t, h);
+    asm("" : "+v"(hi));  // (or the compiler rounds a once more to have it by itself)
     const bf2 l = {(__bf16)(a - of_bits(hi << 16)), (__bf16)(b - of_bits(hi & 0xffff0000u))};
     lo = __builtin_bit_cast(uint32_t, l);
 }
@@ -432,7 +433,7 @@ struct Half {
 };
 
 template <int T, int D, int NT>
-__global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
+__global__ __launch_bounds__(kThreads, D < 128 || (D == 128 && T == CCB_KV8_BF16) ? 4 : 2) void kv4_k_attend(Plan p)
 {
     constexpr int NB = D / 16;                          // blocks of 16 dimensions
     constexpr int NJ = D / 32;                          // steps of the first product
@@ -516,13 +517,16 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
         const int32_t last = row0 + 16 * NT < p.rows ? row0 + 16 * NT - 1 : p.rows - 1;
         seen_by(a, r, last, p.rows, group, allBegin, unused);
         seen_by(a, r, row0, p.rows, group, unused, allEnd);
+        allBegin = __builtin_amdgcn_readfirstlane(allBegin), allEnd = __builtin_amdgcn_readfirstlane(allEnd);
     }
 
     f4 o[NT][NB];
-    float m[NT], ref[NT], l[NT];
+    // What weights are relative to, a maximum that scores may pass by kSlack; the
+    // lowest float for a row that has seen nothing (less it, every score grows).
+    float ref[NT], l[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        m[nt] = -INFINITY, ref[nt] = 0.0f, l[nt] = 0.0f;
+        ref[nt] = -FLT_MAX, l[nt] = 0.0f;
 #pragma unroll
         for (int d = 0; d < NB; ++d) o[nt][d] = f4{0, 0, 0, 0};
     }
@@ -540,17 +544,21 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
 
     for (int32_t seg = lo; seg < hi; seg += kSegment) {
         const int32_t segEnd = hi - seg < kSegment ? hi : seg + kSegment;
-        // lane i holds the first row of the wave's i-th half tile, among all of the
-        // cache's (less than 2^32 - 1), or kNone
-        uint32_t rows = kNone;
+        // Lane i holds the first row of the wave's i-th half tile, among all of the
+        // cache's (less than 2^32).  Bit i of `held` is clear where that page is
+        // unseen: page 0 is loaded in its place, and not used.
+        uint32_t rows = 0;
+        bool seen = false;
         {
             const int32_t t = seg + laneAt;
             if (t < segEnd && t + 16 > r.first) {
                 const int32_t page = checked_page(early && seg == lo ? entry : table[t >> shift], c.numPages);
-                if (page < 0) report(a.err);
+                seen = page >= 0;
+                if (!seen) report(a.err);
                 else rows = ((((uint32_t)page * (uint32_t)c.heads) + (uint32_t)h) << shift) + ((uint32_t)t & (uint32_t)(P - 1));
             }
         }
+        const uint64_t held = __ballot(seen);
         const int32_t nTiles = ((segEnd - seg + kTile - 1) / kTile - wave + kWaves - 1) / kWaves;
 
         auto load = [&](int32_t i, const uint8_t* codes, const uint8_t* scales, Half<D>(&x)[2]) {
@@ -559,8 +567,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
             asm("" : "+v"(codesAt), "+v"(scaleAt0), "+v"(scaleAt1));
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                uint32_t row = (uint32_t)__builtin_amdgcn_readlane((int32_t)rows, 2 * i + half);
-                row = row == kNone ? 0 : row;  // an unseen page's place: page 0 is loaded and not used
+                const uint32_t row = (uint32_t)__builtin_amdgcn_readlane((int32_t)rows, 2 * i + half);
                 x[half].load(codes, scales, row, codesAt, scaleAt0, scaleAt1);
             }
         };
@@ -568,9 +575,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
         Half<D> key[2], val[2];
         auto step = [&](int32_t i) {
             const int32_t t0 = seg + (i * kWaves + wave) * kTile;
-            const bool there0 = (uint32_t)__builtin_amdgcn_readlane((int32_t)rows, 2 * i) != kNone;
-            const bool there1 = (uint32_t)__builtin_amdgcn_readlane((int32_t)rows, 2 * i + 1) != kNone;
-            const bool whole = t0 >= allBegin && t0 + kTile <= allEnd && there0 && there1;
+            const uint32_t pair = (uint32_t)(held >> (2 * i)) & 3u;
+            const bool whole = t0 >= allBegin && t0 + kTile <= allEnd && pair == 3u;
             // scores
             f4 s[NT][2];
             {
@@ -603,6 +609,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
             if (!whole || loud) {
                 asm volatile("");  // a branch: its instructions would be a third of the step's
                 by = 1.0f;
+                const bool there0 = (pair & 1u) != 0, there1 = (pair & 2u) != 0;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -638,44 +645,53 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
 #pragma unroll
             for (int d = 0; d < NR; ++d) value[d] = transposed(d);
             __builtin_amdgcn_sched_barrier(0);
-            float mx[NT];
+            f4 y[NT][2];  // exponents, then weights
+            auto exponents = [&](int nt) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[nt][half][e] = fmaf(s[nt][half][e], by, -ref[nt]);
+            };
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                mx[nt] = fmaxf(fmaxf(s[nt][0].x, s[nt][0].y), fmaxf(s[nt][0].z, s[nt][0].w));
-                mx[nt] = fmaxf(mx[nt], fmaxf(fmaxf(s[nt][1].x, s[nt][1].y), fmaxf(s[nt][1].z, s[nt][1].w))) * by;
-                grows |= mx[nt] > m[nt] + kSlack;
+                exponents(nt);
+                const float x = fmaxf(fmaxf(y[nt][0].x, y[nt][0].y), fmaxf(y[nt][0].z, y[nt][0].w));
+                grows |= fmaxf(x, fmaxf(fmaxf(y[nt][1].x, y[nt][1].y), fmaxf(y[nt][1].z, y[nt][1].w))) > kSlack;
             }
             if (__any(grows)) {  // a new maximum, for the row's four lanes alike
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float top = fmaxf(mx[nt], __shfl_xor(mx[nt], 16, 64));
-                    top = fmaxf(m[nt], fmaxf(top, __shfl_xor(top, 32, 64)));
-                    ref[nt] = top == -INFINITY ? 0.0f : top;
-                    const float f = exp2_(m[nt] - ref[nt]);
-                    m[nt] = top;
+                    float top = fmaxf(fmaxf(s[nt][0].x, s[nt][0].y), fmaxf(s[nt][0].z, s[nt][0].w));
+                    top = fmaxf(top, fmaxf(fmaxf(s[nt][1].x, s[nt][1].y), fmaxf(s[nt][1].z, s[nt][1].w))) * by;
+                    top = fmaxf(top, __shfl_xor(top, 16, 64));
+                    top = fmaxf(ref[nt], fmaxf(top, __shfl_xor(top, 32, 64)));
+                    const float f = exp2_(ref[nt] - top);
+                    ref[nt] = top;
                     l[nt] *= f;
 #pragma unroll
                     for (int d = 0; d < NB; ++d) o[nt][d] *= f;
-                    loud |= __any(fabsf(ref[nt]) > 0x1p20f) != 0;
+                    loud |= __ballot(fabsf(top) > 0x1p20f && top != -FLT_MAX) != 0;
                 }
                 if (loud) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) s[nt][0] *= by, s[nt][1] *= by;
                     by = 1.0f;
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) exponents(nt);
             }
             u4 ph[NT], pl[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    f4 y;
+                    f4 p;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = exp2_(fmaf(s[nt][half][e], by, -ref[nt]));
-                    l[nt] += (y.x + y.y) + (y.z + y.w);
+                    for (int e = 0; e < 4; ++e) p[e] = exp2_(y[nt][half][e]);
+                    l[nt] += (p.x + p.y) + (p.z + p.w);
                     uint32_t h0, l0, h1, l1;
-                    pieces(y.x, y.y, h0, l0);
-                    pieces(y.z, y.w, h1, l1);
+                    pieces(p.x, p.y, h0, l0);
+                    pieces(p.z, p.w, h1, l1);
                     ph[nt][2 * half] = h0, ph[nt][2 * half + 1] = h1;
                     pl[nt][2 * half] = l0, pl[nt][2 * half + 1] = l1;
                 }
@@ -711,7 +727,8 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
     for (int nt = 0; nt < NT; ++nt) {
         l[nt] += __shfl_xor(l[nt], 16, 64);
         l[nt] += __shfl_xor(l[nt], 32, 64);
-        if (g == 0) sm[wave][nt * 16 + n] = m[nt], sl[wave][nt * 16 + n] = l[nt];
+        if (l[nt] == 0.0f) ref[nt] = -INFINITY;
+        if (g == 0) sm[wave][nt * 16 + n] = ref[nt], sl[wave][nt * 16 + n] = l[nt];
     }
     __syncthreads();
     const int64_t part = ((int64_t)h * p.runs + number) * p.rows;
@@ -720,7 +737,7 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_k_attend(Plan p)
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][nt * 16 + n]);
-        const float f = l[nt] == 0.0f ? 0.0f : exp2_(m[nt] - top);  // (a NaN stays)
+        const float f = l[nt] == 0.0f ? 0.0f : exp2_(ref[nt] - top);  // (a NaN stays)
         // chunks of 4 dimensions are swapped so that rows fall on different banks
         float* dst = (float*)vBuf[wave] + n * D;
 #pragma unroll
