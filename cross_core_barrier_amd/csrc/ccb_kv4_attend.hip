@@ -25,7 +25,7 @@
 // instructions less a tile and was 2% faster: 24.3 us against 24.9 for 32
 // sequences of 100 to 4096 tokens, too little for what it loses.)
 //
-// What bounds it.  A tile of 32 tokens (D = 128) costs a wave about 260
+// What bounds it.  A tile of 32 tokens (D = 128) costs a wave about 250
 // instructions for 4352 bytes, which a workgroup of 8 waves gets through in 1.1
 // us: large even calls are bound by memory (64 sequences of 16384 tokens: 1.13 GB
 // in 198 us, 5.7 TB/s), a long sequence on its own workgroup by the issue of
@@ -433,13 +433,16 @@ struct Half {
 };
 
 template <int T, int D, int NT>
-__global__ __launch_bounds__(kThreads, D < 128 || (D == 128 && T == CCB_KV8_BF16) ? 4 : 2) void kv4_k_attend(Plan p)
+// (two workgroups a CU where the registers suffice)
+__global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16) ? 4 : 2) void kv4_k_attend(Plan p)
 {
     constexpr int NB = D / 16;                          // blocks of 16 dimensions
     constexpr int NJ = D / 32;                          // steps of the first product
     constexpr int NQ = T == CCB_KV8_BF16 ? 1 : 2;       // bf16 pieces of a query: exact
-    // A token's values in LDS, and 32 bytes more: the 8 tokens that half a wave
-    // reads 16 dimensions of fall on all the banks, and so do 8 writes of 16 bytes.
+    // A token's values in LDS, and 32 bytes more: the 4 tokens that a quarter of a
+    // wave reads 16 dimensions of fall on all the banks.  Writes meet in pairs (64
+    // cycles a tile of 160 in all); to swap two pieces in every other four lanes
+    // takes that away for 8 instructions more, and 25.3 us instead of 24.1.
     constexpr int S = 2 * D + 32;
     __shared__ __attribute__((aligned(16))) uint8_t vBuf[kWaves][kTile * S];
     __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT];
