@@ -49,15 +49,15 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kThreads = 512;                  // of a workgroup that takes a run of tokens
+constexpr int kThreads = 512;  // of a workgroup that takes a run of tokens
 constexpr int kWaves = kThreads / 64;
 constexpr int kJoinThreads = 256;
-constexpr int kTile = 32;                     // tokens of a wave's step
+constexpr int kTile = 32;                // tokens of a wave's step
 constexpr int kRunUnit = kWaves * kTile;
 constexpr int kSegment = 32 * kRunUnit;  // tokens whose pages fit a wave's lanes
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kJoinHere = 64;    // runs that the last of them may join, at most
+constexpr int kJoinHere = 64;   // runs that the last of them may join, at most
 constexpr int kJoinRuns = 32;   // more of them are joined by a workgroup, not a wave
 constexpr float kSlack = 8.0f;  // how far (in powers of two) scores may pass the running maximum
 
@@ -70,17 +70,17 @@ typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
 struct Plan {
     ccb::Kv4AttendArgs a;
-    int32_t rows;       // of a cache head
-    int32_t rowBlocks;  // workgroups that share a run of tokens
-    int32_t runs;       // of a head, over all sequences, at most: see chunk_of
-    int32_t whole;      // units of a sequence that is one run
-    float least;        // units of a run, at least
-    float lowBy, highBy;  // about 1 / runs and 1 / (runs - sequences): see place_of
-    bool joinHere;      // the run that ends last joins a sequence's, else another kernel
-    float* partO;       // [head][run][row][D], of sequences with several runs
-    float2* partML;     // [head][run][row]: maximum (base 2) and sum
-    uint64_t* tags;     // [head][rowBlock][run]: see join_here
-    uint64_t tag;
+    int32_t rows;         // of a cache head
+    int32_t rowBlocks;    // workgroups that share a run of tokens
+    int32_t runs;         // of a head, over all sequences, at most: see place_of
+    int32_t whole;        // units of a sequence that is one run
+    float least;          // units of a run, at least
+    float lowBy, highBy;  // about 1 / runs and 1 / (runs - sequences)
+    bool joinHere;        // the run that ends last joins a sequence's, else another kernel
+    float* partO;         // [head][run][row][D], of sequences with several runs
+    float2* partML;       // [head][run][row]: maximum (base 2) and sum
+    uint64_t* tags;       // [head][rowBlock][run]: see join_here
+    uint64_t tag;         // of this call
 };
 
 __device__ __forceinline__ f4 mfma(const u4& a, const u4& b, const f4& c)

@@ -262,6 +262,40 @@ def test_class_checks_its_rows(cpu_cache, monkeypatch):
     assert reached == ["append", "attend", "append", "append", "read"]
 
 
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """The entry points act on the current device: the classes make their own
+    current for the call, and leave it alone where it is already."""
+    import contextlib
+    from cross_core_barrier_amd import ccb, kv4, kv8, pages
+    current, where = [0], []
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+    for name in ("kv4_append", "kv4_attend", "kv4_read", "pages_trim", "pages_grow"):
+        def entry(*a):
+            where.append(current[0])
+            return 0
+        monkeypatch.setattr(ccb, f"ccb_{name}", entry)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(kv8, "_current_device", lambda: current[0])
+    monkeypatch.setattr(kv8, "_current_stream", lambda index: 0)
+    for cls in (kv4.Kv4Cache, pages.PagePool):
+        monkeypatch.setattr(cls, "_on_gpu", lambda self: None)  # the CPU's index, -1, plays another GPU's
+    c, pool = kv4.Kv4Cache.allocate(8, 2, 16, 64, 3, 2, device="cpu"), pages.PagePool.allocate(8, 16, device="cpu")
+    x, q, slots = torch.zeros((3, 2, 64)).half(), torch.zeros((3, 1, 4, 64)).half(), torch.zeros(3, dtype=torch.int64)
+    n, maps = torch.zeros(3, dtype=torch.int32), pool.maps(3, 5)
+    for other in (0, -1):
+        current[0] = other
+        for call in (lambda: c.append(x, x, slots), lambda: c.attend(q), lambda: c.read(5),
+                     lambda: pool.trim(c.page_table, c.lens, n), lambda: pool.grow(c.page_table, c.lens, n, maps)):
+            del where[:]
+            call()
+            assert where == [-1] and current[0] == other
+
+
 def test_session_refuses_what_does_not_fit():
     """Before any page is taken."""
     from cross_core_barrier_amd.kv8_decode import PooledSession
