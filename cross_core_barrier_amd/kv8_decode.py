@@ -211,6 +211,7 @@ class PooledSession:
         self.workspace = self.cache.attend_workspace(q_heads)
         self.x = torch.zeros((batch, q_heads * head_dim), dtype=dtype, device=dev)  # a step's input and output
         self.asks = torch.zeros(batch, dtype=torch.int32, device=dev)  # tokens that a step adds: 1 where somebody sits
+        self.taken = set()  # seats where somebody sits
         self.graph = None
 
     def _numbers(self, seats, fill: int, value) -> torch.Tensor:
@@ -221,6 +222,9 @@ class PooledSession:
 
     def leave(self, seats: list) -> None:
         """Requests that end: their pages go back."""
+        if not self.taken.issuperset(seats):
+            raise ValueError(f"seats {seats}: somebody sits in {sorted(self.taken)}")
+        self.taken.difference_update(seats)
         self.pool.trim(self.cache.page_table, self.cache.lens, self._numbers(seats, -1, 0))
         self.asks[seats] = 0
 
@@ -230,6 +234,8 @@ class PooledSession:
         lens = [p.shape[0] for p in prompts]
         if len(lens) != len(seats) or len(set(seats)) != len(seats) or not all(1 <= n <= self.limit for n in lens):
             raise ValueError(f"prompts: one for each seat, of 1 to {self.limit} tokens")
+        if not all(0 <= b < self.batch for b in seats) or not self.taken.isdisjoint(seats):
+            raise ValueError(f"seats {seats}: free ones of {self.batch}, somebody sits in {sorted(self.taken)}")
         order = sorted(range(len(seats)), key=lambda i: seats[i])  # as the new tokens are numbered
         rows = torch.cat([prompts[i] for i in order])
         maps = self.pool.maps(self.batch, rows.shape[0])
@@ -241,6 +247,7 @@ class PooledSession:
         for i in sat:
             self.x[seats[i]] = prompts[i][-1]
             self.asks[seats[i]] = 1
+            self.taken.add(seats[i])
         return [seats[i] for i in sat]
 
     def _step(self) -> None:
@@ -283,6 +290,8 @@ class PooledSession:
 
 def serve(a) -> None:
     """Requests on the 4-bit cache: prompts of unlike lengths, each decoded to the limit."""
+    if a.prompt >= a.limit:
+        raise ValueError(f"--prompt {a.prompt}: less than --limit {a.limit}, or no step is left to a request")
     s = PooledSession(batch=a.batch, limit=a.limit)
     d = s.x.shape[1]
     waiting = [torch.randn((max(1, a.prompt - 37 * (b % a.batch)), d), device="cuda", dtype=s.x.dtype)

@@ -306,3 +306,25 @@ def test_session_refuses_what_does_not_fit():
     for seats, lens in (([0], [97]), ([0], [0]), ([0, 1], [5]), ([1, 1], [5, 5])):
         with pytest.raises(ValueError):
             s.sit(seats, [torch.zeros((n, 64)) for n in lens])
+
+
+def test_session_refuses_seats_that_are_not_free():
+    """A prompt in a seat that is taken would go on behind the one that sits there."""
+    from cross_core_barrier_amd.kv8_decode import PooledSession
+    s = PooledSession.__new__(PooledSession)  # the checks need no device
+    s.batch, s.limit, s.taken = 3, 96, {1}
+    for seats in ([1], [0, 1], [3], [-1]):
+        with pytest.raises(ValueError, match="somebody sits"):
+            s.sit(seats, [torch.zeros((5, 64)) for _ in seats])
+    for seats in ([0], [0, 1], [-2]):
+        with pytest.raises(ValueError, match="somebody sits"):
+            s.leave(seats)
+    assert s.taken == {1}
+
+
+@pytest.mark.parametrize("prompt", ["100", "101"])
+def test_decode_command_refuses_prompts_at_the_limit(prompt):
+    """Such a request would sit, with no step left to it, in a seat taken for free."""
+    from cross_core_barrier_amd import kv8_decode
+    with pytest.raises(ValueError, match="--prompt"):
+        kv8_decode.main(["--format", "mxfp4", "--batch", "2", "--limit", "100", "--prompt", prompt])
