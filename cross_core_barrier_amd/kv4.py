@@ -131,6 +131,8 @@ class Kv4Cache(OnDevice):
             raise ValueError("q: [batch, queries, q_heads, head_dim]")
         if q.requires_grad:
             _no_gradient("q")
+        if not 0 <= window < 2 ** 31:  # (the library gets the low 32 bits)
+            raise ValueError("window: 0 (none) to 2^31 - 1 tokens")
         shape = q.shape
         queries, q_heads = shape[1], shape[2]
         s = None if stream is None else self._enter(stream)

@@ -328,3 +328,13 @@ def test_decode_command_refuses_prompts_at_the_limit(prompt):
     from cross_core_barrier_amd import kv8_decode
     with pytest.raises(ValueError, match="--prompt"):
         kv8_decode.main(["--format", "mxfp4", "--batch", "2", "--limit", "100", "--prompt", prompt])
+
+
+@pytest.mark.parametrize("window", [-1, 2 ** 31, 2 ** 32 + 5])
+def test_windows_past_32_bits_are_refused(monkeypatch, window):
+    """2^32 + 5 tokens would arrive as 5."""
+    from cross_core_barrier_amd import kv4
+    monkeypatch.setattr(kv4.Kv4Cache, "_on_gpu", lambda self: None)
+    c = kv4.Kv4Cache.allocate(8, 2, 16, 64, 3, 2, device="cpu")
+    with pytest.raises(ValueError, match="window"):
+        c.attend(torch.zeros((3, 1, 4, 64)).half(), window=window)
