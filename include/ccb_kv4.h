@@ -57,12 +57,13 @@ typedef struct ccbKv4Cache {
 
 /* Write new tokens: row i of kNew and vNew becomes the token at slots[i] (page
  * slots[i] / pageSize, slot slots[i] % pageSize); a row with slot -1 is left
- * out (and every row, where the cache's batch is 0).  For each head and each 32 dimensions of a row, with a the largest
- * finite |x| among them: e is the least whole number with a <= 7 * 2^e, at
- * least -64 and at most 125; the scale is e + 127; a code is x / 2^e rounded
- * once to e2m1 (half to even), saturated at +-6 (with this e nothing that is
- * finite is off by more than half a step, but for values above 7 * 2^125 and
- * below 2^-66); NaN becomes 0 and an infinity +-6.
+ * out (and every row, where the cache's batch is 0).  For each head and each 32
+ * dimensions of a row, with a the largest finite |x| among them: e is the least
+ * whole number with a <= 7 * 2^e, at least -64 and at most 125; the scale is
+ * e + 127; a code is x / 2^e rounded once to e2m1 (half to even), saturated at
+ * +-6 (with this e nothing that is finite is off by more than half a step, but
+ * for values above 7 * 2^125 and below 2^-66); NaN becomes 0 and an infinity
+ * +-6.
  * Two rows of one call should not have the same slot: which of them each 8
  * dimensions and each scale are from is not defined then.
  *   kNew, vNew  [nNew][heads][headDim], bf16 or fp16 (strideBatch is not used)
@@ -82,8 +83,10 @@ CCB_API ccbStatus ccb_kv4_append(const ccbKv4Cache* cache, const ccbKv8Rows* kNe
  * a query that sees nothing (an empty sequence, or i < nQuery - n) gets out =
  * 0 and lse = -infinity.  Products q k are exact, sums are kept in 32 bits, a
  * weight enters the sum of values within 2^-18 of itself, and out is rounded
- * once to its type.  Results do not depend on timing: the same call gives the
- * same bits.
+ * once to its type.  Weights are relative to a maximum that later scores may
+ * have passed by a factor of 2^8: where that and the number of tokens take the
+ * values past 2^128 (|v| >= 2^90 at the most tokens there can be) a sum may be
+ * infinite.  Results do not depend on timing: the same call gives the same bits.
  *   q, out  [batch][nQuery][headsQ][headDim], of one type.  out may be q itself
  *           (the same data and strides) and overlaps it in no other way.
  *   lse     device float [batch][nQuery][headsQ], or NULL
