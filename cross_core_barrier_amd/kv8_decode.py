@@ -230,17 +230,26 @@ class PooledSession:
 
     def sit(self, seats: list, prompts: list) -> list:
         """Prompts [tokens, d] for free seats.  Returns the seats that got pages;
-        the others stay free.  Waits for the device."""
+        the others stay free.  Waits for the device.  What is refused takes no
+        page: a seat whose prompt failed behind grow would hold its tokens."""
         lens = [p.shape[0] for p in prompts]
         if len(lens) != len(seats) or len(set(seats)) != len(seats) or not all(1 <= n <= self.limit for n in lens):
             raise ValueError(f"prompts: one for each seat, of 1 to {self.limit} tokens")
         if not all(0 <= b < self.batch for b in seats) or not self.taken.isdisjoint(seats):
             raise ValueError(f"seats {seats}: free ones of {self.batch}, somebody sits in {sorted(self.taken)}")
+        x = self.x
+        if not all(p.dim() == 2 and p.shape[1] == x.shape[1] and p.dtype == x.dtype and p.device == x.device
+                   for p in prompts):
+            raise ValueError(f"prompts: [tokens, {x.shape[1]}] {x.dtype} on {x.device}")
+        if torch.is_grad_enabled() and any(p.requires_grad for p in prompts):
+            raise ValueError("prompts: no gradient is computed here; detach them, or call under torch.no_grad()")
+        if not seats:
+            return []
         order = sorted(range(len(seats)), key=lambda i: seats[i])  # as the new tokens are numbered
         rows = torch.cat([prompts[i] for i in order])
         maps = self.pool.maps(self.batch, rows.shape[0])
-        self.pool.grow(self.cache.page_table, self.cache.lens, self._numbers(seats, 0, lens), maps)
         _, k, v = self.layer.project(rows)
+        self.pool.grow(self.cache.page_table, self.cache.lens, self._numbers(seats, 0, lens), maps)
         self.cache.append(k, v, maps.slots)
         granted = maps.granted.tolist()
         sat = [i for i in order if granted[seats[i]] > 0]

@@ -687,3 +687,20 @@ def test_decode_command_serves_requests(kv4, capsys):
     # prompts of 90, 53, 16, 90, 53, 16 tokens, to 100 each: the first seat's ends after 10 steps, and after 20
     out = capsys.readouterr().out
     assert "3 seats, 30 steps, 2 requests ended" in out and "lengths now 46 to 83" in out
+
+
+def test_pooled_session_after_a_refused_prompt(kv4):
+    """The seat is as free as before."""
+    from cross_core_barrier_amd.kv8_decode import PooledSession
+    _say("pooled session: a refused prompt")
+    s = PooledSession(batch=2, heads=1, q_heads=2, head_dim=64, page_size=16, limit=40, seed=4)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    rows = torch.randn((20, 128), generator=gen, device="cuda").to(s.x.dtype)
+    for bad in (rows[:, :64], rows.half(), rows.cpu(), rows.clone().requires_grad_()):
+        with pytest.raises(ValueError, match="prompts"):
+            s.sit([0], [bad])
+    assert s.cache.lens.tolist() == [0, 0] and s.pool.count.item() == 6
+    assert s.sit([], []) == [] and s.sit([0], [rows]) == [0]
+    s.step()
+    assert s.cache.lens.tolist() == [21, 0] and s.pool.count.item() == 4
+    s.pool.check()

@@ -338,3 +338,46 @@ def test_windows_past_32_bits_are_refused(monkeypatch, window):
     c = kv4.Kv4Cache.allocate(8, 2, 16, 64, 3, 2, device="cpu")
     with pytest.raises(ValueError, match="window"):
         c.attend(torch.zeros((3, 1, 4, 64)).half(), window=window)
+
+
+def test_session_refuses_prompts_before_pages_are_taken():
+    """Behind grow a refusal would leave the prompt's tokens in a seat that counts
+    as free, and the next one's behind them."""
+    from cross_core_barrier_amd.kv8_decode import PooledSession
+
+    class Calls:
+        def __getattr__(self, name):
+            raise AssertionError(f"reached {name}")
+    s = PooledSession.__new__(PooledSession)
+    s.batch, s.limit, s.taken = 3, 96, set()
+    s.x = torch.zeros((3, 64), dtype=torch.bfloat16)
+    s.pool = s.cache = s.layer = Calls()
+    good = torch.zeros((5, 64), dtype=torch.bfloat16)
+    for bad in (good[:, :32], good.half(), good.to("meta"), good[None], good.clone().requires_grad_()):
+        for prompts in ([bad], [good, bad]):
+            with pytest.raises(ValueError, match="prompts"):
+                s.sit(list(range(len(prompts))), prompts)
+    assert s.sit([], []) == [] and s.taken == set()
+    with pytest.raises(AssertionError, match="reached maps"):
+        s.sit([0], [good])
+
+
+def test_session_projects_before_pages_are_taken():
+    """(which may fail for want of memory)"""
+    from cross_core_barrier_amd.kv8_decode import PooledSession
+
+    class Pool:
+        def maps(self, batch, tokens):
+            return None
+
+        def grow(self, *a):
+            raise AssertionError("pages are taken")
+
+    class Layer:
+        def project(self, rows):
+            raise RuntimeError("no memory")
+    s = PooledSession.__new__(PooledSession)
+    s.batch, s.limit, s.taken, s.pool, s.layer = 3, 96, set(), Pool(), Layer()
+    s.x = torch.zeros((3, 64))
+    with pytest.raises(RuntimeError, match="no memory"):
+        s.sit([1], [torch.zeros((5, 64))])
