@@ -210,7 +210,8 @@ class PooledSession:
         self.maps = self.pool.maps(batch, batch)  # of a step
         self.workspace = self.cache.attend_workspace(q_heads)
         self.x = torch.zeros((batch, q_heads * head_dim), dtype=dtype, device=dev)  # a step's input and output
-        self.asks = torch.zeros(batch, dtype=torch.int32, device=dev)  # tokens that a step adds: 1 where somebody sits
+        # what a seat's request grows to, 0 where nobody sits, and the tokens that a step adds: 1 up to there
+        self.limits, self.asks = (torch.zeros(batch, dtype=torch.int32, device=dev) for _ in range(2))
         self.taken = set()  # seats where somebody sits
         self.graph = None
 
@@ -226,7 +227,7 @@ class PooledSession:
             raise ValueError(f"seats {seats}: somebody sits in {sorted(self.taken)}")
         self.taken.difference_update(seats)
         self.pool.trim(self.cache.page_table, self.cache.lens, self._numbers(seats, -1, 0))
-        self.asks[seats] = 0
+        self.limits[seats] = 0
 
     def sit(self, seats: list, prompts: list) -> list:
         """Prompts [tokens, d] for free seats.  Returns the seats that got pages;
@@ -255,12 +256,13 @@ class PooledSession:
         sat = [i for i in order if granted[seats[i]] > 0]
         for i in sat:
             self.x[seats[i]] = prompts[i][-1]
-            self.asks[seats[i]] = 1
+            self.limits[seats[i]] = self.limit
             self.taken.add(seats[i])
         return [seats[i] for i in sat]
 
     def _step(self) -> None:
         q, k, v = self.layer.project(self.x[:, None])
+        torch.lt(self.cache.lens, self.limits, out=self.asks)
         self.pool.grow(self.cache.page_table, self.cache.lens, self.asks, self.maps)
         # the step's tokens stand one behind the other: seats that ask for none are left out
         of = self.maps.sequences.clamp(min=0).long()
@@ -270,7 +272,8 @@ class PooledSession:
         self.x.copy_(torch.where(self.maps.granted.unsqueeze(1) > 0, self.layer.output(out), self.x))
 
     def step(self, graph: bool = True) -> torch.Tensor:
-        """One token more for every request; returns the layer's output."""
+        """One token more for every request below the limit (one that is there stays
+        as it is until it leaves); returns the layer's output."""
         if not graph:
             self._step()
         else:
@@ -282,8 +285,8 @@ class PooledSession:
     def _capture(self) -> None:
         """Capture the step.  The run outside the capture that this needs is
         made with nobody asking for a token, which changes nothing."""
-        x, asks = self.x.clone(), self.asks.clone()
-        self.asks.zero_()
+        x, limits = self.x.clone(), self.limits.clone()
+        self.limits.zero_()
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
@@ -294,7 +297,7 @@ class PooledSession:
         with torch.cuda.graph(self.graph):
             self._step()
         self.x.copy_(x)
-        self.asks.copy_(asks)
+        self.limits.copy_(limits)
 
 
 def serve(a) -> None:

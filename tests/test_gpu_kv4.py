@@ -704,3 +704,41 @@ def test_pooled_session_after_a_refused_prompt(kv4):
     s.step()
     assert s.cache.lens.tolist() == [21, 0] and s.pool.count.item() == 4
     s.pool.check()
+
+
+@pytest.mark.parametrize("graph", [True, False])
+@pytest.mark.parametrize("limit", [32, 40])
+def test_pooled_session_stops_at_the_limit(kv4, limit, graph):
+    """A limit that fills its pages, and one that does not: a request at it stays
+    as it is, the others go on, and nothing is reported."""
+    from cross_core_barrier_amd.kv8_decode import PooledSession
+    _say(f"pooled session: limit {limit} graph={graph}")
+    ends = []
+    for full in (True, False):  # the same neighbour beside a request that ends, and beside none
+        s = PooledSession(batch=3, heads=1, q_heads=2, head_dim=64, page_size=16, limit=limit, seed=4)
+        gen = torch.Generator(device="cuda").manual_seed(10)
+        rows = torch.randn((64, 128), generator=gen, device="cuda").to(s.x.dtype)
+        s.sit([1], [rows[:5]])
+        if full:
+            s.sit([0, 2], [rows[:limit - 2], rows[:limit]])
+        at_limit = []
+        for i in range(8):
+            s.step(graph)
+            if i >= 1:
+                at_limit.append(s.x[::2].clone())
+        lens = [limit, 13, limit] if full else [0, 13, 0]
+        assert s.cache.lens.tolist() == lens
+        assert s.pool.count.item() == s.cache.k.shape[0] - sum(-(-n // 16) for n in lens)
+        assert all(torch.equal(x, at_limit[0]) for x in at_limit)
+        if full:
+            assert torch.equal(s.x[2], rows[limit - 1])
+            s.leave([0, 2])
+            assert s.sit([2], [rows[:3]]) == [2]
+            s.step(graph)
+            assert s.cache.lens.tolist() == [0, 14, 4]
+        else:
+            s.step(graph)
+        s.cache.check()
+        s.pool.check()
+        ends.append(s.x[1].clone())
+    assert torch.equal(*ends)  # (rows of the same products, and a sequence in one run)
