@@ -742,3 +742,14 @@ def test_pooled_session_stops_at_the_limit(kv4, limit, graph):
         s.pool.check()
         ends.append(s.x[1].clone())
     assert torch.equal(*ends)  # (rows of the same products, and a sequence in one run)
+
+
+@pytest.mark.parametrize("steps,ended,lens", [(1, 1, "26 to 99"), (2, 2, "27 to 64"), (3, 2, "28 to 65")])
+def test_decode_command_counts_requests_of_the_first_step(kv4, capsys, steps, ended, lens):
+    """Prompts of 99, 62, 25, 99, 62, 25 tokens, to 100 each: the first seat's end with
+    the first step and the second."""
+    from cross_core_barrier_amd import kv8_decode
+    _say(f"kv8_decode --format mxfp4, {steps} steps, prompts one short of the limit")
+    kv8_decode.main(["--batch", "3", "--steps", str(steps), "--prompt", "99", "--limit", "100", "--format", "mxfp4"])
+    out = capsys.readouterr().out
+    assert f"3 seats, {steps} steps, {ended} requests ended" in out and f"lengths now {lens}" in out
