@@ -914,6 +914,9 @@ uint64_t new_tag()
     return n != 0 ? n : next.fetch_add(1, std::memory_order_relaxed);
 }
 
+// Whether a kernel of its own joins what is cut.
+bool joins_apart(const Plan& p) { return p.runs > p.a.c.batch && !p.joinHere; }
+
 int64_t join_groups(const Plan& p)
 {
     const int64_t rows = (int64_t)p.rows * p.a.c.batch * p.a.c.heads;
@@ -925,7 +928,7 @@ hipError_t launch(const Plan& p, hipStream_t s)
 {
     const int64_t groups = (int64_t)p.a.c.heads * p.rowBlocks * p.runs;
     hipError_t e = enqueue(kv4_k_attend<T, D, 1>, groups, kThreads, s, p);
-    if (e == hipSuccess && p.runs > p.a.c.batch && !p.joinHere) e = enqueue(kv4_k_join<T>, join_groups(p), kJoinThreads, s, p, D);
+    if (e == hipSuccess && joins_apart(p)) e = enqueue(kv4_k_join<T>, join_groups(p), kJoinThreads, s, p, D);
     return e;
 }
 
@@ -948,7 +951,7 @@ bool kv4_attend_fits(const ccbKv4Cache& c, int32_t headsQ, int32_t nQuery, int32
     p.a.c = c;
     return make_plan(p, c, headsQ, nQuery, window, nullptr) <= wsBytes &&
            kv8_launch_fits((int64_t)c.heads * p.rowBlocks * p.runs, kThreads) &&
-           kv8_launch_fits(join_groups(p), kJoinThreads);
+           (!joins_apart(p) || kv8_launch_fits(join_groups(p), kJoinThreads));
 }
 
 hipError_t kv4_attend(const Kv4AttendArgs& a, hipStream_t s)

@@ -753,3 +753,22 @@ def test_decode_command_counts_requests_of_the_first_step(kv4, capsys, steps, en
     kv8_decode.main(["--batch", "3", "--steps", str(steps), "--prompt", "99", "--limit", "100", "--format", "mxfp4"])
     out = capsys.readouterr().out
     assert f"3 seats, {steps} steps, {ended} requests ended" in out and f"lengths now {lens}" in out
+
+
+def test_attend_of_2_26_rows(kv4):
+    """A call of 4.2 million workgroups, more rows than the kernel that joins runs would
+    hold: 1024 sequences alike, each as it comes out by itself."""
+    rng = np.random.default_rng(27)
+    c = _host(rng, [40], 8, 16, 64)
+    one = _device(kv4, c)
+    many = kv4.Kv4Cache(one.k, one.v, one.k_scale, one.v_scale, one.page_table.repeat(1024, 1), one.lens.repeat(1024))
+    q = torch.from_numpy(rng.normal(0, 1, (1, 1024, 64, 64))).bfloat16().cuda()
+    _say("attend 1024 sequences, 1024 queries, 64 heads")
+    want, want_lse = one.attend(q)
+    out, lse = many.attend(q.expand(1024, -1, -1, -1))
+    torch.cuda.synchronize()
+    assert (want[0, :984] == 0).all() and (want[0, 984:] != 0).any(-1).all()
+    assert torch.equal(lse, want_lse.expand_as(lse))
+    for b0 in range(0, 1024, 128):  # (8.6 GB)
+        assert torch.equal(out[b0:b0 + 128], want.expand(128, -1, -1, -1))
+    many.check()

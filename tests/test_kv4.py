@@ -381,3 +381,22 @@ def test_session_projects_before_pages_are_taken():
     s.x = torch.zeros((3, 64))
     with pytest.raises(RuntimeError, match="no memory"):
         s.sit([1], [torch.zeros((5, 64))])
+
+
+@pytest.mark.parametrize("batch,queries", [(1023, 1024), (1024, 1024), (64, 16384), (2048, 512), (2047, 1024)])
+def test_accepts_what_a_launch_holds(ccb, batch, queries):
+    """Up to 2^27 rows (fewer than 2^23 workgroups of 512 threads, 16 rows each) where
+    nothing is cut: the kernel that joins runs, which holds fewer than 2^26, is not
+    started then."""
+    c = _cache(ccb, heads=8, batch=batch, headDim=128, maxPages=8, tableStride=8, pageSize=128)
+    r, out, inv = _rows(ccb), _rows(ccb, data=13 << 20), ccb.CCB_ERR_INVALID_VALUE
+    size = ccb.ccb_kv4_attend_workspace_bytes(c, 64, queries)
+    assert size == 128
+    if torch.cuda.is_available():
+        pytest.skip("what is accepted would be enqueued")
+    assert ccb.ccb_kv4_attend(c, r, out, None, 64, queries, 0.1, 0, 9 << 20, size) not in (inv, ccb.CCB_OK)
+    more = _cache(ccb, heads=8, batch=2048, headDim=128, maxPages=8, tableStride=8, pageSize=128)
+    assert ccb.ccb_kv4_attend(more, r, out, None, 64, 1024, 0.1, 0, 9 << 20, size) == inv
+    # 2^26 rows of sequences that may be cut into more runs than the last of them joins
+    long = _cache(ccb, heads=1, batch=1 << 16, headDim=128, maxPages=1 << 14, tableStride=1 << 14, pageSize=128)
+    assert ccb.ccb_kv4_attend(long, r, out, None, 64, 16, 0.1, 0, 9 << 20, 1 << 62) == inv
