@@ -25,7 +25,7 @@ from typing import Optional
 import torch
 
 from . import ccb
-from .kv8 import _ROWS, OnDevice, _need, _no_gradient
+from .kv8 import _ROWS, OnDevice, _int32, _need, _no_gradient
 
 GROUP = 32  # dimensions that share a scale
 _PACKED = {t: kind for t, kind in _ROWS.items() if kind != ccb.CCB_KV8_FP32}
@@ -105,6 +105,8 @@ class Kv4Cache(OnDevice):
         n = k_new.shape[0]
         if n != v_new.shape[0] or k.type != v.type:
             raise ValueError("v_new: shape and dtype of k_new")
+        if n >> 31:
+            _int32("tokens", n)
         if slots.dtype is not torch.int64 or slots.dim() != 1 or slots.shape[0] != n \
                 or slots.get_device() != self._index or not slots.is_contiguous():
             raise ValueError(f"slots: [{n}] int64, contiguous, on {self.device}")
@@ -115,6 +117,7 @@ class Kv4Cache(OnDevice):
         """A workspace for attend() calls of these sizes that follow each other."""
         if self._index < 0:
             self._on_gpu()
+        _int32("attend", q_heads, queries)
         n = ccb.ccb_kv4_attend_workspace_bytes(self._c, q_heads, queries)
         _need(n > 0, "attend: sizes that ccb_kv4_attend refuses")
         return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -166,6 +169,7 @@ class Kv4Cache(OnDevice):
             raise ValueError("dtype: float32, bfloat16 or float16")
         if first is not None:
             self._ints(first, (self.batch,), "first")
+        _int32("count", count)
         s = None if stream is None else self._enter(stream)
         both = torch.empty((2, self.batch, count, self.heads, self.head_dim), dtype=dtype, device=self.device)
         if s is not None:

@@ -40,6 +40,13 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+def _int32(what: str, *numbers: int) -> None:
+    """The library's integers have 32 bits: of a larger one it would get the low ones."""
+    for n in numbers:
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"{what}: {n} is no number of 32 bits")
+
+
 def _no_gradient(what: str) -> None:
     if torch.is_grad_enabled():
         raise ValueError(f"{what}: no gradient is computed here; detach it, or call under torch.no_grad()")
@@ -186,6 +193,8 @@ class Kv8Cache(OnDevice):
         if k_new.requires_grad or v_new.requires_grad:
             _no_gradient("k_new, v_new")
         n = k_new.shape[1]
+        if n >> 31:
+            _int32("tokens", n)
         _need(n == v_new.shape[1] and k.type == v.type, "v_new: shape and dtype of k_new")
         self._ints(counts, (self.batch,), "counts")
         s = None if stream is None else self._enter(stream)
@@ -197,6 +206,7 @@ class Kv8Cache(OnDevice):
         of a cache head and each token there is room for."""
         if self._index < 0:
             self._on_gpu()
+        _int32("attend", q_heads, queries)
         n = ccb.ccb_kv8_attend_workspace_bytes(self._c, q_heads, queries, int(accumulate))
         _need(n > 0, "attend: sizes that ccb_kv8_attend refuses")
         return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -213,6 +223,8 @@ class Kv8Cache(OnDevice):
         _need(q.dim() == 4, "q: [batch, queries, q_heads, head_dim]")
         if q.requires_grad:
             _no_gradient("q")
+        if window >> 31:
+            _int32("window", window)
         shape = q.shape
         queries, q_heads = shape[1], shape[2]
         s = None if stream is None else self._enter(stream)
@@ -239,6 +251,7 @@ class Kv8Cache(OnDevice):
         """A workspace for evict() calls with this budget that follow each other."""
         if self._index < 0:
             self._on_gpu()
+        _int32("budget", budget)
         n = ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
         _need(n > 0, "evict: sizes that ccb_kv8_evict refuses")
         return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -254,6 +267,7 @@ class Kv8Cache(OnDevice):
         if self._index < 0:
             self._on_gpu()
         _need(to._index == self._index, "to: on the cache's device")
+        _int32("budget, recent, sinks", budget, recent, sinks)
         self._ints(kept, (self.batch, self.heads, budget), "kept")
         s = None if stream is None else self._enter(stream)
         need = 0 if workspace is not None else ccb.ccb_kv8_evict_workspace_bytes(self._c, budget)
@@ -269,6 +283,7 @@ class Kv8Cache(OnDevice):
         kind = _ROWS.get(dtype)
         _need(kind is not None, "dtype: float32, bfloat16 or float16")
         self._ints(first, (self.batch,), "first")
+        _int32("count", count)
         s = None if stream is None else self._enter(stream)
         both = torch.empty((2, self.batch, count, self.heads, self.head_dim), dtype=dtype, device=self.device)
         if s is not None:

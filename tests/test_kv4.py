@@ -400,3 +400,33 @@ def test_accepts_what_a_launch_holds(ccb, batch, queries):
     # 2^26 rows of sequences that may be cut into more runs than the last of them joins
     long = _cache(ccb, heads=1, batch=1 << 16, headDim=128, maxPages=1 << 14, tableStride=1 << 14, pageSize=128)
     assert ccb.ccb_kv4_attend(long, r, out, None, 64, 16, 0.1, 0, 9 << 20, 1 << 62) == inv
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """Of 2^32 + 5 the library would get 5."""
+    from cross_core_barrier_amd import ccb, kv4, kv8
+
+    def reached(*a):
+        raise AssertionError("reached the library")
+    for name in ("kv4_append", "kv8_append", "kv4_attend_workspace_bytes", "kv8_attend", "kv8_attend_workspace_bytes",
+                 "kv8_evict", "kv8_evict_workspace_bytes", "kv4_read", "kv8_read"):
+        monkeypatch.setattr(ccb, f"ccb_{name}", reached)
+    monkeypatch.setattr(kv8.OnDevice, "_on_gpu", lambda self: None)
+    monkeypatch.setattr(kv8, "_current_stream", lambda index: 0)
+    monkeypatch.setattr(kv8, "_current_device", lambda: -1)
+    big = 2 ** 32 + 5
+    c4 = kv4.Kv4Cache.allocate(8, 2, 16, 64, 3, 2, device="cpu")
+    c8, to = (kv8.Kv8Cache.allocate(8, 2, 16, 64, 3, 2, "int8", weights=True, device="cpu") for _ in range(2))
+    row, rows = torch.zeros((1, 2, 64)).half(), torch.zeros((3, 1, 2, 64)).half()
+    slots, q = torch.zeros(1, dtype=torch.int64), torch.zeros((3, 1, 4, 64)).half()
+    for call in (lambda: c4.append(row.expand(big, 2, 64), row.expand(big, 2, 64), slots),
+                 lambda: c8.append(rows.expand(3, big, 2, 64), rows.expand(3, big, 2, 64)),
+                 lambda: c4.attend_workspace(big), lambda: c4.attend_workspace(4, big),
+                 lambda: c8.attend_workspace(big), lambda: c8.attend_workspace(4, big),
+                 lambda: c8.attend(q, window=big), lambda: c8.attend(q, window=-big), lambda: c8.evict_workspace(big),
+                 lambda: c8.evict(to, big), lambda: c8.evict(to, 5, recent=big), lambda: c8.evict(to, 5, sinks=2 ** 31),
+                 lambda: c4.read(big), lambda: c8.read(big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    with pytest.raises(AssertionError, match="library"):
+        c8.append(rows, rows)
