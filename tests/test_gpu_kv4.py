@@ -772,3 +772,34 @@ def test_attend_of_2_26_rows(kv4):
     for b0 in range(0, 1024, 128):  # (8.6 GB)
         assert torch.equal(out[b0:b0 + 128], want.expand(128, -1, -1, -1))
     many.check()
+
+
+@pytest.mark.parametrize("keys,values,q_size", [(0, 127, 2.0 ** 124), (1, 127, 2.0 ** 123), (2, 127, 2.0 ** 122),
+                                                (0, 0, 1.0), (127, 1, 1.0), (120, 2, 3.0), (127, 8, 1.0)])
+def test_attend_smallest_scales(kv4, keys, values, q_size):
+    """Scales below those that an append writes, whose values are bf16's subnormals
+    among them: keys under queries that bring them back, and values as they are
+    (there half a step of out is 2^-134)."""
+    rng = np.random.default_rng(28)
+    lens = [40, 700, 1500]
+    c = _host(rng, lens, 1, 16, 64)
+    for w, low in (("ks", keys), ("vs", values)):
+        c[w][c[w] != 255] = rng.integers(low, low + 3, c[w].shape)[c[w] != 255]
+    cache = _device(kv4, c)
+    q = torch.from_numpy(rng.normal(0, q_size, (3, 1, 3, 64))).bfloat16()
+    _say(f"attend scales from {keys} and {values}")
+    want, lse, mag, big = oracle.attend(c, q.double().numpy(), 1.0, 0)
+    assert big.max() > 0.5 or keys == values == 0
+    out, got = cache.attend(q.cuda(), scale=1.0)
+    rel, tol_lse, tol = _bounds(64, max(lens), mag, big, lse)
+    y = out.double().cpu().numpy()
+    # sums of values are rounded in steps of 2^-149, once for each of two products of 32 tokens and each join
+    assert np.all(np.abs(y - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 2.0 ** -134 + 2.0 ** -140)
+    assert np.all(np.abs(got.double().cpu().numpy() - lse) <= tol_lse)
+    # a scale of 0 that counted as nothing would be seen, in keys or in values
+    c0 = dict(c, k=np.where(np.repeat(c["ks"] == 0, 16, -1), 0, c["k"]), v=np.where(np.repeat(c["vs"] == 0, 16, -1), 0, c["v"]))
+    if keys == 0 or values == 0:
+        other, other_lse, _, _ = oracle.attend(c0, q.double().numpy(), 1.0, 0)
+        assert np.any(np.abs(other - want) > 2 * (tol + 2.0 ** -8 * np.abs(want) + 2.0 ** -134)) or \
+            np.any(np.abs(other_lse - lse) > 2 * tol_lse)
+    cache.check()
