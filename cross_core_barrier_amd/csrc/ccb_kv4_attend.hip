@@ -52,6 +52,7 @@ using namespace kv8;
 constexpr int kThreads = 512;  // of a workgroup that takes a run of tokens
 constexpr int kWaves = kThreads / 64;
 constexpr int kJoinThreads = 256;
+constexpr int kRows = 16;                // of a workgroup
 constexpr int kTile = 32;                // tokens of a wave's step
 constexpr int kRunUnit = kWaves * kTile;
 constexpr int kSegment = 32 * kRunUnit;  // tokens whose pages fit a wave's lanes
@@ -292,14 +293,14 @@ __device__ __forceinline__ void merge(float& top, float& all, float top2, float 
 // joins already.  The tag is this call's own number, so that it does not matter
 // what the workspace held, and the tags are cleared, so that a replayed call may
 // use its number again.
-template <int T, int D, int R>
+template <int T, int D>
 __device__ __forceinline__ void join_here(const Plan& p, const Place& runs, int32_t run, int32_t h, int32_t row0,
                                           uint8_t* lds)
 {
     const int32_t n = runs.n;
     __shared__ int32_t all;
     const int tid = threadIdx.x;
-    uint64_t* tags = p.tags + ((int64_t)h * p.rowBlocks + row0 / R) * p.runs + runs.first;
+    uint64_t* tags = p.tags + ((int64_t)h * p.rowBlocks + row0 / kRows) * p.runs + runs.first;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid < 64) {
@@ -320,10 +321,10 @@ __device__ __forceinline__ void join_here(const Plan& p, const Place& runs, int3
 
     constexpr int V = D / 4, kWide = 8;  // vectors of a row; loads in flight
     f4* const sums = (f4*)lds;                   // [thread]
-    float* const factor = (float*)(sums + kThreads);  // [run][R]
-    float* const top = factor + kJoinHere * R;   // [R]
-    float* const total = top + R;                // [R]
-    const int32_t rows = p.rows - row0 < R ? p.rows - row0 : R, items = V * rows;
+    float* const factor = (float*)(sums + kThreads);  // [run][kRows]
+    float* const top = factor + kJoinHere * kRows;   // [kRows]
+    float* const total = top + kRows;                // [kRows]
+    const int32_t rows = p.rows - row0 < kRows ? p.rows - row0 : kRows, items = V * rows;
     const int32_t side = kThreads / items;  // runs side by side, where a pass has threads for them
     const int32_t sg = side > 1 ? tid / items : 0, by = side > 1 ? side : 1;
     const int64_t first = ((int64_t)h * p.runs + runs.first) * p.rows + row0;
@@ -351,7 +352,7 @@ __device__ __forceinline__ void join_here(const Plan& p, const Place& runs, int3
                 float l = x.y * f;
 #pragma unroll
                 for (int d = 32; d >= 1; d >>= 1) l += __shfl_xor(l, d, 64);
-                if (lane < n) factor[lane * R + i] = f;
+                if (lane < n) factor[lane * kRows + i] = f;
                 if (lane == 0) top[i] = m, total[i] = l;
             }
             __syncthreads();
@@ -361,8 +362,8 @@ __device__ __forceinline__ void join_here(const Plan& p, const Place& runs, int3
             const float* f = factor + item / V;
 #pragma unroll
             for (int k = 0; k < kWide; ++k)
-                if (sg + k * by < n) o += v[k] * f[(sg + k * by) * R];
-            for (int32_t s = sg + kWide * by; s < n; s += by) o += part_at(s, item) * f[s * R];
+                if (sg + k * by < n) o += v[k] * f[(sg + k * by) * kRows];
+            for (int32_t s = sg + kWide * by; s < n; s += by) o += part_at(s, item) * f[s * kRows];
         }
         if (side > 1) {
             sums[tid] = o;
@@ -432,7 +433,7 @@ struct Half {
     }
 };
 
-template <int T, int D, int NT>
+template <int T, int D>
 // (two workgroups a CU where the registers suffice)
 __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16) ? 4 : 2) void kv4_k_attend(Plan p)
 {
@@ -445,7 +446,7 @@ __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16)
     // takes that away for 8 instructions more, and 25.3 us instead of 24.1.
     constexpr int S = 2 * D + 32;
     __shared__ __attribute__((aligned(16))) uint8_t vBuf[kWaves][kTile * S];
-    __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT];
+    __shared__ float sm[kWaves][kRows], sl[kWaves][kRows];
 
     const ccb::Kv4AttendArgs& a = p.a;
     const ccbKv4Cache& c = a.c;
@@ -454,7 +455,7 @@ __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16)
     uint32_t rest = blockIdx.x;
     const int32_t h = rest % (uint32_t)c.heads;
     rest /= (uint32_t)c.heads;
-    const int32_t row0 = (int32_t)(rest % (uint32_t)p.rowBlocks) * (16 * NT);
+    const int32_t row0 = (int32_t)(rest % (uint32_t)p.rowBlocks) * kRows;
     const int32_t number = rest / (uint32_t)p.rowBlocks;
     const int32_t P = c.pageSize, group = a.headsQ / c.heads;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -489,50 +490,43 @@ __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16)
     // computes row0's again, for nothing).  Scores are scaled by |scale|, a
     // negative one turns the queries' signs.
     const float scale2 = fabsf(a.scale) * kLog2e;
-    u4 q[NT][NJ][NQ];
-    int32_t begin[NT], end[NT];
+    u4 q[NJ][NQ];
+    int32_t begin, end;
+    const int32_t mine = row0 + n;
+    seen_by(a, r, mine, p.rows, group, begin, end);
+    const uint16_t* src = (const uint16_t*)a.q.data + row_at(a.q, b, h, mine < p.rows ? mine : row0, group) + g * (D / 4);
+    const uint32_t turn = a.scale < 0 ? 0x80008000u : 0u;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int32_t row = row0 + nt * 16 + n;
-        seen_by(a, r, row, p.rows, group, begin[nt], end[nt]);
-        const uint16_t* src = (const uint16_t*)a.q.data + row_at(a.q, b, h, row < p.rows ? row : row0, group) + g * (D / 4);
-        const uint32_t turn = a.scale < 0 ? 0x80008000u : 0u;
+    for (int j = 0; j < NJ; ++j) {
+        u4 x = *(const u4*)(src + 8 * j);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            u4 x = *(const u4*)(src + 8 * j);
+        for (int e = 0; e < 4; ++e) x[e] ^= turn;
+        if constexpr (NQ == 1) {
+            q[j][0] = x;
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] ^= turn;
-            if constexpr (NQ == 1) {
-                q[nt][j][0] = x;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t hi, low;
-                    pieces(widen<T>(x[e] & 0xffffu), widen<T>(x[e] >> 16), hi, low);
-                    q[nt][j][0][e] = hi, q[nt][j][NQ - 1][e] = low;
-                }
+            for (int e = 0; e < 4; ++e) {
+                uint32_t hi, low;
+                pieces(widen<T>(x[e] & 0xffffu), widen<T>(x[e] >> 16), hi, low);
+                q[j][0][e] = hi, q[j][NQ - 1][e] = low;
             }
         }
     }
     // tokens in [allBegin, allEnd) are seen by every row of the workgroup
     int32_t allBegin, allEnd, unused;
     {
-        const int32_t last = row0 + 16 * NT < p.rows ? row0 + 16 * NT - 1 : p.rows - 1;
+        const int32_t last = row0 + kRows < p.rows ? row0 + kRows - 1 : p.rows - 1;
         seen_by(a, r, last, p.rows, group, allBegin, unused);
         seen_by(a, r, row0, p.rows, group, unused, allEnd);
         allBegin = __builtin_amdgcn_readfirstlane(allBegin), allEnd = __builtin_amdgcn_readfirstlane(allEnd);
     }
 
-    f4 o[NT][NB];
+    f4 o[NB];
     // What weights are relative to, a maximum that scores may pass by kSlack; the
     // lowest float for a row that has seen nothing (less it, every score grows).
-    float ref[NT], l[NT];
+    float ref = -FLT_MAX, l = 0.0f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        ref[nt] = -FLT_MAX, l[nt] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < NB; ++d) o[nt][d] = f4{0, 0, 0, 0};
-    }
+    for (int d = 0; d < NB; ++d) o[d] = f4{0, 0, 0, 0};
 
     // Whether a maximum has passed 2^20: what the product's rounding adds to the
     // maximum, 2^-24 of it, would no longer be small as an exponent.
@@ -581,14 +575,13 @@ __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16)
             const uint32_t pair = (uint32_t)(held >> (2 * i)) & 3u;
             const bool whole = t0 >= allBegin && t0 + kTile <= allEnd && pair == 3u;
             // scores
-            f4 s[NT][2];
+            f4 s[2];
             {
                 float f[2][2];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     f[half][0] = of_bits(key[half].s0 << 23), f[half][1] = of_bits(key[half].s1 << 23);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) s[nt][half] = f4{0, 0, 0, 0};
+                    s[half] = f4{0, 0, 0, 0};
                 }
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
@@ -596,9 +589,7 @@ __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16)
                     for (int half = 0; half < 2; ++half) {
                         const u4 k8 = key[half].values(j, g, f[half][0], f[half][1]);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int k = 0; k < NQ; ++k) s[nt][half] = mfma(k8, q[nt][j][k], s[nt][half]);
+                        for (int k = 0; k < NQ; ++k) s[half] = mfma(k8, q[j][k], s[half]);
                     }
             }
             // the next tile's keys (behind the last one's: the same again, so that the
@@ -614,13 +605,11 @@ __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16)
                 by = 1.0f;
                 const bool there0 = (pair & 1u) != 0, there1 = (pair & 2u) != 0;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int32_t t = t0 + 4 * g + e;
-                        s[nt][0][e] = t >= begin[nt] && t < end[nt] && there0 ? s[nt][0][e] * scale2 : -INFINITY;
-                        s[nt][1][e] = t + 16 >= begin[nt] && t + 16 < end[nt] && there1 ? s[nt][1][e] * scale2 : -INFINITY;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const int32_t t = t0 + 4 * g + e;
+                    s[0][e] = t >= begin && t < end && there0 ? s[0][e] * scale2 : -INFINITY;
+                    s[1][e] = t + 16 >= begin && t + 16 < end && there1 ? s[1][e] * scale2 : -INFINITY;
+                }
                 // values that are not there: any scale, but a number
                 if (!(there0 && t0 + n < r.len)) val[0].s0 = val[0].s1 = 127;
                 if (!(there1 && t0 + 16 + n < r.len)) val[1].s0 = val[1].s1 = 127;
@@ -648,56 +637,45 @@ __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16)
 #pragma unroll
             for (int d = 0; d < NR; ++d) value[d] = transposed(d);
             __builtin_amdgcn_sched_barrier(0);
-            f4 y[NT][2];  // exponents, then weights
-            auto exponents = [&](int nt) {
+            f4 y[2];  // exponents, then weights
+            auto exponents = [&]() {
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[nt][half][e] = fmaf(s[nt][half][e], by, -ref[nt]);
+                    for (int e = 0; e < 4; ++e) y[half][e] = fmaf(s[half][e], by, -ref);
             };
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                exponents(nt);
-                const float x = fmaxf(fmaxf(y[nt][0].x, y[nt][0].y), fmaxf(y[nt][0].z, y[nt][0].w));
-                grows |= fmaxf(x, fmaxf(fmaxf(y[nt][1].x, y[nt][1].y), fmaxf(y[nt][1].z, y[nt][1].w))) > kSlack;
-            }
+            exponents();
+            const float x = fmaxf(fmaxf(y[0].x, y[0].y), fmaxf(y[0].z, y[0].w));
+            grows |= fmaxf(x, fmaxf(fmaxf(y[1].x, y[1].y), fmaxf(y[1].z, y[1].w))) > kSlack;
             if (__any(grows)) {  // a new maximum, for the row's four lanes alike
+                float top = fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[0].z, s[0].w));
+                top = fmaxf(top, fmaxf(fmaxf(s[1].x, s[1].y), fmaxf(s[1].z, s[1].w))) * by;
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                top = fmaxf(ref, fmaxf(top, __shfl_xor(top, 32, 64)));
+                const float f = exp2_(ref - top);
+                ref = top;
+                l *= f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float top = fmaxf(fmaxf(s[nt][0].x, s[nt][0].y), fmaxf(s[nt][0].z, s[nt][0].w));
-                    top = fmaxf(top, fmaxf(fmaxf(s[nt][1].x, s[nt][1].y), fmaxf(s[nt][1].z, s[nt][1].w))) * by;
-                    top = fmaxf(top, __shfl_xor(top, 16, 64));
-                    top = fmaxf(ref[nt], fmaxf(top, __shfl_xor(top, 32, 64)));
-                    const float f = exp2_(ref[nt] - top);
-                    ref[nt] = top;
-                    l[nt] *= f;
-#pragma unroll
-                    for (int d = 0; d < NB; ++d) o[nt][d] *= f;
-                    loud |= __ballot(fabsf(top) > 0x1p20f && top != -FLT_MAX) != 0;
-                }
+                for (int d = 0; d < NB; ++d) o[d] *= f;
+                loud |= __ballot(fabsf(top) > 0x1p20f && top != -FLT_MAX) != 0;
                 if (loud) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) s[nt][0] *= by, s[nt][1] *= by;
+                    s[0] *= by, s[1] *= by;
                     by = 1.0f;
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) exponents(nt);
+                exponents();
             }
-            u4 ph[NT], pl[NT];
+            u4 ph, pl;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int half = 0; half < 2; ++half) {
+                f4 p;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    f4 p;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = exp2_(y[nt][half][e]);
-                    l[nt] += (p.x + p.y) + (p.z + p.w);
-                    uint32_t h0, l0, h1, l1;
-                    pieces(p.x, p.y, h0, l0);
-                    pieces(p.z, p.w, h1, l1);
-                    ph[nt][2 * half] = h0, ph[nt][2 * half + 1] = h1;
-                    pl[nt][2 * half] = l0, pl[nt][2 * half + 1] = l1;
-                }
+                for (int e = 0; e < 4; ++e) p[e] = exp2_(y[half][e]);
+                l += (p.x + p.y) + (p.z + p.w);
+                uint32_t h0, l0, h1, l1;
+                pieces(p.x, p.y, h0, l0);
+                pieces(p.z, p.w, h1, l1);
+                ph[2 * half] = h0, ph[2 * half + 1] = h1;
+                pl[2 * half] = l0, pl[2 * half + 1] = l1;
             }
 #pragma unroll
             for (int d0 = 0; d0 < NB; d0 += NR) {
@@ -706,13 +684,9 @@ __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16)
                     for (int d = 0; d < NR; ++d) value[d] = transposed(d0 + d);
                 }
 #pragma unroll
-                for (int d = 0; d < NR; ++d)
+                for (int d = 0; d < NR; ++d) o[d0 + d] = mfma(value[d], ph, o[d0 + d]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) o[nt][d0 + d] = mfma(value[d], ph[nt], o[nt][d0 + d]);
-#pragma unroll
-                for (int d = 0; d < NR; ++d)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) o[nt][d0 + d] = mfma(value[d], pl[nt], o[nt][d0 + d]);
+                for (int d = 0; d < NR; ++d) o[d0 + d] = mfma(value[d], pl, o[d0 + d]);
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
@@ -726,54 +700,48 @@ __global__ __launch_bounds__(kThreads, D < 96 || (D <= 128 && T == CCB_KV8_BF16)
     }
 
     // join the waves
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        l[nt] += __shfl_xor(l[nt], 16, 64);
-        l[nt] += __shfl_xor(l[nt], 32, 64);
-        if (l[nt] == 0.0f) ref[nt] = -INFINITY;
-        if (g == 0) sm[wave][nt * 16 + n] = ref[nt], sl[wave][nt * 16 + n] = l[nt];
-    }
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (l == 0.0f) ref = -INFINITY;
+    if (g == 0) sm[wave][n] = ref, sl[wave][n] = l;
     __syncthreads();
     const int64_t part = ((int64_t)h * p.runs + number) * p.rows;
+    float top = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float top = -INFINITY;
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][n]);
+    const float f = l == 0.0f ? 0.0f : exp2_(ref - top);  // (a NaN stays)
+    // chunks of 4 dimensions are swapped so that rows fall on different banks
+    float* dst = (float*)vBuf[wave] + n * D;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm[w][nt * 16 + n]);
-        const float f = l[nt] == 0.0f ? 0.0f : exp2_(ref[nt] - top);  // (a NaN stays)
-        // chunks of 4 dimensions are swapped so that rows fall on different banks
-        float* dst = (float*)vBuf[wave] + n * D;
+    for (int d = 0; d < NB; ++d) *(f4*)(dst + (((4 * d + g) ^ (n & 7)) * 4)) = o[d] * f;
+    __syncthreads();
+    for (int32_t at = threadIdx.x; at < 4 * D; at += kThreads) {
+        const int32_t i = at / (D / 4), d4 = at % (D / 4), row = row0 + i;
+        if (row >= p.rows) continue;
+        f4 sum = {0, 0, 0, 0};
+        float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
-        for (int d = 0; d < NB; ++d) *(f4*)(dst + (((4 * d + g) ^ (n & 7)) * 4)) = o[nt][d] * f;
-        __syncthreads();
-        for (int32_t at = threadIdx.x; at < 4 * D; at += kThreads) {
-            const int32_t i = at / (D / 4), d4 = at % (D / 4), row = row0 + nt * 16 + i;
-            if (row >= p.rows) continue;
-            f4 sum = {0, 0, 0, 0};
-            float mm = -INFINITY, ll = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                sum += *(const f4*)((const float*)vBuf[w] + i * D + ((d4 ^ (i & 7)) * 4));
-                mm = fmaxf(mm, sm[w][nt * 16 + i]);
-            }
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                ll += sl[w][nt * 16 + i] == 0.0f ? 0.0f : sl[w][nt * 16 + i] * exp2_(sm[w][nt * 16 + i] - mm);
-            if (runs.n == 1) {
-                write_row<T>(p, b, h, row, d4, sum, mm, ll);
-            } else if (p.joinHere) {
-                float* dst = p.partO + (part + row) * D + d4 * 4;
-                store_shared(dst, sum.x, sum.y);
-                store_shared(dst + 2, sum.z, sum.w);
-                if (d4 == 0) store_shared((float*)(p.partML + part + row), mm, ll);
-            } else {
-                *(f4*)(p.partO + (part + row) * D + d4 * 4) = sum;
-                if (d4 == 0) p.partML[part + row] = make_float2(mm, ll);
-            }
+        for (int w = 0; w < kWaves; ++w) {
+            sum += *(const f4*)((const float*)vBuf[w] + i * D + ((d4 ^ (i & 7)) * 4));
+            mm = fmaxf(mm, sm[w][i]);
         }
-        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            ll += sl[w][i] == 0.0f ? 0.0f : sl[w][i] * exp2_(sm[w][i] - mm);
+        if (runs.n == 1) {
+            write_row<T>(p, b, h, row, d4, sum, mm, ll);
+        } else if (p.joinHere) {
+            float* dst = p.partO + (part + row) * D + d4 * 4;
+            store_shared(dst, sum.x, sum.y);
+            store_shared(dst + 2, sum.z, sum.w);
+            if (d4 == 0) store_shared((float*)(p.partML + part + row), mm, ll);
+        } else {
+            *(f4*)(p.partO + (part + row) * D + d4 * 4) = sum;
+            if (d4 == 0) p.partML[part + row] = make_float2(mm, ll);
+        }
     }
-    if (runs.n > 1 && p.joinHere) join_here<T, D, 16 * NT>(p, runs, run, h, row0, vBuf[0]);
+    __syncthreads();
+    if (runs.n > 1 && p.joinHere) join_here<T, D>(p, runs, run, h, row0, vBuf[0]);
 }
 
 // Joins the runs of a row: four rows to a workgroup, or one where there are
@@ -846,7 +814,7 @@ size_t make_plan(Plan& p, const ccbKv4Cache& c, int32_t headsQ, int32_t nQuery, 
     const int64_t rows = (int64_t)nQuery * (headsQ / c.heads), batch = c.batch;
     auto up = [](int64_t x, int64_t by) { return (x + by - 1) / by; };
     p.rows = (int32_t)rows;
-    p.rowBlocks = (int32_t)up(rows, 16);
+    p.rowBlocks = (int32_t)up(rows, kRows);
     const int64_t groups = (int64_t)c.heads * p.rowBlocks;  // workgroups that take a run
     // tokens that a sequence's queries may see, from a tile's border
     const int64_t room = (int64_t)c.maxPages * c.pageSize;
@@ -900,7 +868,7 @@ size_t make_plan(Plan& p, const ccbKv4Cache& c, int32_t headsQ, int32_t nQuery, 
     const int64_t extra = p.runs - batch + 1, byLength = up(up(span, kRunUnit), (int64_t)p.least);
     const int64_t here = extra < byLength ? extra : byLength, few = up(2 * p.runs, batch);
     p.joinHere = here <= kJoinHere &&
-                 (here < few ? here : few) * (rows < 16 ? rows : 16) * c.headDim * 4 <= (64 << 10);
+                 (here < few ? here : few) * (rows < kRows ? rows : kRows) * c.headDim * 4 <= (64 << 10);
     return bytes;
 }
 
@@ -927,7 +895,7 @@ template <int T, int D>
 hipError_t launch(const Plan& p, hipStream_t s)
 {
     const int64_t groups = (int64_t)p.a.c.heads * p.rowBlocks * p.runs;
-    hipError_t e = enqueue(kv4_k_attend<T, D, 1>, groups, kThreads, s, p);
+    hipError_t e = enqueue(kv4_k_attend<T, D>, groups, kThreads, s, p);
     if (e == hipSuccess && joins_apart(p)) e = enqueue(kv4_k_join<T>, join_groups(p), kJoinThreads, s, p, D);
     return e;
 }
