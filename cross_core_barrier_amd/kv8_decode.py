@@ -210,9 +210,9 @@ class PooledSession:
         self.maps = self.pool.maps(batch, batch)  # of a step
         self.workspace = self.cache.attend_workspace(q_heads)
         self.x = torch.zeros((batch, q_heads * head_dim), dtype=dtype, device=dev)  # a step's input and output
-        # what a seat's request grows to, 0 where nobody sits, and the tokens that a step adds: 1 up to there
-        self.limits, self.asks = (torch.zeros(batch, dtype=torch.int32, device=dev) for _ in range(2))
+        self.asks = torch.zeros(batch, dtype=torch.int32, device=dev)  # tokens that a step adds: 1 for seats in room
         self.taken = set()  # seats where somebody sits
+        self.room = {}  # of seats that ask for tokens: how many there are to the limit, at least
         self.graph = None
 
     def _numbers(self, seats, fill: int, value) -> torch.Tensor:
@@ -227,7 +227,9 @@ class PooledSession:
             raise ValueError(f"seats {seats}: somebody sits in {sorted(self.taken)}")
         self.taken.difference_update(seats)
         self.pool.trim(self.cache.page_table, self.cache.lens, self._numbers(seats, -1, 0))
-        self.limits[seats] = 0
+        self.asks[seats] = 0
+        for seat in seats:
+            self.room.pop(seat, None)
 
     def sit(self, seats: list, prompts: list) -> list:
         """Prompts [tokens, d] for free seats.  Returns the seats that got pages;
@@ -256,13 +258,14 @@ class PooledSession:
         sat = [i for i in order if granted[seats[i]] > 0]
         for i in sat:
             self.x[seats[i]] = prompts[i][-1]
-            self.limits[seats[i]] = self.limit
             self.taken.add(seats[i])
+            if lens[i] < self.limit:
+                self.asks[seats[i]] = 1
+                self.room[seats[i]] = self.limit - lens[i]
         return [seats[i] for i in sat]
 
     def _step(self) -> None:
         q, k, v = self.layer.project(self.x[:, None])
-        torch.lt(self.cache.lens, self.limits, out=self.asks)
         self.pool.grow(self.cache.page_table, self.cache.lens, self.asks, self.maps)
         # the step's tokens stand one behind the other: seats that ask for none are left out
         of = self.maps.sequences.clamp(min=0).long()
@@ -273,7 +276,9 @@ class PooledSession:
 
     def step(self, graph: bool = True) -> torch.Tensor:
         """One token more for every request below the limit (one that is there stays
-        as it is until it leaves); returns the layer's output."""
+        as it is until it leaves); returns the layer's output.  Waits for the
+        device where a request may be at the limit and has not left."""
+        self._count()
         if not graph:
             self._step()
         else:
@@ -282,11 +287,27 @@ class PooledSession:
             self.graph.replay()
         return self.x
 
+    def _count(self) -> None:
+        """Who is at the limit asks no more.  A step adds a token at most, so that the
+        lengths need to be looked at only after as many steps as there was room for
+        (fewer tokens than that came where the pool was empty)."""
+        due = [seat for seat, n in self.room.items() if n == 0]
+        if due:
+            lens = self.cache.lens.tolist()
+            self.room.update((seat, self.limit - lens[seat]) for seat in due)
+            full = [seat for seat in due if self.room[seat] == 0]
+            if full:
+                self.asks[full] = 0
+            for seat in full:
+                del self.room[seat]
+        for seat in self.room:
+            self.room[seat] -= 1
+
     def _capture(self) -> None:
         """Capture the step.  The run outside the capture that this needs is
         made with nobody asking for a token, which changes nothing."""
-        x, limits = self.x.clone(), self.limits.clone()
-        self.limits.zero_()
+        x, asks = self.x.clone(), self.asks.clone()
+        self.asks.zero_()
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
@@ -297,7 +318,7 @@ class PooledSession:
         with torch.cuda.graph(self.graph):
             self._step()
         self.x.copy_(x)
-        self.limits.copy_(limits)
+        self.asks.copy_(asks)
 
 
 def serve(a) -> None:

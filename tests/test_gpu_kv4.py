@@ -803,3 +803,30 @@ def test_attend_smallest_scales(kv4, keys, values, q_size):
         assert np.any(np.abs(other - want) > 2 * (tol + 2.0 ** -8 * np.abs(want) + 2.0 ** -134)) or \
             np.any(np.abs(other_lse - lse) > 2 * tol_lse)
     cache.check()
+
+
+@pytest.mark.parametrize("graph", [True, False])
+def test_pooled_session_waits_just_below_the_limit(kv4, graph):
+    """Steps without a token do not count towards the limit, and one that waited for
+    its page gets there."""
+    from cross_core_barrier_amd.kv8_decode import PooledSession
+    _say(f"pooled session: a token that waits below the limit, graph={graph}")
+    s = PooledSession(batch=2, heads=1, q_heads=2, head_dim=64, page_size=16, limit=36, pages=4, seed=4)
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    rows = torch.randn((36, 128), generator=gen, device="cuda").to(s.x.dtype)
+    assert s.sit([0, 1], [rows[:30], rows[:20]]) == [0, 1]
+    for _ in range(2 + 13):
+        s.step(graph)  # to the end of their second pages; seat 0 could be at the limit by its steps
+    assert s.cache.lens.tolist() == [32, 32]
+    s.leave([1])
+    for n in (33, 34, 35, 36, 36, 36):
+        s.step(graph)
+        assert s.cache.lens.tolist() == [n, 0]
+    s.leave([0])
+    assert s.sit([1, 0], [rows[:35], rows[:1]]) == [0, 1]
+    for n in (36, 36):
+        s.step(graph)
+        assert s.cache.lens.tolist()[1] == n
+    assert s.cache.lens.tolist() == [3, 36]
+    s.cache.check()
+    s.pool.check()
