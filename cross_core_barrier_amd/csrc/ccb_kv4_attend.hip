@@ -28,9 +28,11 @@
 // What bounds it.  A tile of 32 tokens (D = 128) costs a wave about 250
 // instructions for 4352 bytes, which a workgroup of 8 waves gets through in 1.1
 // us: large even calls are bound by memory (64 sequences of 16384 tokens: 1.13 GB
-// in 198 us, 5.7 TB/s), a long sequence on its own workgroup by the issue of
-// instructions (30 GB/s a CU), and short calls by the start (about 6 us: launch,
-// length -> page -> codes, the join of the waves).  Taking two tiles ahead, 16
+// in 197 us, 5.7 TB/s), a long sequence on its own workgroup by a tile's chain of
+// work in two waves a SIMD (30 GB/s a CU; vector instructions take 45% of a busy
+// SIMD's cycles, matrix products 19%, and the waves wait for 40% of their time), and
+// short calls by the start (about 6 us: launch, length -> page -> codes, the join of
+// the waves).  Taking two tiles ahead, 16
 // waves a workgroup, the next tile's scores beside this one's weights, or all
 // transposed reads at once changed little or cost (24.5 us against 26.2, 23.5,
 // 26.6 and 25.0; 16 waves take 19.6 us against 14.6 for 200 short sequences).
@@ -187,8 +189,9 @@ struct Place {
 // The sequence that run u belongs to, or (u < 0) sequence b itself.  A run's
 // length, for all sequences, is the least with which there are no more than
 // p.runs runs (of up to 64 sequences; of more, one that is enough for that), so
-// that a long sequence has many workgroups and a short one few.  The host knows
-// only the capacity, which may be many times what a sequence holds.
+// that a long sequence has many workgroups and a short one few, as far as make_plan
+// has left more runs than sequences.  The host knows only the capacity, which may be
+// many times what a sequence holds.
 __device__ __forceinline__ Place place_of(const Plan& p, int32_t u, int32_t b)
 {
     const int lane = threadIdx.x & 63;
@@ -825,7 +828,11 @@ size_t make_plan(Plan& p, const ccbKv4Cache& c, int32_t headsQ, int32_t nQuery, 
     // brings no bandwidth, pays its start once more and makes more to join (16
     // sequences of 4096 tokens 20.4 us, with 384 or 512 workgroups 23.7 and 21.5;
     // 8 of 1500 to 16384, D = 256, 26.3 and 41).  More where a run could pass 2 MB
-    // of codes: many short sequences do not wait for a long one's end.
+    // of codes: many short sequences do not wait for a long one's end.  Measured on
+    // lengths that spread evenly, and right for those.  One long sequence among as many
+    // short ones as there are CUs for stays whole, whatever the lengths are: of 8 heads, D
+    // = 128, one sequence of 16384 tokens among 200 each, 28 take 24.2 us, 31 45.4 and
+    // 32 72 (32 of 2098 each, three times the tokens, 15.4).
     constexpr int64_t target = 256, limit = 16 * target;
     const int64_t longest = (1 << 21) / c.headDim;
     // A sequence of so many units stays whole: a join costs 3 us, a unit 1.1 at D =

@@ -7,8 +7,10 @@
 // share of the tokens or pages, and finds their sequences by bisection in LDS.
 // What the call changes of its own inputs (lens, count) is written by the
 // workgroup that ends last, when all others have read them: it is the one that
-// finds the counters of `state` full, and leaves them at 0.  Small calls are one
-// workgroup.
+// finds the counters of `state` full, and leaves them at 0.  A grow's grid goes by the
+// room for tokens (up to 2048 are one workgroup), a trim's by the table's capacity, since
+// the host knows no lengths: 64 sequences of up to 126 pages are 4 workgroups, and a
+// wide table starts up to 512 to take back a few pages.
 //
 // What bounds it: latency.  A step of 64 sequences takes 3.6 us (trim) and 6.4
 // (grow), of which 2.5 is the start and the rest a chain of loads: lengths, two

@@ -28,7 +28,9 @@
  *
  * Contents past lens[b], and pages that no sequence uses, may hold any bytes
  * and reach no result.  Within a sequence no scale is 255 (NaN);
- * ccb_kv4_append writes 63 to 252.
+ * ccb_kv4_append writes 63 to 252.  Values of 2^128 and more, which only scales of
+ * 253 and 254 make, are infinite: within a sequence no value is one for
+ * ccb_kv4_attend (it would reach queries that do not see it, as a NaN).
  */
 #ifndef CCB_KV4_H
 #define CCB_KV4_H
@@ -86,7 +88,8 @@ CCB_API ccbStatus ccb_kv4_append(const ccbKv4Cache* cache, const ccbKv8Rows* kNe
  * once to its type.  Weights are relative to a maximum that later scores may
  * have passed by a factor of 2^8: where that and the number of tokens take the
  * values past 2^128 (|v| >= 2^90 at the most tokens there can be) a sum may be
- * infinite.  Results do not depend on timing: the same call gives the same bits.
+ * infinite.  Scores beyond the largest float are infinite: +infinity makes its
+ * query's results NaN, and -infinity counts as unseen.  Results do not depend on timing: the same call gives the same bits.
  *   q, out  [batch][nQuery][headsQ][headDim], of one type.  out may be q itself
  *           (the same data and strides) and overlaps it in no other way.
  *   lse     device float [batch][nQuery][headsQ], or NULL
